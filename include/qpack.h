@@ -84,6 +84,10 @@ typedef QP_ENUM(qp_dtype) { QP_F32 = 0, QP_F16 = 1, QP_BF16 = 2 } qp_dtype;
  * (0x7F / 0xFF are +-480). Lanes are packed as in the affine mode. */
 typedef QP_ENUM(qp_mode) { QP_MXFP4 = 1, QP_MXFP8 = 2, QP_NVFP4 = 3 } qp_mode;
 
+/* Activation of the gated feed-forward block: SiLU(z) = z / (1 + exp(-z)), or
+ * GELU in its tanh form, z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2. */
+typedef QP_ENUM(qp_act) { QP_SILU = 0, QP_GELU_TANH = 1 } qp_act;
+
 /*
  * Affine group quantization (ollama quantize.go `loadAndQuantizeArray`,
  * emily `QuantizedWeight.from_dense/2`), computed on the device.
@@ -363,6 +367,139 @@ qp_status qgemv_moe_ffn(const void* a, qp_dtype a_dtype, const int32_t* ids,
                         qp_dtype sb_dtype, int64_t num_experts, int64_t d_model, int64_t d_ff,
                         int32_t bits, int32_t group_size, void* out, void* workspace,
                         size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Dense gated feed-forward block over packed weights (the block of
+ * qgemv_moe_ffn with one set of weights for every row):
+ *   g = x Wg^T,  u = x Wu^T,  h = act(g) * u,  y = h Wd^T
+ *   x        device, x_dtype [m, d_model]
+ *   gate_*, up_*  device, weights [d_ff, d_model] as in qmatmul
+ *   down_*   device, weight [d_model, d_ff]
+ *   saved    device, x_dtype [2, m, d_ff] (output): g, then u, for
+ *            qffn_backward; or null where no gradient is wanted
+ *   y        device, x_dtype [m, d_model] (output)
+ *   workspace device, >= qffn_workspace_bytes(m, d_model, d_ff, dtype), 16-byte aligned
+ * d_model and d_ff must be multiples of group_size; sb_dtype must equal
+ * x_dtype. fp32 accumulation; h (and g and u where they are kept) is rounded
+ * to x_dtype between the products. m == 0 is a no-op; d_ff == 0 writes zeros.
+ */
+size_t qffn_workspace_bytes(int64_t m, int64_t d_model, int64_t d_ff, qp_dtype dtype);
+qp_status qffn(const void* x, qp_dtype x_dtype, int64_t m, int64_t d_model, int64_t d_ff,
+               const uint32_t* gate_wq, const void* gate_scales, const void* gate_biases,
+               const uint32_t* up_wq, const void* up_scales, const void* up_biases,
+               const uint32_t* down_wq, const void* down_scales, const void* down_biases,
+               qp_dtype sb_dtype, int32_t bits, int32_t group_size, qp_act act, void* saved,
+               void* y, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of qffn. The codes are integers and are not trained; each
+ * group's scale and bias is, with dW the gradient of the dense weight:
+ *   dscales[n, G] = sum_{k in G} q[n, k] dW[n, k],  dbiases[n, G] = sum_{k in G} dW[n, k]
+ *   dh = dy Wd,  dg = dh * u * act'(g),  du = dh * act(g),  dx = dg Wg + du Wu,
+ *   dWg = dg^T x,  dWu = du^T x,  dWd = dy^T (act(g) * u)
+ *   dy       device, x_dtype [m, d_model]
+ *   saved    device, x_dtype [2, m, d_ff], as qffn wrote it
+ *   dx       device, x_dtype [m, d_model] (output), or null
+ *   dgate_*, dup_*  device, x_dtype [d_ff, d_model/group_size] (outputs); ddown_*
+ *            [d_model, d_ff/group_size]; a null pair is not computed (x is
+ *            read for the gate's and up's only)
+ *   workspace device, >= qffn_backward_workspace_bytes(...), 16-byte aligned
+ * fp32 accumulation; dg, du and h are rounded to x_dtype between the
+ * products. Deterministic. With m == 0 the weights' gradients are zeros.
+ */
+size_t qffn_backward_workspace_bytes(int64_t m, int64_t d_model, int64_t d_ff, int32_t bits,
+                                     int32_t group_size, qp_dtype dtype);
+qp_status qffn_backward(const void* x, const void* dy, const void* saved, qp_dtype x_dtype,
+                        int64_t m, int64_t d_model, int64_t d_ff, const uint32_t* gate_wq,
+                        const void* gate_scales, const void* gate_biases, const uint32_t* up_wq,
+                        const void* up_scales, const void* up_biases, const uint32_t* down_wq,
+                        const void* down_scales, const void* down_biases, qp_dtype sb_dtype,
+                        int32_t bits, int32_t group_size, qp_act act, void* dx,
+                        void* dgate_scales, void* dgate_biases, void* dup_scales,
+                        void* dup_biases, void* ddown_scales, void* ddown_biases,
+                        void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of qmatmul: dx = dy W, and the scales' and biases' gradients of
+ * dW = dy^T x as in qffn_backward.
+ *   x        device, x_dtype [m, k] (read for the weight's gradients only)
+ *   dy       device, x_dtype [m, n]
+ *   dx       device, x_dtype [m, k] (output), or null
+ *   dscales, dbiases  device, x_dtype [n, k/group_size] (outputs), or both null
+ *   workspace device, >= qmatmul_backward_workspace_bytes(...), 16-byte aligned
+ * fp32 accumulation, deterministic. n == 0 writes zeros to dx, m == 0 zeros to
+ * the weight's gradients.
+ */
+size_t qmatmul_backward_workspace_bytes(int64_t m, int64_t k, int64_t n, int32_t bits,
+                                        int32_t group_size, qp_dtype dtype);
+qp_status qmatmul_backward(const void* x, const void* dy, qp_dtype x_dtype, int64_t m, int64_t k,
+                           const uint32_t* wq, const void* scales, const void* biases,
+                           qp_dtype sb_dtype, int64_t n, int32_t bits, int32_t group_size,
+                           void* dx, void* dscales, void* dbiases, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Lookup in a packed embedding table, with a factor:
+ *   out[t, i] = factor * (q[v, i] * s'[v, i/gs] + b'[v, i/gs]),  v = ids[t]
+ *   ids      device, int32 [n_tokens]; an id outside [0, n_rows) gives a row of zeros
+ *   wq, scales, biases  device, the table [n_rows, k] as in qmatmul
+ *   out      device, sb_dtype [n_tokens, k] (output), rounded once from fp32
+ */
+qp_status qembedding(const int32_t* ids, int64_t n_tokens, const uint32_t* wq, const void* scales,
+                     const void* biases, qp_dtype sb_dtype, int64_t n_rows, int64_t k,
+                     int32_t bits, int32_t group_size, float factor, void* out,
+                     hipStream_t stream);
+
+/*
+ * Gradient of qembedding with respect to the table's scales and biases:
+ *   dscales[v, G] = factor * sum_{t: ids[t] = v} sum_{i in G} q[v, i] dout[t, i],
+ *   dbiases[v, G] = factor * sum_{t: ids[t] = v} sum_{i in G} dout[t, i]
+ *   dout     device, dtype [n_tokens, k]
+ *   dscales, dbiases  device, dtype [n_rows, k/group_size] (outputs, every
+ *            row written: zeros where no token asked for it)
+ *   workspace device, >= qembedding_backward_workspace_bytes(...), 16-byte aligned
+ * Tokens are sorted by id on the device and a row's tokens are summed in token
+ * order in fp32, rounded once: deterministic. Ids outside [0, n_rows) add nothing.
+ * n_tokens is at most 2^29.
+ */
+size_t qembedding_backward_workspace_bytes(int64_t n_tokens, int64_t k, int32_t bits,
+                                           int32_t group_size);
+qp_status qembedding_backward(const int32_t* ids, int64_t n_tokens, const void* dout,
+                              qp_dtype dtype, const uint32_t* wq, int64_t n_rows, int64_t k,
+                              int32_t bits, int32_t group_size, float factor, void* dscales,
+                              void* dbiases, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream);
+
+/*
+ * Controls on a batch of logit rows before sampling. Row b's tokens are
+ * history[history_offsets[b] .. history_offsets[b + 1]), the first
+ * prompt_lens[b] of them its prompt, the others made; c is how often token v
+ * was made. In fp32, rounded once to dtype:
+ *   v among the row's tokens:  z = z > 0 ? z / repetition[b] : z * repetition[b]
+ *   c > 0:                     z = z - frequency[b] * c - presence[b]
+ *   v among the row's biases:  z = z + bias (the last entry of v counts)
+ *   v not allowed by the mask: z = -infinity
+ *   logits   device, dtype [rows, vocab], rows in_stride elements apart
+ *   history  device, int32 [history_len]; history_offsets int32 [rows + 1];
+ *            prompt_lens int32 [rows], or null (every token was made)
+ *   repetition, frequency, presence  device, fp32 [rows], each or null (1, 0, 0)
+ *   bias_ids, bias_values  device, int32 / fp32 [bias_len], row b's entries from
+ *            bias_offsets[b] to bias_offsets[b + 1]; or null
+ *   mask     device, u32 words, bit v % 32 of word v / 32 set where v is
+ *            allowed, rows mask_stride words apart (0: one mask for all); or null
+ *   out      device, dtype [rows, vocab], rows out_stride elements apart
+ *            (output); it may be logits itself, with the same stride
+ * Tokens outside [0, vocab) are ignored, and offsets are held inside
+ * history_len and bias_len. A row whose mask allows nothing becomes -infinity
+ * throughout. Deterministic.
+ */
+qp_status qlogits_adjust(const void* logits, qp_dtype dtype, int64_t rows, int64_t vocab,
+                         int64_t in_stride, const int32_t* history, int64_t history_len,
+                         const int32_t* history_offsets, const int32_t* prompt_lens,
+                         const float* repetition, const float* frequency, const float* presence,
+                         const int32_t* bias_ids, const float* bias_values, int64_t bias_len,
+                         const int32_t* bias_offsets, const uint32_t* mask, int64_t mask_stride,
+                         void* out, int64_t out_stride, hipStream_t stream);
 
 #ifdef __cplusplus
 }

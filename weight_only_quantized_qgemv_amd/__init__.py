@@ -12,6 +12,10 @@ Calls (same names as the C ABI):
     qgemv_moe_id(a, ids, ..., wq, scales, biases, ...) -> out
     qgemv_moe_id_gate_up_silu(a, ids, ..., gate, up, ...) -> SiLU(gate) * up
     qgemv_moe_workspace_bytes(n_pairs, num_experts)
+    qffn(x, gate, up, down, bits, group_size)      -> dense gated block, qffn_backward its gradients
+    qmatmul_backward(x, dy, wq, scales, biases, ...) -> dx, dscales, dbiases
+    qembedding(ids, wq, scales, biases, ...)       -> rows of a packed table, qembedding_backward
+    qlogits_adjust(logits, ...)                    -> penalties, biases and masks on logits
 """
 from __future__ import annotations
 
@@ -32,7 +36,10 @@ EXPORTS = ("qpack_quantize", "qpack_dequantize", "qpack_dequantize_mx", "qmatmul
            "qgemv_moe_id_gate_up_silu",
            "qgemv_moe_ffn_workspace_bytes", "qgemv_moe_ffn", "qpack_quantize_int8_tensor",
            "qpack_dequantize_int8_tensor", "qmatmul_int8_tensor", "qmatmul_t_workspace_bytes",
-           "qmatmul_t", "qpack_last_error",
+           "qmatmul_t", "qffn_workspace_bytes", "qffn", "qffn_backward_workspace_bytes",
+           "qffn_backward", "qmatmul_backward_workspace_bytes", "qmatmul_backward", "qembedding",
+           "qembedding_backward_workspace_bytes", "qembedding_backward", "qlogits_adjust",
+           "qpack_last_error",
            "qpack_version")
 
 
@@ -94,6 +101,31 @@ def lib() -> ctypes.CDLL:
         L.qmatmul_t.argtypes = [P, ctypes.c_int, I64, I64, P, P, P, ctypes.c_int, I64, I32, I32, P,
                                 P, SZ, P]
         L.qmatmul_t.restype = ctypes.c_int
+        CI = ctypes.c_int
+        L.qffn_workspace_bytes.argtypes = [I64, I64, I64, CI]
+        L.qffn_workspace_bytes.restype = SZ
+        L.qffn.argtypes = [P, CI, I64, I64, I64] + [P] * 9 + [CI, I32, I32, CI, P, P, P, SZ, P]
+        L.qffn.restype = CI
+        L.qffn_backward_workspace_bytes.argtypes = [I64, I64, I64, I32, I32, CI]
+        L.qffn_backward_workspace_bytes.restype = SZ
+        L.qffn_backward.argtypes = ([P, P, P, CI, I64, I64, I64] + [P] * 9 + [CI, I32, I32, CI] +
+                                    [P] * 8 + [SZ, P])
+        L.qffn_backward.restype = CI
+        L.qmatmul_backward_workspace_bytes.argtypes = [I64, I64, I64, I32, I32, CI]
+        L.qmatmul_backward_workspace_bytes.restype = SZ
+        L.qmatmul_backward.argtypes = [P, P, CI, I64, I64, P, P, P, CI, I64, I32, I32, P, P, P, P,
+                                       SZ, P]
+        L.qmatmul_backward.restype = CI
+        L.qembedding.argtypes = [P, I64, P, P, P, CI, I64, I64, I32, I32, ctypes.c_float, P, P]
+        L.qembedding.restype = CI
+        L.qembedding_backward_workspace_bytes.argtypes = [I64, I64, I32, I32]
+        L.qembedding_backward_workspace_bytes.restype = SZ
+        L.qembedding_backward.argtypes = [P, I64, P, CI, P, I64, I64, I32, I32, ctypes.c_float, P,
+                                          P, P, SZ, P]
+        L.qembedding_backward.restype = CI
+        L.qlogits_adjust.argtypes = [P, CI, I64, I64, I64, P, I64, P, P, P, P, P, P, P, I64, P, P,
+                                     I64, P, I64, P]
+        L.qlogits_adjust.restype = CI
         L.qpack_last_error.restype = ctypes.c_char_p
         L.qpack_version.restype = ctypes.c_char_p
         _lib = L
@@ -417,4 +449,248 @@ def qmatmul_t(x, wq, scales, biases, bits: int, group_size: int, out=None, works
     check(lib().qmatmul_t(_ptr(x), dtype_code(x.dtype), m, k, _ptr(wq), _ptr(scales), _ptr(biases),
                           dtype_code(scales.dtype), n, bits, group_size, _ptr(out), _ptr(workspace),
                           workspace.numel(), _stream(x)))
+    return out
+
+
+# ------------------------------------------------------------------ the operators around the products
+
+ACTS = {"silu": 0, "gelu_tanh": 1}
+
+
+def _act_code(act: str) -> int:
+    code = ACTS.get(act)
+    if code is None:
+        raise ValueError(f"unknown activation {act!r} (one of {', '.join(ACTS)})")
+    return code
+
+
+def _like(t, like, name, shape=None, dtype=None):
+    """t is a contiguous tensor on like's device (of `shape`, of `dtype`); returns t."""
+    if not t.is_cuda or t.device != like.device:
+        raise ValueError(f"{name} must be a device tensor on {like.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    return t
+
+
+def _check_packed(w, like, name, n, k, bits, group_size):
+    """(wq, scales, biases) of a weight [n, k] beside `like`."""
+    import torch
+    wq, scales, biases = w
+    _like(wq, like, name + " codes", (n, k * bits // 32), torch.int32)
+    groups = (n, k // group_size if group_size > 0 else 0)
+    _like(scales, like, name + " scales", groups)
+    _like(biases, like, name + " biases", groups, scales.dtype)
+    return scales.dtype
+
+
+def _workspace(nbytes, like, workspace):
+    import torch
+    if workspace is None:
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=like.device)
+    return _like(workspace, like, "workspace")
+
+
+def _ws_bytes(workspace) -> int:
+    return workspace.numel() * workspace.element_size()
+
+
+def _check_ffn(x, gate, up, down, bits, group_size):
+    if x.dim() != 2:
+        raise ValueError("x must be a contiguous [m, d_model] tensor")
+    _like(x, x, "x")
+    m, d = x.shape
+    f = gate[0].shape[0]
+    dt = _check_packed(gate, x, "gate", f, d, bits, group_size)
+    for w, name, n, k in ((up, "up", f, d), (down, "down", d, f)):
+        if _check_packed(w, x, name, n, k, bits, group_size) != dt:
+            raise ValueError("gate, up and down must have scales of one dtype")
+    return m, d, f, dt
+
+
+def qffn_workspace_bytes(m: int, d_model: int, d_ff: int, dtype) -> int:
+    return int(lib().qffn_workspace_bytes(m, d_model, d_ff, dtype_code(dtype)))
+
+
+def qffn(x, gate, up, down, bits: int, group_size: int, act: str = "silu", saved=None, out=None,
+         workspace=None):
+    """y = (act(x Wg^T) * (x Wu^T)) Wd^T for x [m, d_model]; gate, up [d_ff, d_model] and down
+    [d_model, d_ff] are (wq, scales, biases) weights. `saved`, an empty [2, m, d_ff] tensor of x's
+    dtype, receives the two projections for qffn_backward. Returns y [m, d_model]."""
+    import torch
+    _dev(x, "x")
+    m, d, f, dt = _check_ffn(x, gate, up, down, bits, group_size)
+    if saved is not None:
+        _like(saved, x, "saved", (2, m, f), x.dtype)
+    if out is None:
+        out = torch.empty((m, d), dtype=x.dtype, device=x.device)
+    else:
+        _like(out, x, "out", (m, d), x.dtype)
+    workspace = _workspace(qffn_workspace_bytes(m, d, f, x.dtype), x, workspace)
+    check(lib().qffn(_ptr(x), dtype_code(x.dtype), m, d, f, *[_ptr(t) for w in (gate, up, down) for t in w],
+                     dtype_code(dt), bits, group_size, _act_code(act),
+                     None if saved is None else _ptr(saved), _ptr(out), _ptr(workspace),
+                     _ws_bytes(workspace), _stream(x)))
+    return out
+
+
+def qffn_backward_workspace_bytes(m: int, d_model: int, d_ff: int, bits: int, group_size: int,
+                                  dtype) -> int:
+    return int(lib().qffn_backward_workspace_bytes(m, d_model, d_ff, bits, group_size,
+                                                   dtype_code(dtype)))
+
+
+def qffn_backward(x, dy, saved, gate, up, down, bits: int, group_size: int, act: str = "silu",
+                  input_grad: bool = True, weight_grads: bool = True, workspace=None):
+    """Gradients of qffn at dy [m, d_model]: (dx, dgate, dup, ddown), each weight's a pair
+    (dscales, dbiases) in x's dtype. dx is None without input_grad, the pairs without
+    weight_grads (frozen weights)."""
+    import torch
+    _dev(x, "x")
+    m, d, f, dt = _check_ffn(x, gate, up, down, bits, group_size)
+    _like(dy, x, "dy", (m, d), x.dtype)
+    _like(saved, x, "saved", (2, m, f), x.dtype)
+    dx = torch.empty((m, d), dtype=x.dtype, device=x.device) if input_grad else None
+    pairs = [None] * 3
+    if weight_grads:
+        pairs = [tuple(torch.empty(w[1].shape, dtype=x.dtype, device=x.device) for _ in range(2))
+                 for w in (gate, up, down)]
+    workspace = _workspace(qffn_backward_workspace_bytes(m, d, f, bits, group_size, x.dtype), x,
+                           workspace)
+    check(lib().qffn_backward(
+        _ptr(x), _ptr(dy), _ptr(saved), dtype_code(x.dtype), m, d, f,
+        *[_ptr(t) for w in (gate, up, down) for t in w], dtype_code(dt), bits, group_size,
+        _act_code(act), None if dx is None else _ptr(dx),
+        *[None if p is None else _ptr(p[i]) for p in pairs for i in range(2)], _ptr(workspace),
+        _ws_bytes(workspace), _stream(x)))
+    return (dx, *pairs)
+
+
+def qmatmul_backward_workspace_bytes(m: int, k: int, n: int, bits: int, group_size: int,
+                                     dtype) -> int:
+    return int(lib().qmatmul_backward_workspace_bytes(m, k, n, bits, group_size, dtype_code(dtype)))
+
+
+def qmatmul_backward(x, dy, wq, scales, biases, bits: int, group_size: int,
+                     input_grad: bool = True, weight_grads: bool = True, workspace=None):
+    """Gradients of y = x @ dequant(W)^T at dy [m, n]: (dx, dscales, dbiases) in x's dtype, each
+    None where it is not asked for."""
+    import torch
+    _dev(x, "x")
+    if x.dim() != 2 or not x.is_contiguous():
+        raise ValueError("x must be a contiguous [m, k] tensor")
+    m, k = x.shape
+    n = wq.shape[0]
+    dt = _check_packed((wq, scales, biases), x, "weight", n, k, bits, group_size)
+    _like(dy, x, "dy", (m, n), x.dtype)
+    dx = torch.empty((m, k), dtype=x.dtype, device=x.device) if input_grad else None
+    ds = db = None
+    if weight_grads:
+        ds, db = (torch.empty(scales.shape, dtype=x.dtype, device=x.device) for _ in range(2))
+    workspace = _workspace(qmatmul_backward_workspace_bytes(m, k, n, bits, group_size, x.dtype), x,
+                           workspace)
+    check(lib().qmatmul_backward(
+        _ptr(x), _ptr(dy), dtype_code(x.dtype), m, k, _ptr(wq), _ptr(scales), _ptr(biases),
+        dtype_code(dt), n, bits, group_size, *[None if t is None else _ptr(t) for t in (dx, ds, db)],
+        _ptr(workspace), _ws_bytes(workspace), _stream(x)))
+    return dx, ds, db
+
+
+def qembedding(ids, wq, scales, biases, bits: int, group_size: int, factor: float = 1.0, out=None):
+    """Rows ids (int32, any shape) of the packed table [n_rows, k], times factor, in the scales'
+    dtype: [*ids.shape, k]. An id outside the table gives zeros."""
+    import torch
+    _like(ids, ids, "ids", None, torch.int32)
+    k = wq.shape[1] * 32 // bits if bits else 0
+    dt = _check_packed((wq, scales, biases), ids, "table", wq.shape[0], k, bits, group_size)
+    shape = (*ids.shape, k)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=ids.device)
+    else:
+        _like(out, ids, "out", shape, dt)
+    check(lib().qembedding(_ptr(ids), ids.numel(), _ptr(wq), _ptr(scales), _ptr(biases),
+                           dtype_code(dt), wq.shape[0], k, bits, group_size, factor, _ptr(out),
+                           _stream(ids)))
+    return out
+
+
+def qembedding_backward_workspace_bytes(n_tokens: int, k: int, bits: int, group_size: int) -> int:
+    return int(lib().qembedding_backward_workspace_bytes(n_tokens, k, bits, group_size))
+
+
+def qembedding_backward(ids, dout, wq, bits: int, group_size: int, factor: float = 1.0,
+                        workspace=None):
+    """Gradients (dscales, dbiases) [n_rows, k / group_size] of the table of qembedding at dout
+    [*ids.shape, k], in dout's dtype."""
+    import torch
+    _like(ids, ids, "ids", None, torch.int32)
+    k = wq.shape[1] * 32 // bits if bits else 0
+    _like(wq, ids, "table codes", None, torch.int32)
+    _like(dout, ids, "dout", (*ids.shape, k))
+    t, n = ids.numel(), wq.shape[0]
+    ds, db = (torch.empty((n, k // group_size if group_size > 0 else 0), dtype=dout.dtype,
+                          device=ids.device) for _ in range(2))
+    workspace = _workspace(qembedding_backward_workspace_bytes(t, k, bits, group_size), ids, workspace)
+    check(lib().qembedding_backward(_ptr(ids), t, _ptr(dout), dtype_code(dout.dtype), _ptr(wq), n, k,
+                                    bits, group_size, factor, _ptr(ds), _ptr(db), _ptr(workspace),
+                                    _ws_bytes(workspace), _stream(ids)))
+    return ds, db
+
+
+def qlogits_adjust(logits, history=None, offsets=None, prompt_lens=None, repetition=None,
+                   frequency=None, presence=None, bias=None, mask=None, out=None):
+    """Penalties, biases and a mask on logits [rows, vocab] (rows may be strided).
+
+    history int32 [h] holds every row's tokens, row b's from offsets[b] to offsets[b + 1] (int32
+    [rows + 1]), the first prompt_lens[b] (int32 [rows]) of them its prompt; repetition, frequency
+    and presence are fp32 [rows]; bias is (ids int32, values fp32, offsets int32 [rows + 1]); mask
+    is int32 words [rows or 1, ceil(vocab / 32)], a set bit where the token is allowed. Returns the
+    adjusted logits in their dtype; out=logits works in place."""
+    import torch
+    if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a device tensor [rows, vocab], its last axis contiguous")
+    rows, vocab = logits.shape
+    if out is None:
+        out = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+    elif (tuple(out.shape) != (rows, vocab) or out.dtype != logits.dtype
+          or out.device != logits.device or (vocab > 1 and out.stride(1) != 1)):
+        raise ValueError("out must be like logits, its last axis contiguous")
+    i32, f32 = torch.int32, torch.float32
+    if history is not None:
+        _like(history, logits, "history", (history.numel(),), i32)
+        if offsets is None:
+            raise ValueError("history needs its rows' offsets")
+    if offsets is not None:
+        _like(offsets, logits, "offsets", (rows + 1,), i32)
+    for t, name, dt in ((prompt_lens, "prompt_lens", i32), (repetition, "repetition", f32),
+                        (frequency, "frequency", f32), (presence, "presence", f32)):
+        if t is not None:
+            _like(t, logits, name, (rows,), dt)
+    bids = bvals = boff = None
+    if bias is not None:
+        bids, bvals, boff = bias
+        _like(bids, logits, "bias ids", (bids.numel(),), i32)
+        _like(bvals, logits, "bias values", bids.shape, f32)
+        _like(boff, logits, "bias offsets", (rows + 1,), i32)
+    mask_stride = 0
+    if mask is not None:
+        if mask.dim() != 2 or mask.shape[0] not in (1, rows):
+            raise ValueError("mask must be [rows or 1, words]")
+        _like(mask, logits, "mask", None, i32)
+        if mask.shape[1] < (vocab + 31) // 32:
+            raise ValueError(f"mask must have {(vocab + 31) // 32} words a row")
+        mask_stride = mask.shape[1] if mask.shape[0] == rows and rows > 1 else 0
+
+    def ptr(t):
+        return None if t is None else t.data_ptr()
+
+    check(lib().qlogits_adjust(
+        ptr(logits), dtype_code(logits.dtype), rows, vocab, logits.stride(0), ptr(history),
+        0 if history is None else history.numel(), ptr(offsets), ptr(prompt_lens), ptr(repetition),
+        ptr(frequency), ptr(presence), ptr(bids), ptr(bvals), 0 if bids is None else bids.numel(),
+        ptr(boff), ptr(mask), mask_stride, ptr(out), out.stride(0), _stream(logits)))
     return out

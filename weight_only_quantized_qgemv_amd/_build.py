@@ -24,8 +24,11 @@ UNITS = ([("api.cpp", "api", {}), ("quantize.hip", "quantize", {}), ("moe.hip", 
           ("qgemm.hip", "qgemm", {}),
           ("dequantize.hip", "dequantize", {}), ("mx_gemv.hip", "mx_gemv", {}),
           ("moe_ffn.hip", "moe_ffn", {}), ("int8_tensor.hip", "int8_tensor", {}),
-          ("qgemv_t.hip", "qgemv_t", {})]
+          ("qgemv_t.hip", "qgemv_t", {}), ("api_model.cpp", "api_model", {}),
+          ("ffn.hip", "ffn", {}), ("grad.hip", "grad", {}), ("embedding.hip", "embedding", {}),
+          ("logits.hip", "logits", {})]
          + [("qgemv.hip", f"qgemv_b{b}", {"QP_BITS": b}) for b in BITS]
+         + [(f"{f}.hip", f"{f}_b{b}", {"QP_BITS": b}) for f in ("xgrad", "wgrad") for b in BITS]
          + [("moe_compute.hip", f"moe_b{b}_n{n}", {"QP_BITS": b, "QP_NMAT": n})
             for b in BITS for n in (1, 2)])
 

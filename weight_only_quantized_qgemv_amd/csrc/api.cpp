@@ -19,11 +19,20 @@
 #include <string>
 
 #include "../../include/qpack.h"
+#include "api_checks.hpp"
 #include "launch.hpp"
 
 namespace {
 
 thread_local std::string g_last_error;
+
+bool bits_ok(int32_t b) { return b == 2 || b == 3 || b == 4 || b == 6 || b == 8; }
+bool gs_ok(int32_t g) { return g == 32 || g == 64 || g == 128; }
+
+} // namespace
+
+namespace qp {
+namespace api {
 
 qp_status fail(qp_status s, const char* fmt, ...)
 {
@@ -49,15 +58,6 @@ qp_status hip_result(hipError_t e, const char* what)
     return ok();
 }
 
-bool bits_ok(int32_t b) { return b == 2 || b == 3 || b == 4 || b == 6 || b == 8; }
-bool gs_ok(int32_t g) { return g == 32 || g == 64 || g == 128; }
-bool dtype_ok(int d) { return d == QP_F32 || d == QP_F16 || d == QP_BF16; }
-size_t esize(int d) { return d == QP_F32 ? 4 : 2; }
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// a * b without int64 overflow (both non-negative).
-bool mul_ok(int64_t a, int64_t b) { return a == 0 || b <= INT64_MAX / a; }
-
 // Checks shared by every call: bits, group size, K divisibility.
 qp_status check_layout(int64_t k, int32_t bits, int32_t gs)
 {
@@ -72,7 +72,10 @@ qp_status check_layout(int64_t k, int32_t bits, int32_t gs)
     return QP_OK;
 }
 
-} // namespace
+} // namespace api
+} // namespace qp
+
+using namespace qp::api;
 
 extern "C" {
 

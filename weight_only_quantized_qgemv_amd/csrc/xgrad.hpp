@@ -1,0 +1,158 @@
+// xgrad.hpp — the input gradient of a quantized linear layer y = x W^T:
+//   dx[m, k] = sum_n dy[m, n] w[n, k],   w = q s' + b',
+// summed over one or two (dy, W) pairs (the gate and up projections of a
+// gated block share their input), and the close that the gated block's down
+// projection needs, where the product is dh and
+//   h = act(g) u,  dg = dh u act'(g),  du = dh act(g)
+// are written in its place.
+#pragma once
+
+#include "act.hpp"
+#include "codes8.hpp"
+#include "common.hpp"
+#include "model_ops.hpp"
+
+namespace qp {
+
+template <int DT>
+__device__ __forceinline__ float load_elem(const void* p, int64_t i)
+{
+    return Elem<DT>::to_f32(static_cast<const typename Elem<DT>::storage*>(p)[i]);
+}
+template <int DT>
+__device__ __forceinline__ void store_elem(void* p, int64_t i, float v)
+{
+    static_cast<typename Elem<DT>::storage*>(p)[i] = Elem<DT>::from_f32(v);
+}
+
+// The result v of element i = m K + k: stored, or closed as above.
+template <int DT>
+__device__ __forceinline__ void xgrad_store(const XgradArgs& a, int64_t i, float v)
+{
+    if (a.g == nullptr) {
+        store_elem<DT>(a.out, i, v);
+        return;
+    }
+    const float u = load_elem<DT>(a.u, i);
+    float act, dact;
+    act_grad_f32(a.act, load_elem<DT>(a.g, i), act, dact);
+    store_elem<DT>(a.dg, i, v * u * dact);
+    store_elem<DT>(a.du, i, v * act);
+    if (a.h != nullptr)
+        store_elem<DT>(a.h, i, act * u);
+}
+
+// Sums the splits' partial sums in split order and closes.
+template <int DT>
+__global__ __launch_bounds__(256) void xgrad_finish_kernel(XgradArgs a, int splits)
+{
+    const int64_t total = a.M * a.K;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        float v = 0.0f;
+        for (int s = 0; s < splits; ++s)
+            v += a.partial[(int64_t)s * total + i];
+        xgrad_store<DT>(a, i, v);
+    }
+}
+
+// Any type, size and alignment: fp32 products on the 32x32x2 matrix
+// instruction. A block of four waves computes 128 x 128 outputs, 32 n a step:
+// dy goes to LDS as fp32 transposed, the weights dequantized, each thread two
+// octets of codes.
+constexpr int XG_BM = 128, XG_BK = 128, XG_N = 32;
+
+template <int BITS, int DT>
+__global__ __launch_bounds__(256) void xgrad_f32_kernel(XgradArgs a, GradPlan plan)
+{
+    using C8 = Codes8<BITS>;
+    __shared__ float as[XG_N][XG_BM + 1];
+    __shared__ __attribute__((aligned(16))) float bs[XG_N][XG_BK];
+    const int tid = (int)threadIdx.x, lane = tid & 63, half = lane >> 5, c32 = lane & 31;
+    const int wm = (tid >> 6) >> 1, wk = (tid >> 6) & 1;
+    const int64_t tiles_k = (a.K + XG_BK - 1) / XG_BK;
+    const int64_t m0 = ((int64_t)blockIdx.x / tiles_k) * XG_BM, k0 = ((int64_t)blockIdx.x % tiles_k) * XG_BK;
+    const int64_t row_words = a.K * BITS / 32, groups = a.K / a.gs;
+    const int64_t steps = (a.N + XG_N - 1) / XG_N;       // of one pair
+    const int64_t lo = (int64_t)blockIdx.y * plan.per_split;
+    int64_t hi = lo + plan.per_split;
+    hi = hi < steps * a.nmat ? hi : steps * a.nmat;
+
+    f32x16_t acc[2][2] = {};
+    float ra[16], rb[2][8];
+    auto fetch = [&](int64_t step) {
+        const int p = step >= steps;
+        const int64_t n0 = (step - (p ? steps : 0)) * XG_N;
+        const int64_t n = n0 + (tid & 31);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int64_t m = m0 + (tid >> 5) + 8 * i;
+            ra[i] = (m < a.M && n < a.N) ? load_elem<DT>(a.dy[p], m * a.dy_stride + n) : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int e = tid + 256 * j;
+            const int64_t r = n0 + (e >> 4), k = k0 + 8 * (e & 15);
+            if (r < a.N && k < a.K) {
+                codes8_at<BITS>(a.w[p].wq + r * row_words, (int)(k >> 3), rb[j]);
+                const int64_t gi = r * groups + k / a.gs;
+                const float s = load_elem<DT>(a.w[p].scales, gi), b = load_elem<DT>(a.w[p].biases, gi);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    rb[j][i] = __builtin_fmaf(rb[j][i], s, b);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    rb[j][i] = 0.0f;
+            }
+        }
+    };
+    if (lo < hi)
+        fetch(lo);
+    for (int64_t step = lo; step < hi; ++step) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            as[tid & 31][(tid >> 5) + 8 * i] = ra[i];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int e = tid + 256 * j;
+            f32x4_t* d = reinterpret_cast<f32x4_t*>(&bs[e >> 4][8 * (e & 15)]);
+            d[0] = f32x4_t{rb[j][0], rb[j][1], rb[j][2], rb[j][3]};
+            d[1] = f32x4_t{rb[j][4], rb[j][5], rb[j][6], rb[j][7]};
+        }
+        __syncthreads();
+        if (step + 1 < hi)
+            fetch(step + 1);
+#pragma unroll
+        for (int kk = 0; kk < XG_N / 2; ++kk) {
+            float fa[2], fb[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                fa[i] = as[2 * kk + half][wm * 64 + 32 * i + c32];
+                fb[i] = bs[2 * kk + half][wk * 64 + 32 * i + c32];
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[i], fb[j], acc[i][j], 0, 0, 0);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int64_t m = m0 + wm * 64 + 32 * i + 8 * (r >> 2) + 4 * half + (r & 3);
+                const int64_t k = k0 + wk * 64 + 32 * j + c32;
+                if (m < a.M && k < a.K) {
+                    if (plan.splits > 1)
+                        a.partial[((int64_t)blockIdx.y * a.M + m) * a.K + k] = acc[i][j][r];
+                    else
+                        xgrad_store<DT>(a, m * a.K + k, acc[i][j][r]);
+                }
+            }
+}
+
+} // namespace qp
