@@ -140,7 +140,7 @@ size_t qffn_backward_workspace_bytes(int64_t m, int64_t d_model, int64_t d_ff, i
 {
     if (check_ffn("qffn_backward", dtype, dtype, m, d_model, d_ff, bits, group_size, QP_SILU) != QP_OK)
         return 0;
-    return qp::ffn_grad_workspace_bytes(m, d_model, d_ff, bits, group_size, (int)dtype);
+    return qp::ffn_grad_workspace_bytes(m, d_model, d_ff, group_size, (int)dtype);
 }
 
 qp_status qffn_backward(const void* x, const void* dy, const void* saved, qp_dtype x_dtype, int64_t m,
@@ -181,7 +181,7 @@ qp_status qffn_backward(const void* x, const void* dy, const void* saved, qp_dty
         if (qp_status s = check_weight(what, "down", down_wq, down_scales, down_biases, es); s != QP_OK)
             return s;
         if (qp_status s = check_workspace(what, workspace, workspace_bytes,
-                                          qp::ffn_grad_workspace_bytes(m, d_model, d_ff, bits, group_size,
+                                          qp::ffn_grad_workspace_bytes(m, d_model, d_ff, group_size,
                                                                        (int)x_dtype)); s != QP_OK)
             return s;
     }
@@ -223,7 +223,7 @@ size_t qmatmul_backward_workspace_bytes(int64_t m, int64_t k, int64_t n, int32_t
 {
     if (check_linear("qmatmul_backward", dtype, dtype, m, k, n, bits, group_size) != QP_OK)
         return 0;
-    return qp::linear_grad_workspace_bytes(m, k, n, bits, group_size, (int)dtype);
+    return qp::linear_grad_workspace_bytes(m, k, n, group_size, (int)dtype);
 }
 
 qp_status qmatmul_backward(const void* x, const void* dy, qp_dtype x_dtype, int64_t m, int64_t k,
@@ -250,7 +250,7 @@ qp_status qmatmul_backward(const void* x, const void* dy, qp_dtype x_dtype, int6
         if (qp_status s = check_weight(what, "the", wq, scales, biases, es); s != QP_OK)
             return s;
         if (qp_status s = check_workspace(what, workspace, workspace_bytes,
-                                          qp::linear_grad_workspace_bytes(m, k, n, bits, group_size,
+                                          qp::linear_grad_workspace_bytes(m, k, n, group_size,
                                                                           (int)x_dtype)); s != QP_OK)
             return s;
     }

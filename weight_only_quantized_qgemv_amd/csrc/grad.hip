@@ -41,6 +41,45 @@ hipError_t wgrad(const WgradArgs& a, const GradPlan& p, hipStream_t st)
     return hipErrorInvalidValue;
 }
 
+inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+int64_t up8(int64_t n) { return (n + 7) & ~(int64_t)7; }
+
+// Whether the tile kernels' 32-bit offsets reach a tile's rows: rows of at
+// most 2^20 elements.
+bool tile_sizes(int64_t n, int64_t k, int dt) { return dt != DT_F32 && n <= (1 << 20) && k <= (1 << 20); }
+
+// The tile kernel rounds each weight to the activations' type. Over fewer than
+// 64 rows (one step, the shortest contraction of the forward tiles too) those
+// roundings, up to 2^-8 of a bfloat16 weight, do not average out: the fp32
+// kernel takes such a product.
+bool averages(int64_t n) { return n >= 64; }
+
+// The larger of the two kernels' partial sums: which one runs depends on the
+// pointers too.
+size_t xgrad_bytes(int64_t m, int64_t n, int64_t k, int nmat)
+{
+    return std::max(xgrad_plan(m, n, k, nmat, false).partial_bytes, xgrad_plan(m, n, k, nmat, true).partial_bytes);
+}
+size_t wgrad_bytes(int64_t m, int64_t n, int64_t k, int nmat, int gs)
+{
+    return std::max(wgrad_plan(m, n, k, nmat, gs, false).partial_bytes, wgrad_plan(m, n, k, nmat, gs, true).partial_bytes);
+}
+
+// Rows of n 16-bit elements copied to rows of up8(n), zeros between.
+__global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restrict__ in, int64_t m, int64_t n,
+                                                       int64_t n8, uint16_t* __restrict__ out)
+{
+    const int64_t octets = m * (n8 / 8);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < octets; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / (n8 / 8), c = 8 * (i - r * (n8 / 8));
+        uint32_t v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = c + j < n ? in[r * n + c + j] : 0u;
+        reinterpret_cast<u32x4_t*>(out)[i] = u32x4_t{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
+    }
+}
+
 // Zeros for a weight's gradients (no rows to sum over).
 hipError_t zero_grads(void* ds, void* db, int dt, int64_t count, hipStream_t st)
 {
@@ -53,64 +92,79 @@ hipError_t zero_grads(void* ds, void* db, int dt, int64_t count, hipStream_t st)
 
 } // namespace
 
-size_t linear_grad_workspace_bytes(int64_t m, int64_t k, int64_t n, int bits, int gs, int dt)
+// The partial sums of one product at a time, then (16-bit rows that are not
+// whole 16-byte pieces) dy in padded rows.
+size_t linear_grad_workspace_bytes(int64_t m, int64_t k, int64_t n, int gs, int dt)
 {
     if (m == 0 || k == 0 || n == 0)
         return 0;
-    return std::max(xgrad_plan(m, n, k, 1, bits, dt).partial_bytes,
-                    wgrad_plan(m, n, k, 1, bits, gs, dt).partial_bytes);
+    const size_t pad = dt != DT_F32 && n % 8 != 0 ? (size_t)m * (size_t)up8(n) * 2 : 0;
+    return up16(std::max(xgrad_bytes(m, n, k, 1), wgrad_bytes(m, n, k, 1, gs))) + pad;
 }
 
 hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t st)
 {
-    if (a.dx != nullptr && a.M * a.K > 0) {
-        if (a.N == 0) {
-            if (hipError_t e = launch_fill_zero(a.dx, a.dt, a.M * a.K, st); e != hipSuccess)
+    const int64_t M = a.M, N = a.N, K = a.K;
+    if (M == 0 || N == 0 || K == 0) {
+        if (a.dx != nullptr && M * K > 0)
+            if (hipError_t e = launch_fill_zero(a.dx, a.dt, M * K, st); e != hipSuccess)
                 return e;
-        } else {
-            XgradArgs x{};
-            x.dy[0] = x.dy[1] = a.dy;
-            x.dy_stride = a.N;
-            x.w[0] = x.w[1] = a.w;
-            x.nmat = 1;
-            x.dt = a.dt;
-            x.M = a.M; x.N = a.N; x.K = a.K;
-            x.bits = a.bits; x.gs = a.gs;
-            x.out = a.dx;
-            x.partial = static_cast<float*>(a.workspace);
-            if (hipError_t e = xgrad(x, xgrad_plan(a.M, a.N, a.K, 1, a.bits, a.dt), st); e != hipSuccess)
-                return e;
-        }
+        return zero_grads(a.dscales, a.dbiases, a.dt, N * (K / a.gs), st);
     }
-    if (a.dscales == nullptr || a.N * a.K == 0)
+    const void* dy = a.dy;
+    int64_t stride = N;
+    bool tiles = tile_sizes(N, K, a.dt) && aligned16(a.x);
+    if (tiles && N % 8 != 0) {
+        uint16_t* const pad = reinterpret_cast<uint16_t*>(
+            static_cast<char*>(a.workspace) + up16(std::max(xgrad_bytes(M, N, K, 1), wgrad_bytes(M, N, K, 1, a.gs))));
+        stride = up8(N);
+        const unsigned blocks = (unsigned)std::min<int64_t>((M * (stride / 8) + 255) / 256, 16384);
+        hipLaunchKernelGGL(pad_rows_kernel, dim3(blocks), dim3(256), 0, st, static_cast<const uint16_t*>(a.dy), M, N,
+                           stride, pad);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess)
+            return e;
+        dy = pad;
+    }
+    tiles = tiles && aligned16(dy);
+    if (a.dx != nullptr) {
+        XgradArgs x{};
+        x.dy[0] = x.dy[1] = dy;
+        x.dy_stride = stride;
+        x.w[0] = x.w[1] = a.w;
+        x.nmat = 1;
+        x.dt = a.dt;
+        x.M = M; x.N = N; x.K = K;
+        x.bits = a.bits; x.gs = a.gs;
+        x.out = a.dx;
+        x.partial = static_cast<float*>(a.workspace);
+        if (hipError_t e = xgrad(x, xgrad_plan(M, N, K, 1, tiles && averages(N)), st); e != hipSuccess)
+            return e;
+    }
+    if (a.dscales == nullptr)
         return hipSuccess;
-    if (a.M == 0)
-        return zero_grads(a.dscales, a.dbiases, a.dt, a.N * (a.K / a.gs), st);
     WgradArgs w{};
     w.x = a.x;
-    w.dy[0] = w.dy[1] = a.dy;
-    w.dy_stride = a.N;
+    w.dy[0] = w.dy[1] = dy;
+    w.dy_stride = stride;
     w.wq[0] = w.wq[1] = a.w.wq;
     w.nmat = 1;
     w.dt = a.dt;
-    w.M = a.M; w.N = a.N; w.K = a.K;
+    w.M = M; w.N = N; w.K = K;
     w.bits = a.bits; w.gs = a.gs;
     w.dscales[0] = a.dscales;
     w.dbiases[0] = a.dbiases;
     w.partial = static_cast<float*>(a.workspace);
-    return wgrad(w, wgrad_plan(a.M, a.N, a.K, 1, a.bits, a.gs, a.dt), st);
+    return wgrad(w, wgrad_plan(M, N, K, 1, a.gs, tiles), st);
 }
 
 // dg, du and h, then the partial sums of one product at a time.
-size_t ffn_grad_workspace_bytes(int64_t m, int64_t d, int64_t f, int bits, int gs, int dt)
+size_t ffn_grad_workspace_bytes(int64_t m, int64_t d, int64_t f, int gs, int dt)
 {
     if (m == 0 || d == 0 || f == 0)
         return 0;
-    size_t part = xgrad_plan(m, d, f, 1, bits, dt).partial_bytes;
-    part = std::max(part, xgrad_plan(m, f, d, 2, bits, dt).partial_bytes);
-    part = std::max(part, wgrad_plan(m, f, d, 2, bits, gs, dt).partial_bytes);
-    part = std::max(part, wgrad_plan(m, f, d, 1, bits, gs, dt).partial_bytes);
-    part = std::max(part, wgrad_plan(m, d, f, 1, bits, gs, dt).partial_bytes);
+    size_t part = std::max(xgrad_bytes(m, d, f, 1), xgrad_bytes(m, f, d, 2));
+    part = std::max(part, std::max(wgrad_bytes(m, f, d, 2, gs), wgrad_bytes(m, f, d, 1, gs)));
+    part = std::max(part, wgrad_bytes(m, d, f, 1, gs));
     return 3 * up16((size_t)m * (size_t)f * elem_size(dt)) + part;
 }
 
@@ -134,6 +188,8 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t st)
     char* const h = du + step;
     float* const partial = reinterpret_cast<float*>(h + step);
 
+    const bool sizes = tile_sizes(D, F, a.dt), dy_tiles = sizes && aligned16(a.dy);
+
     XgradArgs x{};
     x.dt = a.dt; x.act = a.act; x.M = M; x.bits = a.bits; x.gs = a.gs;
     x.partial = partial;
@@ -146,7 +202,7 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t st)
     x.u = static_cast<const char*>(a.saved) + mf;
     x.dg = dg; x.du = du;
     x.h = a.ddown[0] != nullptr ? h : nullptr;
-    if (hipError_t e = xgrad(x, xgrad_plan(M, D, F, 1, a.bits, a.dt), st); e != hipSuccess)
+    if (hipError_t e = xgrad(x, xgrad_plan(M, D, F, 1, dy_tiles && averages(D)), st); e != hipSuccess)
         return e;
     if (a.dx != nullptr) {
         x.g = x.u = nullptr;
@@ -156,7 +212,7 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t st)
         x.nmat = 2;
         x.N = F; x.K = D;
         x.out = a.dx;
-        if (hipError_t e = xgrad(x, xgrad_plan(M, F, D, 2, a.bits, a.dt), st); e != hipSuccess)
+        if (hipError_t e = xgrad(x, xgrad_plan(M, F, D, 2, sizes && averages(F)), st); e != hipSuccess)
             return e;
     }
     WgradArgs w{};
@@ -178,7 +234,7 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t st)
     add(dg, a.gate, a.dgate);
     add(du, a.up, a.dup);
     if (w.nmat > 0)
-        if (hipError_t e = wgrad(w, wgrad_plan(M, F, D, w.nmat, a.bits, a.gs, a.dt), st); e != hipSuccess)
+        if (hipError_t e = wgrad(w, wgrad_plan(M, F, D, w.nmat, a.gs, sizes && aligned16(a.x)), st); e != hipSuccess)
             return e;
     if (a.ddown[0] == nullptr)
         return hipSuccess;
@@ -187,7 +243,7 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t st)
     w.dy_stride = D;
     w.nmat = 0;
     add(static_cast<const char*>(a.dy), a.down, a.ddown);
-    return wgrad(w, wgrad_plan(M, D, F, 1, a.bits, a.gs, a.dt), st);
+    return wgrad(w, wgrad_plan(M, D, F, 1, a.gs, dy_tiles), st);
 }
 
 } // namespace qp

@@ -88,16 +88,19 @@ struct WgradArgs {
     float* partial;         // fp32 partial sums of the splits (wgrad_plan)
 };
 
-// How a gradient product is cut: `tile` chooses the kernel's tile, `splits`
-// the pieces of the contraction, whose fp32 partial sums take partial_bytes.
+// How a gradient product is cut: `tile` chooses the kernel and its tile,
+// `splits` the pieces of the contraction (per_split steps of the kernel each),
+// whose fp32 partial sums take partial_bytes.
 struct GradPlan {
-    int tile;               // 0: the fp32 kernel for every shape; else see the kernel file
+    int tile;               // 0: the fp32 kernel for every shape; else see gradtile.hpp
     int splits;
-    int64_t per_split;      // contraction length of a piece
+    int64_t per_split;
     size_t partial_bytes;
 };
-GradPlan xgrad_plan(int64_t m, int64_t n, int64_t k, int nmat, int bits, int dt);
-GradPlan wgrad_plan(int64_t m, int64_t n, int64_t k, int nmat, int bits, int gs, int dt);
+// The plan for these sizes: `tiles` asks for the matrix-core tile kernels
+// (16-bit activations in rows of whole 16-byte pieces, 16-byte aligned).
+GradPlan xgrad_plan(int64_t m, int64_t n, int64_t k, int nmat, bool tiles);
+GradPlan wgrad_plan(int64_t m, int64_t n, int64_t k, int nmat, int gs, bool tiles);
 #define QP_GRAD_DECL(B)                                                                        \
     hipError_t launch_xgrad_b##B(const XgradArgs& a, const GradPlan& p, hipStream_t stream);   \
     hipError_t launch_wgrad_b##B(const WgradArgs& a, const GradPlan& p, hipStream_t stream);
@@ -118,7 +121,7 @@ struct LinearGradArgs {
     void *dscales, *dbiases;   // [N, K/gs] of dt, or both null
     void* workspace;        // >= linear_grad_workspace_bytes, 16-byte aligned
 };
-size_t linear_grad_workspace_bytes(int64_t m, int64_t k, int64_t n, int bits, int gs, int dt);
+size_t linear_grad_workspace_bytes(int64_t m, int64_t k, int64_t n, int gs, int dt);
 hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t stream);
 
 struct FfnGradArgs {
@@ -132,7 +135,7 @@ struct FfnGradArgs {
     void *dgate[2], *dup[2], *ddown[2];   // scales, biases; null pairs are not computed
     void* workspace;        // >= ffn_grad_workspace_bytes, 16-byte aligned
 };
-size_t ffn_grad_workspace_bytes(int64_t m, int64_t d, int64_t f, int bits, int gs, int dt);
+size_t ffn_grad_workspace_bytes(int64_t m, int64_t d, int64_t f, int gs, int dt);
 hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t stream);
 
 // ---- the packed embedding table (embedding.hip)

@@ -2,19 +2,45 @@
 // once per bit width (QP_BITS).
 #include <algorithm>
 
+#include "gradtile.hpp"
 #include "wgrad.hpp"
 
 namespace qp {
 
 namespace {
 
+template <int BITS, int DT, int BT>
+hipError_t run_tile(const WgradArgs& a, const GradPlan& p, hipStream_t st)
+{
+    constexpr int LDS = gradtile::wgrad_lds<BT, BT>();
+    static_assert(LDS <= 160 * 1024, "LDS budget");
+    const void* kern = reinterpret_cast<const void*>(&gradtile::wgrad_tile_kernel<BITS, DT, BT, BT>);
+    static bool attr_set = false;   // per instantiation; set before its first launch
+    if (!attr_set) {
+        if (hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, LDS); e != hipSuccess)
+            return e;
+        attr_set = true;
+    }
+    const int64_t tiles_k = (a.K + BT - 1) / BT, tiles = (a.N + BT - 1) / BT * tiles_k;
+    const int per_xcd = (int)((tiles * a.nmat + 7) / 8);
+    hipLaunchKernelGGL((gradtile::wgrad_tile_kernel<BITS, DT, BT, BT>), dim3((unsigned)per_xcd * 8, (unsigned)p.splits),
+                       dim3(2 * BT), LDS, st, a, p, (int)tiles_k, (int)tiles, per_xcd);
+    return hipGetLastError();
+}
+
 template <int BITS, int DT>
 hipError_t run(const WgradArgs& a, const GradPlan& p, hipStream_t st)
 {
-    const int64_t tiles = ((a.N + WG_BN - 1) / WG_BN) * ((a.K + WG_BK - 1) / WG_BK);
-    hipLaunchKernelGGL((wgrad_f32_kernel<BITS, DT>), dim3((unsigned)tiles, (unsigned)p.splits, (unsigned)a.nmat),
-                       dim3(256), 0, st, a, p);
-    if (hipError_t e = hipGetLastError(); e != hipSuccess)
+    hipError_t e = hipErrorInvalidValue;
+    if (p.tile == 0) {
+        const int64_t tiles = ((a.N + WG_BN - 1) / WG_BN) * ((a.K + WG_BK - 1) / WG_BK);
+        hipLaunchKernelGGL((wgrad_f32_kernel<BITS, DT>), dim3((unsigned)tiles, (unsigned)p.splits, (unsigned)a.nmat),
+                           dim3(256), 0, st, a, p);
+        e = hipGetLastError();
+    } else if constexpr (DT != DT_F32) {
+        e = p.tile == 1 ? run_tile<BITS, DT, 256>(a, p, st) : run_tile<BITS, DT, 128>(a, p, st);
+    }
+    if (e != hipSuccess)
         return e;
     if (p.splits > 1) {
         const int64_t count = a.N * (a.K / a.gs);
@@ -43,13 +69,15 @@ hipError_t QP_CAT(launch_wgrad_b, QP_BITS)(const WgradArgs& a, const GradPlan& p
 }
 
 #if QP_BITS == 4
-GradPlan wgrad_plan(int64_t m, int64_t n, int64_t k, int nmat, int, int gs, int)
+GradPlan wgrad_plan(int64_t m, int64_t n, int64_t k, int nmat, int gs, bool tile_kernels)
 {
-    const int64_t tiles = nmat * ((n + WG_BN - 1) / WG_BN) * ((k + WG_BK - 1) / WG_BK);
-    const int64_t steps = (m + WG_M - 1) / WG_M;
-    int64_t splits = std::clamp<int64_t>(std::min((512 + tiles - 1) / std::max<int64_t>(tiles, 1), steps / 8), 1, 64);
     GradPlan p{};
-    p.tile = 0;
+    auto count = [&](int64_t b) { return nmat * ((n + b - 1) / b) * ((k + b - 1) / b); };
+    p.tile = !tile_kernels ? 0 : count(256) >= 256 ? 1 : 2;
+    const int64_t step = p.tile == 0 ? WG_M : gradtile::STEP, want = p.tile == 1 ? 256 : 512;
+    const int64_t tiles = std::max<int64_t>(count(p.tile == 1 ? 256 : 128), 1);
+    const int64_t steps = (m + step - 1) / step;
+    const int64_t splits = std::clamp<int64_t>(std::min(want / tiles, steps / 8), 1, 64);
     p.per_split = std::max<int64_t>((steps + splits - 1) / splits, 1);
     p.splits = (int)std::max<int64_t>((steps + p.per_split - 1) / p.per_split, 1);
     p.partial_bytes = p.splits > 1 ? (size_t)p.splits * (size_t)nmat * 2 * (size_t)n * (size_t)(k / gs) * 4 : 0;
