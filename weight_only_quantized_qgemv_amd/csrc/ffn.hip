@@ -55,6 +55,18 @@ hipError_t product(const FfnArgs& a, const void* x, int64_t k, const QWeight& w,
     return launch_qgemm(g, st);
 }
 
+hipError_t gate_up(const GateUpArgs& a, hipStream_t st, bool* done)
+{
+    switch (a.bits) {
+    case 2: return launch_gate_up_b2(a, st, done);
+    case 3: return launch_gate_up_b3(a, st, done);
+    case 4: return launch_gate_up_b4(a, st, done);
+    case 6: return launch_gate_up_b6(a, st, done);
+    case 8: return launch_gate_up_b8(a, st, done);
+    }
+    return hipErrorInvalidValue;
+}
+
 size_t elem_size(int dt) { return dt == DT_F32 ? 4 : 2; }
 size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
@@ -73,7 +85,13 @@ hipError_t launch_ffn(const FfnArgs& a, hipStream_t st)
     char* const h = static_cast<char*>(a.workspace);
     char* const g = a.saved != nullptr ? static_cast<char*>(a.saved) : h;
     char* const u = a.saved != nullptr ? g + (size_t)a.M * (size_t)a.F * elem_size(a.dt) : h + hb;
-    if (a.F > 0) {
+    bool done = false;
+    if (a.F > 0 && a.D > 0) {
+        GateUpArgs k{a.x, a.dt, a.act, a.M, a.D, a.F, a.gate, a.up, a.bits, a.gs, h, a.saved};
+        if (hipError_t e = gate_up(k, st, &done); e != hipSuccess)
+            return e;
+    }
+    if (a.F > 0 && !done) {
         if (hipError_t e = product(a, a.x, a.D, a.gate, a.F, g, st); e != hipSuccess)
             return e;
         if (hipError_t e = product(a, a.x, a.D, a.up, a.F, u, st); e != hipSuccess)

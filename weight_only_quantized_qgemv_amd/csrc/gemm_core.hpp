@@ -34,9 +34,11 @@
 //    strip share an L2.
 // Fused gate / up (NMAT = 2): the weight tile holds BN / 2 gate rows then the
 // same BN / 2 up rows; each wave's fragments pair a gate column with its up
-// column in the same lane, and the epilogue writes SiLU(gate) * up.
+// column in the same lane, and the epilogue writes SiLU(gate) * up (the dense
+// form: any activation of act.hpp, and the two products where they are kept).
 #pragma once
 
+#include "act.hpp"
 #include "codepair.hpp"
 #include "common.hpp"
 #include "mx.hpp"
@@ -61,6 +63,10 @@ struct GemmArgs {
     const int32_t* n_tiles;    // device tile count
     int top_k;
     uint32_t outer_b, inner_b; // pair p's row: x + (p/top_k)*outer_b + (p%top_k)*inner_b bytes
+    // Dense fused form: the activation (act.hpp), and where the two products
+    // are kept ([M, N] each, y_bytes), or null.
+    int act;
+    void* saved[2];
 };
 
 namespace gemm {
@@ -266,7 +272,6 @@ __global__ __launch_bounds__(THREADS) void qgemm_tile_kernel(GemmArgs ga)
     static_assert(FN >= NMAT && FN % NMAT == 0 && FN * 32 * WGN == BN, "wave columns");
     static_assert(NMAT == 1 || (BNO % 64 == 0 && (BNO * CL::CPR) % 64 == 0),
                   "each DMA instruction within one matrix");
-    static_assert(NMAT == 1 || ROUTED, "the fused form is routed");
     constexpr int A_STAGE = BM * ROW_BYTES;
     constexpr int A_INSTR = A_STAGE / 1024 / WAVES;        // 1 KB DMA instructions per wave
     static_assert(A_INSTR * 1024 * WAVES == A_STAGE, "activation stage in whole DMA blocks");
@@ -327,7 +332,7 @@ __global__ __launch_bounds__(THREADS) void qgemm_tile_kernel(GemmArgs ga)
         if (tile >= ga.tiles)
             return;
         m0 = (tile / ga.tiles_n) * BM;
-        n0 = (tile % ga.tiles_n) * BN;
+        n0 = (tile % ga.tiles_n) * BNO;
     }
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
@@ -670,10 +675,18 @@ __global__ __launch_bounds__(THREADS) void qgemm_tile_kernel(GemmArgs ga)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 float v = acc[i][j][r];
-                if constexpr (NMAT == 2)
-                    v = silu_f32(v) * acc[i][j + FNO][r];
                 const uint32_t off = (orow[r] >= 0 && col < N)
                     ? ((uint32_t)orow[r] * (uint32_t)N + (uint32_t)col) * 2 : OOB;
+                if constexpr (NMAT == 2 && ROUTED)
+                    v = silu_f32(v) * acc[i][j + FNO][r];
+                if constexpr (NMAT == 2 && !ROUTED) {
+                    const float u = acc[i][j + FNO][r];
+                    if (ga.saved[0] != nullptr) {   // uniform
+                        __builtin_amdgcn_raw_buffer_store_b16(Elem<DT>::from_f32(v), rsrc(ga.saved[0], ga.y_bytes), off, 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b16(Elem<DT>::from_f32(u), rsrc(ga.saved[1], ga.y_bytes), off, 0, 0);
+                    }
+                    v = act_f32(ga.act, v) * u;
+                }
                 __builtin_amdgcn_raw_buffer_store_b16(Elem<DT>::from_f32(v), ry, off, 0, 0);
             }
         }

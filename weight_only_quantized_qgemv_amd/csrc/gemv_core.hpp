@@ -101,6 +101,8 @@ struct GemvKernelArgs {
     uint32_t out_bytes;      // size of `out` in bytes (< 2^31)
     uint32_t x_bytes;        // bytes of activations reachable from `x` (< 2^31; read
                              // by the matrix-core kernel's table DMA)
+    int act;                 // activation of the gated form (0: SiLU; act.hpp), read by
+                             // the skinny matrix-core kernel
 };
 
 // Tiles of a launch and tile t's expert, first pair slot and pair count;

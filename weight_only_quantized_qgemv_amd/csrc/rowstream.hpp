@@ -23,8 +23,11 @@
 // from there. The first row batch's loads are issued before that set-up (and
 // after the raw activation loads, which are waited for first), so the set-up
 // runs under the weight stream's latency.
+// NMAT = 2 is the gated form: a wave streams the same rows of a gate and an up
+// matrix through one set of slices and stores act(gate) * up.
 #pragma once
 
+#include "act.hpp"
 #include "common.hpp"
 #include "codepair.hpp"
 #include "gemv_core.hpp"
@@ -39,6 +42,11 @@ struct RowStreamArgs {
     void* y;                    // [M, N]
     int M, N, K, gs;
     uint32_t units_row;         // K / 32
+    // The gated form (NMAT = 2): y = act(x W^T) * (x Up^T), Up of W's shape.
+    const uint32_t* up_wq;
+    const void* up_scales;
+    const void* up_biases;
+    int act;
 };
 
 template <int DT> struct RowStreamPair;
@@ -85,14 +93,14 @@ template <int BITS, int UPL, int MT = 1> constexpr int rowstream_depth()
         return d;
 }
 
-template <int BITS, int DT, int MT, int UPL, int WPB, bool WIDE, int KL>
+template <int BITS, int DT, int MT, int UPL, int WPB, bool WIDE, int KL, int NMAT = 1>
 __global__ __launch_bounds__(64 * WPB) void qgemv_rowstream_kernel(RowStreamArgs a)
 {
     using PX = RowStreamPair<DT>;
     using E = Elem<DT>;
     using St = typename E::storage;
     static_assert(BITS == 2 || BITS == 3 || BITS == 4 || BITS == 6 || BITS == 8, "code widths");
-    constexpr int D = rowstream_depth<BITS, UPL, MT>();
+    constexpr int D = rowstream_depth<BITS, UPL * NMAT, MT>();
     using CO = CodeOrder<BITS>;
     const int lane = threadIdx.x & 63;
     // A wave is S slots of KL lanes (KL = 32 for rows of at most 32 units, so
@@ -113,9 +121,13 @@ __global__ __launch_bounds__(64 * WPB) void qgemv_rowstream_kernel(RowStreamArgs
 
     const uint32_t row_bytes = (uint32_t)a.K * BITS / 8;
     const uint32_t groups_row = (uint32_t)(a.K / a.gs);
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.wq, (uint32_t)a.N * row_bytes);
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.scales, (uint32_t)a.N * groups_row * 2);
-    const __amdgpu_buffer_rsrc_t rb = make_rsrc(a.biases, (uint32_t)a.N * groups_row * 2);
+    __amdgpu_buffer_rsrc_t rw[NMAT], rs[NMAT], rb[NMAT];
+#pragma unroll
+    for (int t = 0; t < NMAT; ++t) {
+        rw[t] = make_rsrc(t ? a.up_wq : a.wq, (uint32_t)a.N * row_bytes);
+        rs[t] = make_rsrc(t ? a.up_scales : a.scales, (uint32_t)a.N * groups_row * 2);
+        rb[t] = make_rsrc(t ? a.up_biases : a.biases, (uint32_t)a.N * groups_row * 2);
+    }
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, (uint32_t)a.M * (uint32_t)a.K * 2);
     St* y = static_cast<St*>(a.y);
     uint32_t gofs[UPL];
@@ -142,12 +154,12 @@ __global__ __launch_bounds__(64 * WPB) void qgemv_rowstream_kernel(RowStreamArgs
     // that need them through the wave's own LDS slots.
     constexpr int SBD = 32 * D * UPL;                // dwords of one batch's scales, gs >= 32
     constexpr int NV = (SBD + 63) / 64;
-    __shared__ uint32_t sbl[WPB][2][WIDE ? SBD : 1];
+    __shared__ uint32_t sbl[WPB][2 * NMAT][WIDE ? SBD : 1];
     const int wv = (int)(threadIdx.x >> 6);
     const uint32_t nd = (uint32_t)(S * D) * groups_row / 2;   // the wave's S * D rows
-    uint32_t sw[NV], bw[NV];
-    uint32_t w[D][UPL][BITS];
-    St sv[D][UPL], bv[D][UPL];
+    uint32_t sw[NMAT][NV], bw[NMAT][NV];
+    uint32_t w[NMAT][D][UPL][BITS];
+    St sv[NMAT][D][UPL], bv[NMAT][D][UPL];
     auto load = [&](int r0) {
         if constexpr (WIDE) {
             const uint32_t base = (uint32_t)r0 * groups_row * 2;
@@ -155,24 +167,29 @@ __global__ __launch_bounds__(64 * WPB) void qgemv_rowstream_kernel(RowStreamArgs
             for (int v = 0; v < NV; ++v) {
                 const uint32_t i = (uint32_t)(lane + 64 * v);
                 const uint32_t off = i < nd ? base + 4 * i : OOB;
-                sw[v] = __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0);
-                bw[v] = __builtin_amdgcn_raw_buffer_load_b32(rb, off, 0, 0);
+#pragma unroll
+                for (int t = 0; t < NMAT; ++t) {
+                    sw[t][v] = __builtin_amdgcn_raw_buffer_load_b32(rs[t], off, 0, 0);
+                    bw[t][v] = __builtin_amdgcn_raw_buffer_load_b32(rb[t], off, 0, 0);
+                }
             }
         }
 #pragma unroll
-        for (int d = 0; d < D; ++d)
+        for (int t = 0; t < NMAT; ++t)
 #pragma unroll
-            for (int j = 0; j < UPL; ++j) {
-                const int u = kl + KL * j, r = r0 + slot * D + d;
-                const bool live = u < (int)a.units_row && r < a.N;
-                buffer_words<BITS, BITS == 8 ? 0 : kStreamPolicy>(
-                    rw, live ? (uint32_t)r * row_bytes + (uint32_t)u * (4 * BITS) : OOB, w[d][j]);
-                if constexpr (!WIDE) {
-                    const uint32_t so = live ? (uint32_t)r * groups_row * 2 + gofs[j] : OOB;
-                    sv[d][j] = buffer_elem<DT>(rs, so);
-                    bv[d][j] = buffer_elem<DT>(rb, so);
+            for (int d = 0; d < D; ++d)
+#pragma unroll
+                for (int j = 0; j < UPL; ++j) {
+                    const int u = kl + KL * j, r = r0 + slot * D + d;
+                    const bool live = u < (int)a.units_row && r < a.N;
+                    buffer_words<BITS, BITS == 8 ? 0 : kStreamPolicy>(
+                        rw[t], live ? (uint32_t)r * row_bytes + (uint32_t)u * (4 * BITS) : OOB, w[t][d][j]);
+                    if constexpr (!WIDE) {
+                        const uint32_t so = live ? (uint32_t)r * groups_row * 2 + gofs[j] : OOB;
+                        sv[t][d][j] = buffer_elem<DT>(rs[t], so);
+                        bv[t][d][j] = buffer_elem<DT>(rb[t], so);
+                    }
                 }
-            }
     };
     // Units past the row take zero scale and bias, as the per-lane loads
     // give them (their codes and activations are zero as well).
@@ -182,8 +199,11 @@ __global__ __launch_bounds__(64 * WPB) void qgemv_rowstream_kernel(RowStreamArgs
             for (int v = 0; v < NV; ++v) {
                 const uint32_t i = (uint32_t)(lane + 64 * v);
                 if (i < nd) {
-                    sbl[wv][0][i] = sw[v];
-                    sbl[wv][1][i] = bw[v];
+#pragma unroll
+                    for (int t = 0; t < NMAT; ++t) {
+                        sbl[wv][2 * t][i] = sw[t][v];
+                        sbl[wv][2 * t + 1][i] = bw[t][v];
+                    }
                 }
             }
 #pragma unroll
@@ -195,10 +215,13 @@ __global__ __launch_bounds__(64 * WPB) void qgemv_rowstream_kernel(RowStreamArgs
                     // e % 2 of slot e / 2 (little-endian); e / 2 < SBD for
                     // every lane, live or not. Read as the slots' own type.
                     const uint32_t e = (uint32_t)(slot * D + d) * groups_row + gofs[j] / 2;
-                    const uint32_t ds = sbl[wv][0][e >> 1], db = sbl[wv][1][e >> 1];
                     const uint32_t sh = 16 * (e & 1);
-                    sv[d][j] = live ? St(ds >> sh) : St(0);
-                    bv[d][j] = live ? St(db >> sh) : St(0);
+#pragma unroll
+                    for (int t = 0; t < NMAT; ++t) {
+                        const uint32_t ds = sbl[wv][2 * t][e >> 1], db = sbl[wv][2 * t + 1][e >> 1];
+                        sv[t][d][j] = live ? St(ds >> sh) : St(0);
+                        bv[t][d][j] = live ? St(db >> sh) : St(0);
+                    }
                 }
         }
     };
@@ -252,18 +275,19 @@ __global__ __launch_bounds__(64 * WPB) void qgemv_rowstream_kernel(RowStreamArgs
         if (!first)
             load(r0);
         exchange();
-        float acc[D * MT];
+        float acc[NMAT * D * MT];
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
+        for (int td = 0; td < NMAT * D; ++td) {
+            const int t = td / D, d = td % D;
             float total[MT];
 #pragma unroll
             for (int m = 0; m < MT; ++m)
                 total[m] = 0.0f;
 #pragma unroll
             for (int j = 0; j < UPL; ++j) {
-                const Orient o = orient<BITS>(E::to_f32(sv[d][j]), E::to_f32(bv[d][j]));
+                const Orient o = orient<BITS>(E::to_f32(sv[t][d][j]), E::to_f32(bv[t][d][j]));
                 uint32_t cp[16];
-                code_pairs<BITS, DT>(w[d][j], o.flip, cp);
+                code_pairs<BITS, DT>(w[t][d][j], o.flip, cp);
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     float part = 0.0f;
@@ -275,16 +299,20 @@ __global__ __launch_bounds__(64 * WPB) void qgemv_rowstream_kernel(RowStreamArgs
             }
 #pragma unroll
             for (int m = 0; m < MT; ++m)
-                acc[d * MT + m] = total[m];
+                acc[td * MT + m] = total[m];
         }
-        reduce_slots<D * MT, KL>(acc);
+        reduce_slots<NMAT * D * MT, KL>(acc);
         if (kl == KL - 1) {
 #pragma unroll
             for (int d = 0; d < D; ++d)
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
-                    if (r0 + slot * D + d < a.N && m < a.M)
-                        y[(int64_t)m * a.N + r0 + slot * D + d] = E::from_f32(acc[d * MT + m]);
+                    if (r0 + slot * D + d < a.N && m < a.M) {
+                        float v = acc[d * MT + m];
+                        if constexpr (NMAT == 2)
+                            v = act_f32(a.act, v) * acc[(D + d) * MT + m];
+                        y[(int64_t)m * a.N + r0 + slot * D + d] = E::from_f32(v);
+                    }
         }
     }
 }

@@ -37,6 +37,7 @@
 // the four lane rows once per slice and kept in LDS next to the partial sums.
 #pragma once
 
+#include "act.hpp"
 #include "codepair.hpp"
 #include "gemv_core.hpp"
 
@@ -666,7 +667,7 @@ __global__ __launch_bounds__(64 * kSkinnyMaxWaves) void qgemv_skinny_kernel(Gemv
                 const int m = 4 * g + r;
                 float v = tot[0][r];
                 if constexpr (NMAT == 2)
-                    v = silu_f32(tot[0][r]) * tot[1][r];
+                    v = act_f32(a.act, tot[0][r]) * tot[1][r];
                 uint32_t off = OOB;
                 if (m < rows && n < r_hi) {
                     const uint32_t pr = a.perm != nullptr ? (uint32_t)a.perm[start + m] : (uint32_t)(start + m);
