@@ -466,13 +466,14 @@ def _act_code(act: str) -> int:
 
 def _like(t, like, name, shape=None, dtype=None):
     """t is a contiguous tensor on like's device (of `shape`, of `dtype`); returns t."""
-    if not t.is_cuda or t.device != like.device:
+    d = t.get_device()                 # -1 for host tensors
+    if d < 0 or d != like.get_device():
         raise ValueError(f"{name} must be a device tensor on {like.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     return t
 

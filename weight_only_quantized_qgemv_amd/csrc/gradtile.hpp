@@ -38,7 +38,11 @@ using gemm::waitcnt_vm_lgkm0;
 constexpr int STEP = 64;
 constexpr uint32_t OOB = 0x80000000u;
 
-__device__ __forceinline__ int turn_swz(int r) { return ((r >> 1) ^ (r >> 3)) & 7; }
+// Fragment reads take 16 lanes a cycle in groups of four consecutive rows (0-3,
+// 12-15, 20-23, 24-27 and the rest): with (r >> 1) & 7 alone those hit 8
+// chunks of both row parities, and the two bits of r >> 4, one value in each
+// half of a 32-row tile, keep that while spreading rows 8 apart.
+__device__ __forceinline__ int turn_swz(int r) { return ((r >> 1) & 7) ^ ((r >> 4) & 3); }
 
 // Which 4 x 8 block a thread turns: octet o of the tile's columns, contraction
 // rows 4 rq .. 4 rq + 3. Eight lanes walk octets, the next lane bit the two
@@ -51,7 +55,7 @@ template <int COLS> struct TurnMap {
     {
         o = (tid & 7) | (((tid >> 4) & (HI - 1)) << 3);
         rq = ((tid >> 3) & 1) | ((tid >> (4 + __builtin_ctz(HI))) << 1);
-        const int x = (rq >> 1) ^ (4 * (o & 1)) ^ (o & 7);   // chunk ^ turn_swz(8 o)
+        const int x = (rq >> 1) ^ (4 * (o & 1)) ^ ((o >> 1) & 3);   // chunk ^ turn_swz(8 o)
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj)
             at[jj] = (uint32_t)((8 * o + 2 * jj) * 128 + ((x ^ jj) << 4) + 8 * (rq & 1));
@@ -64,8 +68,8 @@ template <int COLS> struct TurnMap {
 };
 
 // Byte offsets of the fragments of LDS rows base + 32 J + lane % 32: chunk
-// 2 kk + lane / 32 of tile J is at frag[kk ^ (2 (J & 1))] + 4096 J, for base a
-// multiple of 32 (32 rows on, the swizzle's bit 2 flips).
+// 2 kk + lane / 32 of tile J is at frag[kk ^ (J & 1)] + 4096 J, for base a
+// multiple of 32 (32 rows on, the swizzle's bit 1 flips).
 __device__ __forceinline__ void frag_offsets(int lane, int base, uint32_t (&f)[4])
 {
     const int c = lane & 31, half = lane >> 5;
@@ -232,10 +236,10 @@ __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPla
             frag_t af[FM], bf[FN];
 #pragma unroll
             for (int i = 0; i < FM; ++i)
-                af[i] = *reinterpret_cast<const frag_t*>(as + fa[kk ^ (2 * (i & 1))] + 4096 * i);
+                af[i] = *reinterpret_cast<const frag_t*>(as + fa[kk ^ (i & 1)] + 4096 * i);
 #pragma unroll
             for (int j = 0; j < FN; ++j)
-                bf[j] = *reinterpret_cast<const frag_t*>(bs + fb[kk ^ (2 * (j & 1))] + 4096 * j);
+                bf[j] = *reinterpret_cast<const frag_t*>(bs + fb[kk ^ (j & 1)] + 4096 * j);
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -427,10 +431,10 @@ __global__ __launch_bounds__(2 * BN) void wgrad_tile_kernel(WgradArgs a, GradPla
             frag_t af[FM], bf[FN];
 #pragma unroll
             for (int i = 0; i < FM; ++i)
-                af[i] = *reinterpret_cast<const frag_t*>(as + fa[kk ^ (2 * (i & 1))] + 4096 * i);
+                af[i] = *reinterpret_cast<const frag_t*>(as + fa[kk ^ (i & 1)] + 4096 * i);
 #pragma unroll
             for (int j = 0; j < FN; ++j)
-                bf[j] = *reinterpret_cast<const frag_t*>(bs + fb[kk ^ (2 * (j & 1))] + 4096 * j);
+                bf[j] = *reinterpret_cast<const frag_t*>(bs + fb[kk ^ (j & 1)] + 4096 * j);
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll

@@ -6,11 +6,13 @@
 //   v not allowed:  z = -inf
 // rounded once to the logits' type.
 //
-// A block takes a tile of one row's vocabulary. It counts the row's tokens
-// that fall into the tile in LDS (integer atomics: their order changes
-// nothing) and notes the last bias entry of each token there, then streams
-// the tile once. Bound by the read and write of the logits; the row's tokens
-// are read once per tile, from L2.
+// A block takes a tile of one row's vocabulary, 16 logits a thread in registers.
+// It counts the row's tokens that fall into the tile in LDS (integer atomics:
+// their order changes nothing), applies the penalties, then uses the same LDS
+// for the last bias entry of each token. Bound by the read and write of the
+// logits; the row's tokens are read once per tile, from L2. One word of LDS a
+// token and 16 tokens a thread let 64 rows of 128K tokens be on the GPU at
+// once; with a word each for counts and biases it takes two rounds.
 #include <algorithm>
 
 #include "common.hpp"
@@ -20,121 +22,191 @@ namespace qp {
 
 namespace {
 
-template <int DT, int TILE>
-__global__ __launch_bounds__(256) void logits_kernel(LogitsArgs a, int64_t tiles, bool vec)
+// Sixteen bytes at any element's address (rows of an odd vocabulary).
+template <int DT> struct Wide;
+template <> struct Wide<DT_F32> { typedef u32x4_t type __attribute__((aligned(4))); };
+template <> struct Wide<DT_F16> { typedef u32x4_t type __attribute__((aligned(2))); };
+template <> struct Wide<DT_BF16> { typedef u32x4_t type __attribute__((aligned(2))); };
+
+constexpr int kThreads = 512, kSets = 2, kTile = kThreads * kSets * 8;
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a, int tiles)
 {
     using E = Elem<DT>;
     using St = typename E::storage;
-    constexpr int VN = 16 / (int)sizeof(St);
-    __shared__ uint32_t count[TILE];   // bit 0: in the prompt; bits 1..: times made
-    __shared__ uint32_t entry[TILE];   // last bias entry + 1
+    constexpr int NV = 8 * (int)sizeof(St) / 16;
+    __shared__ __attribute__((aligned(16))) uint32_t slot[kTile];
     const int64_t row = (int64_t)blockIdx.x / tiles;
-    const int64_t v0 = ((int64_t)blockIdx.x % tiles) * TILE;
-    const int n = (int)(a.vocab - v0 < TILE ? a.vocab - v0 : TILE);
+    const int v0 = ((int)((int64_t)blockIdx.x % tiles)) * kTile;
+    const int n = (int)(a.vocab - v0 < kTile ? a.vocab - v0 : kTile);
     const int tid = (int)threadIdx.x;
     const bool hist = a.history != nullptr, bias = a.bias_ids != nullptr;
-    if (hist || bias) {
-        for (int i = tid; i < TILE; i += 256) {
-            count[i] = 0;
-            entry[i] = 0;
+
+    // Everything whose address is known is asked for first: the tile's logits
+    // (set s of a thread: eight from 8 (tid + s kThreads) on), the row's
+    // parameters, the mask's byte of each set (a tile starts at a whole word,
+    // and a word's bytes are in order), the ends of the row's tokens and
+    // biases; then the first tokens. It arrives while the counts are cleared.
+    const St* in = static_cast<const St*>(a.logits) + row * a.in_stride + v0;
+    u32x4_t raw[kSets][NV];
+    uint32_t allowed[kSets];
+#pragma unroll
+    for (int s = 0; s < kSets; ++s) {
+        const int i0 = 8 * (tid + s * kThreads);
+        if (i0 + 8 <= n) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                raw[s][j] = *reinterpret_cast<const typename Wide<DT>::type*>(in + i0 + j * (16 / (int)sizeof(St)));
         }
-        __syncthreads();
+        allowed[s] = 0xFFu;
+        if (a.mask != nullptr && i0 < n)
+            allowed[s] = a.mask[row * a.mask_stride + ((v0 + i0) >> 5)] >> (i0 & 31);
     }
-    if (hist) {
-        int64_t lo = a.offsets[row], hi = a.offsets[row + 1];
-        lo = lo < 0 ? 0 : lo;
-        hi = hi < a.history_len ? hi : a.history_len;
-        const int64_t made = lo + (a.prompt_lens != nullptr ? a.prompt_lens[row] : 0);
-        for (int64_t i = lo + tid; i < hi; i += 256) {
-            const int64_t v = a.history[i] - v0;
-            if (v >= 0 && v < n) {
-                if (i >= made)
-                    atomicAdd(&count[v], 2u);
-                else
-                    atomicOr(&count[v], 1u);
-            }
-        }
-    }
-    int64_t b0 = 0;
-    if (bias) {
-        int64_t hi = a.bias_offsets[row + 1];
-        b0 = a.bias_offsets[row];
-        b0 = b0 < 0 ? 0 : b0;
-        hi = hi < a.bias_len ? hi : a.bias_len;
-        for (int64_t i = b0 + tid; i < hi; i += 256) {
-            const int64_t v = a.bias_ids[i] - v0;
-            if (v >= 0 && v < n)
-                atomicMax(&entry[v], (uint32_t)(i - b0) + 1u);
-        }
-    }
-    if (hist || bias)
-        __syncthreads();
     const float rep = a.repetition != nullptr ? a.repetition[row] : 1.0f;
     const float freq = a.frequency != nullptr ? a.frequency[row] : 0.0f;
     const float pres = a.presence != nullptr ? a.presence[row] : 0.0f;
-    const uint32_t* mask = a.mask != nullptr ? a.mask + row * a.mask_stride : nullptr;
-    const St* in = static_cast<const St*>(a.logits) + row * a.in_stride + v0;
-    St* out = static_cast<St*>(a.out) + row * a.out_stride + v0;
-    auto adjust = [&](int i, float z) {
-        if (hist) {
-            const uint32_t c = count[i];
-            if (c != 0) {
-                z = z > 0.0f ? z / rep : z * rep;
-                if (c > 1)
-                    z = z - freq * (float)(c >> 1) - pres;
-            }
-        }
-        if (bias) {
-            const uint32_t e = entry[i];
-            if (e != 0)
-                z += a.bias_values[b0 + (int64_t)e - 1];
-        }
-        if (mask != nullptr) {
-            const int64_t v = v0 + i;
-            if (((mask[v >> 5] >> (v & 31)) & 1u) == 0)
-                z = -__builtin_inff();
-        }
-        return z;
+    int lo = 0, hi = 0, b0 = 0, b1 = 0;
+    int64_t made = 0;
+    if (hist) {
+        lo = a.offsets[row];
+        hi = a.offsets[row + 1];
+        lo = lo < 0 ? 0 : lo;
+        hi = hi < (int)a.history_len ? hi : (int)a.history_len;
+        made = (int64_t)lo + (a.prompt_lens != nullptr ? a.prompt_lens[row] : 0);
+    }
+    if (bias) {
+        b0 = a.bias_offsets[row];
+        b1 = a.bias_offsets[row + 1];
+        b0 = b0 < 0 ? 0 : b0;
+        b1 = b1 < (int)a.bias_len ? b1 : (int)a.bias_len;
+    }
+    constexpr int U = 4;
+    int32_t t[U], tb = -1;
+    auto fetch = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            t[j] = i + j * kThreads < hi ? a.history[i + j * kThreads] : -1;
     };
-    int i = tid * VN;
-    if (vec) {
-        for (; i + VN <= n; i += 256 * VN) {
-            u32x4_t w = *reinterpret_cast<const u32x4_t*>(in + i);
-            float z[VN];
+    fetch(lo + tid);
+    if (b0 + tid < b1)
+        tb = a.bias_ids[b0 + tid];
+    auto clear = [&]() {
 #pragma unroll
-            for (int j = 0; j < VN; ++j) {
-                if constexpr (DT == DT_F32)
-                    z[j] = adjust(i + j, __uint_as_float(w[j]));
-                else
-                    z[j] = adjust(i + j, E::to_f32((uint16_t)(w[j / 2] >> (16 * (j % 2)))));
-            }
+        for (int j = 0; j < 2 * kSets; ++j)
+            reinterpret_cast<u32x4_t*>(slot)[tid + j * kThreads] = u32x4_t{0, 0, 0, 0};
+    };
+    auto slots = [&](int s, uint32_t (&c)[8]) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if constexpr (DT == DT_F32)
-                    w[j] = __float_as_uint(z[j]);
-                else
-                    w[j] = (uint32_t)E::from_f32(z[2 * j]) | ((uint32_t)E::from_f32(z[2 * j + 1]) << 16);
-            }
-            *reinterpret_cast<u32x4_t*>(out + i) = w;
+        for (int j = 0; j < 8; j += 4) {
+            const u32x4_t w = *reinterpret_cast<const u32x4_t*>(slot + 8 * (tid + s * kThreads) + j);
+            c[j] = w.x; c[j + 1] = w.y; c[j + 2] = w.z; c[j + 3] = w.w;
         }
-        for (int j = i; j < n && j < i + VN; ++j)
-            out[j] = E::from_f32(adjust(j, E::to_f32(in[j])));
-    } else {
-        for (int j = tid; j < n; j += 256)
-            out[j] = E::from_f32(adjust(j, E::to_f32(in[j])));
+    };
+    // Slot: bit 0, in the prompt; the rest, times made.
+    if (hist) {
+        clear();
+        __syncthreads();
+        for (int i = lo + tid; i < hi; i += U * kThreads) {
+            if (i != lo + tid)
+                fetch(i);
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const uint32_t v = (uint32_t)t[j] - (uint32_t)v0;
+                if (t[j] >= v0 && v < (uint32_t)n) {
+                    if (i + j * kThreads >= made)
+                        atomicAdd(&slot[v], 2u);
+                    else
+                        atomicOr(&slot[v], 1u);
+                }
+            }
+        }
+        __syncthreads();
+    }
+    float z[kSets][8];
+#pragma unroll
+    for (int s = 0; s < kSets; ++s) {
+        const int i0 = 8 * (tid + s * kThreads);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (i0 + 8 <= n) {
+                if constexpr (DT == DT_F32)
+                    z[s][j] = __uint_as_float(raw[s][j / 4][j % 4]);
+                else
+                    z[s][j] = E::to_f32((uint16_t)(raw[s][0][j / 2] >> (16 * (j % 2))));
+            } else {
+                z[s][j] = i0 + j < n ? E::to_f32(in[i0 + j]) : 0.0f;
+            }
+        }
+        if (hist) {
+            uint32_t c[8];
+            slots(s, c);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c[j] != 0) {
+                    z[s][j] = z[s][j] > 0.0f ? z[s][j] / rep : z[s][j] * rep;
+                    if (c[j] > 1)
+                        z[s][j] = z[s][j] - freq * (float)(c[j] >> 1) - pres;
+                }
+        }
+    }
+    // Slot: the token's last bias entry + 1.
+    if (bias) {
+        __syncthreads();   // the counts have been read
+        clear();
+        __syncthreads();
+        for (int i = b0 + tid; i < b1; i += kThreads) {
+            if (i != b0 + tid)
+                tb = a.bias_ids[i];
+            const uint32_t v = (uint32_t)tb - (uint32_t)v0;
+            if (tb >= v0 && v < (uint32_t)n)
+                atomicMax(&slot[v], (uint32_t)(i - b0) + 1u);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < kSets; ++s) {
+            uint32_t e[8];
+            slots(s, e);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (e[j] != 0)
+                    z[s][j] += a.bias_values[(int64_t)b0 + e[j] - 1];
+        }
+    }
+    St* out = static_cast<St*>(a.out) + row * a.out_stride + v0;
+#pragma unroll
+    for (int s = 0; s < kSets; ++s) {
+        const int i0 = 8 * (tid + s * kThreads);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (((allowed[s] >> j) & 1u) == 0)
+                z[s][j] = -__builtin_inff();
+        if (i0 + 8 <= n) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                u32x4_t w;
+#pragma unroll
+                for (int l = 0; l < 4; ++l) {
+                    if constexpr (DT == DT_F32)
+                        w[l] = __float_as_uint(z[s][4 * j + l]);
+                    else
+                        w[l] = (uint32_t)E::from_f32(z[s][2 * l]) | ((uint32_t)E::from_f32(z[s][2 * l + 1]) << 16);
+                }
+                *reinterpret_cast<typename Wide<DT>::type*>(out + i0 + j * (16 / (int)sizeof(St))) = w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (i0 + j < n)
+                    out[i0 + j] = E::from_f32(z[s][j]);
+        }
     }
 }
 
 template <int DT> hipError_t run(const LogitsArgs& a, hipStream_t st)
 {
-    constexpr int TILE = 4096;
-    constexpr int64_t ES = DT == DT_F32 ? 4 : 2;
-    const int64_t tiles = (a.vocab + TILE - 1) / TILE;
-    auto rows16 = [&](const void* p, int64_t stride) {
-        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (a.rows == 1 || (stride * ES) % 16 == 0);
-    };
-    const bool vec = rows16(a.logits, a.in_stride) && rows16(a.out, a.out_stride);
-    hipLaunchKernelGGL((logits_kernel<DT, TILE>), dim3((unsigned)(tiles * a.rows)), dim3(256), 0, st, a, tiles, vec);
+    const int64_t tiles = (a.vocab + kTile - 1) / kTile;
+    hipLaunchKernelGGL((logits_kernel<DT>), dim3((unsigned)(tiles * a.rows)), dim3(kThreads), 0, st, a, (int)tiles);
     return hipGetLastError();
 }
 
