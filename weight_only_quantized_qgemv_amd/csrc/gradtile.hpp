@@ -339,6 +339,92 @@ __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPla
 
 // ------------------------------------------------------------------ dW = dy^T x
 
+// The sums of a wave's 128 k (from kw on) x 32 FN weight rows (from nw on).
+// Tile i, register r: k = kw + 32 i + 8 (r / 4) + 4 half + r % 4 of weight row
+// nw + 32 j + lane % 32: unit i of the wave's four. All the codes are asked
+// for before any is used; a unit is moved down by the half's four codes once.
+template <int BITS, int DT, int FN>
+__device__ __forceinline__ void wgrad_close(const WgradArgs& a, const GradPlan& plan, int mat, int split, int64_t kw,
+                                            int64_t nw, int lane, const f32x16_t (&acc)[4][FN])
+{
+    const int half = lane >> 5;
+    const uint32_t row = (uint32_t)(a.K * BITS / 8);
+    // Rows of the tile from nw on; units past K are past the row's codes.
+    const int64_t left = a.N - nw;
+    const uint32_t rows = left > 32 * FN ? 32 * FN : left > 0 ? (uint32_t)left : 0u;
+    const __amdgpu_buffer_rsrc_t rw = rsrc(reinterpret_cast<const char*>(a.wq[mat]) + nw * row, rows * row);
+    uint32_t w[FN][4][BITS];
+    static_for<FN>([&](auto J) {
+        static_for<4>([&](auto I) {
+            constexpr int i = decltype(I)::value, j = decltype(J)::value;
+            const uint32_t off = kw + 32 * i < a.K
+                ? (uint32_t)(32 * j + (lane & 31)) * row + (uint32_t)(kw / 32 + i) * (4 * BITS) : OOB;
+#pragma unroll
+            for (int b = 0; b < BITS; ++b)
+                w[j][i][b] = __builtin_amdgcn_raw_buffer_load_b32(rw, off + 4 * b, 0, 0);
+        });
+    });
+    // Of unit i of row tile j: the scale's sum in lanes 0-31, the bias's in the
+    // others. (No branch before the last of them: the accumulators would be
+    // moved about.)
+    float v[FN][4];
+    static_for<FN>([&](auto J) {
+        constexpr int j = decltype(J)::value;
+        static_for<4>([&](auto I) {
+            constexpr int i = decltype(I)::value;
+            uint32_t u[BITS];   // the unit from code 4 half on
+#pragma unroll
+            for (int b = 0; b < BITS; ++b) {
+                constexpr int WS = 4 * BITS / 32, SH = 4 * BITS % 32;   // four codes: whole words and bits
+                const uint32_t lo = b + WS < BITS ? w[j][i][b + WS < BITS ? b + WS : 0] : 0u;
+                const uint32_t hi = b + WS + 1 < BITS ? w[j][i][b + WS + 1 < BITS ? b + WS + 1 : 0] : 0u;
+                const uint32_t moved = SH == 0 ? lo : __builtin_amdgcn_alignbit(hi, lo, SH);
+                u[b] = half ? moved : w[j][i][b];
+            }
+            using CB = CodeBytes<BITS>;
+            uint32_t bw[CB::NBW];
+            CB::split(u, bw);
+            float s = 0.0f, b = 0.0f;
+            static_for<16>([&](auto R) {
+                constexpr int r = decltype(R)::value, c = 8 * (r >> 2) + (r & 3);
+                s = __builtin_fmaf(CB::template code<c>(bw), acc[i][j][r], s);
+                b += acc[i][j][r];
+            });
+            // The upper half of s for the lower half of b, then both halves' sum.
+            const auto x = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, s),
+                                                            __builtin_bit_cast(uint32_t, b), false, false);
+            v[j][i] = __builtin_bit_cast(float, (uint32_t)x[0]) + __builtin_bit_cast(float, (uint32_t)x[1]);
+        });
+    });
+    // Lanes 0-31 store the scales' sums, lanes 32-63 the biases'.
+    using St = typename Elem<DT>::storage;
+    const int64_t groups = a.K / a.gs, count = a.N * groups, at = (nw + (lane & 31)) * groups + kw / a.gs;
+    const bool parts = plan.splits > 1;
+    float* const pd = parts ? a.partial + (((int64_t)split * a.nmat + mat) * 2 + half) * count + at : nullptr;
+    St* const sd = parts ? nullptr : static_cast<St*>(half ? a.dbiases[mat] : a.dscales[mat]) + at;
+    const int per = a.gs / 32;                                      // units of a group
+    const int live = (int)((a.K - kw) / a.gs < 4 / per ? (a.K - kw) / a.gs : 4 / per);   // groups in range
+    auto store = [&](int j, int g, float v) {
+        if (nw + 32 * j + (lane & 31) < a.N && g < live) {
+            const int64_t o = (int64_t)(32 * j) * groups + g;
+            if (parts)
+                pd[o] = v;
+            else
+                sd[o] = Elem<DT>::from_f32(v);
+        }
+    };
+    if (per == 1) {
+        static_for<FN>([&](auto J) { static_for<4>([&](auto I) { store(J, I, v[J][I]); }); });
+    } else if (per == 2) {
+        static_for<FN>([&](auto J) {
+            store(J, 0, v[J][0] + v[J][1]);
+            store(J, 1, v[J][2] + v[J][3]);
+        });
+    } else {
+        static_for<FN>([&](auto J) { store(J, 0, (v[J][0] + v[J][1]) + (v[J][2] + v[J][3])); });
+    }
+}
+
 // A: x [64][BK] turned (its LDS rows are k), B: dy [64][BN] turned (n).
 // WKW x WNW waves, each 128 k (every group closes inside a wave) x WN n.
 template <int BK, int BN> constexpr int wgrad_lds() { return 2 * (BK + BN) * 128; }
@@ -454,43 +540,186 @@ __global__ __launch_bounds__(2 * BN) void wgrad_tile_kernel(WgradArgs a, GradPla
             run_step(kt + 1, std::integral_constant<int, 1>{});
     }
 
-    // Tile i, register r: k = k0 + 128 wk + 32 i + 8 (r / 4) + 4 half + r % 4
-    // of weight row n: unit i of the wave's four.
-    const int64_t row_words = a.K * BITS / 32;
-    const int64_t kw = k0 + 128 * wk;
+    wgrad_close<BITS, DT, FN>(a, plan, mat, (int)blockIdx.y, k0 + 128 * wk, n0 + wn * WN, lane, acc);
+}
+
+// The same product with four waves of 128 k x 128 n, one on each SIMD: a
+// fragment is read from LDS by half as many waves, and nothing but the step's
+// own order has to hide the latencies. So the order is fixed: each kk's 16
+// matrix instructions carry, between them, the reads of the next kk's
+// fragments and a share of the turning of step kt + 1. The step's one barrier
+// stands before its last kk: by then the next step's tile is written and this
+// step's last fragments are in registers, and the last kk's instructions
+// cover the first reads of the next step.
+// The blocks are persistent (one a CU) and the pipeline runs on from one tile
+// to the next: loads and turning are two steps and one step ahead of the
+// products, in whatever tile that is, so only the sums at a tile's end stand
+// still.
+struct WideItem {
+    int mat, split, kt, hi;   // weight, piece of the contraction, next step, its end
+    int64_t n0, k0;
+};
+
+// Tiles in the order in which an XCD's blocks share most: bands of 8 tiles of
+// k, within a band row by row of n.
+__device__ __forceinline__ void band_order(int tile, int tiles_n, int tiles_k, int& tn, int& tk)
+{
+    const int band = tile / (8 * tiles_n), in = tile % (8 * tiles_n);
+    const int width = tiles_k - 8 * band < 8 ? tiles_k - 8 * band : 8;
+    tn = in / width;
+    tk = 8 * band + in % width;
+}
+
+template <int BITS, int DT>
+__global__ __launch_bounds__(256) void wgrad_wide_kernel(WgradArgs a, GradPlan plan, int tiles_n, int tiles_k)
+{
+    using T = MfmaTraits<DT>;
+    using frag_t = typename T::frag_t;
+    constexpr int BT = 256, STAGE = BT * 128;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    char* const a_st = lds;
+    char* const b_st = lds + 2 * STAGE;
+
+    const int tid = (int)threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wk = wave >> 1, wn = wave & 1;
+    const int steps = (int)((a.M + STEP - 1) / STEP);
+    // Items: tiles of every weight, split by split, XCD by XCD.
+    const int tiles = tiles_n * tiles_k, items = tiles * a.nmat * plan.splits, per_xcd = (items + 7) / 8;
+    const int local = (int)(blockIdx.x / 8), stride = (int)(gridDim.x / 8), first = (int)(blockIdx.x % 8) * per_xcd;
+    auto item_at = [&](int round, WideItem& it) {
+        const int l = local + round * stride;
+        if (l >= per_xcd || first + l >= items)
+            return false;
+        const int i = first + l, t = i % (tiles * a.nmat);
+        it.split = i / (tiles * a.nmat);
+        it.mat = t / tiles;
+        int tn, tk;
+        band_order(t % tiles, tiles_n, tiles_k, tn, tk);
+        it.n0 = (int64_t)tn * BT;
+        it.k0 = (int64_t)tk * BT;
+        it.kt = it.split * (int)plan.per_split;
+        it.hi = it.kt + (int)plan.per_split < steps ? it.kt + (int)plan.per_split : steps;
+        return true;
+    };
+    WideItem cur, ahead;   // the item being multiplied, and that being loaded
+    if (!item_at(0, cur))
+        return;
+    ahead = cur;
+
+    // One 8 x 8 block of each operand a thread: contraction rows 8 ro .. 8 ro + 7
+    // of the step, columns 8 o .. 8 o + 7 of the tile. A column's eight values are
+    // one 16-byte chunk of its LDS row: four rows a thread, in 8-byte halves,
+    // took 80 cycles a write (64 KB a step) against 2 steps' time in all.
+    const int o = tid & 31, ro = tid >> 5;
+    const uint32_t xrow = (uint32_t)a.K * 2, yrow = (uint32_t)(a.dy_stride * 2);
+    uint32_t off[2];   // of x and dy, in the item being loaded
+    auto set_off = [&]() {
+        const int64_t k = ahead.k0 + 8 * o, n = ahead.n0 + 8 * o;
+        off[0] = k < a.K ? (uint32_t)(8 * ro) * xrow + (uint32_t)k * 2 : OOB;
+        off[1] = n < a.N ? (uint32_t)(8 * ro) * yrow + (uint32_t)n * 2 : OOB;
+    };
+    // LDS offset of column 8 o + j: chunk ro of that row.
+    uint32_t at[4];
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-        const int64_t n = n0 + wn * WN + 32 * j + (lane & 31);
-        float ps[4], pb[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t w[BITS];
-            const bool live = n < a.N && kw + 32 * i < a.K;
-#pragma unroll
-            for (int b = 0; b < BITS; ++b)
-                w[b] = live ? a.wq[mat][n * row_words + (kw / 32 + i) * BITS + b] : 0u;
-            float s = 0.0f, b = 0.0f;
-            static_for<16>([&](auto R) {
-                constexpr int r = decltype(R)::value, c = 8 * (r >> 2) + (r & 3);
-                const uint32_t q = half ? unit_code<BITS, c + 4>(w) : unit_code<BITS, c>(w);
-                s = __builtin_fmaf((float)q, acc[i][j][r], s);
-                b += acc[i][j][r];
-            });
-            ps[i] = s + __shfl_xor(s, 32, 64);
-            pb[i] = b + __shfl_xor(b, 32, 64);
+    for (int jj = 0; jj < 4; ++jj)
+        at[jj] = (uint32_t)((8 * o + 2 * jj) * 128 + ((ro ^ turn_swz(8 * o + 2 * jj)) << 4));
+    set_off();
+    int ahead_round = 0;
+    // The step being loaded: its 64 rows of x and dy, built once a step in
+    // scalar registers (built at each load, they cost more than the load).
+    __amdgpu_buffer_rsrc_t rx, ry;
+    auto set_rows = [&]() {
+        const bool any = ahead.kt < ahead.hi;
+        const int64_t m = any ? (int64_t)ahead.kt * STEP : 0, left = any ? a.M - m : 0;
+        const uint32_t rows = (uint32_t)(left < STEP ? left : STEP);
+        rx = rsrc(static_cast<const char*>(a.x) + m * xrow, rows * xrow);
+        ry = rsrc(static_cast<const char*>(ahead.mat ? a.dy[1] : a.dy[0]) + m * yrow, rows * yrow);
+    };
+    set_rows();
+    auto advance = [&]() {   // the load cursor, one step on
+        if (++ahead.kt >= ahead.hi) {
+            if (item_at(++ahead_round, ahead))
+                set_off();
+            else
+                ahead.kt = ahead.hi = 0x3FFFFFFF;   // nothing left: loads read zeros
         }
-        if (n < a.N) {
-            const int per = a.gs / 32;   // tiles of a group
-            for (int i = 0; i < 4 && kw + 32 * i < a.K; i += per) {
-                float v = 0.0f;
-                static_for<4>([&](auto I) {
-                    constexpr int ii = decltype(I)::value;
-                    if (ii >= i && ii < i + per)
-                        v += half ? pb[ii] : ps[ii];
-                });
-                wgrad_store<DT>(a, plan, mat, (int)blockIdx.y, n, (kw + 32 * i) / a.gs, half != 0, v);
+        set_rows();
+    };
+    u32x4_t raw[2][8];
+    auto load = [&](auto G, auto I) {   // row i of operand g's block
+        constexpr int g = decltype(G)::value, i = decltype(I)::value;
+        raw[g][i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+            g == 0 ? rx : ry, off[g], (int)((uint32_t)i * (g == 0 ? xrow : yrow)), 0));
+    };
+    // Column j of operand g's block, turned, into a stage.
+    auto put = [&](int stage, auto G, auto J) {
+        constexpr int g = decltype(G)::value, j = decltype(J)::value, d = j / 2;
+        constexpr uint32_t sel = j % 2 ? 0x07060302u : 0x05040100u;
+        const u32x4_t(&v)[8] = raw[g];
+        *reinterpret_cast<u32x4_t*>((g == 0 ? a_st : b_st) + stage * STAGE + at[d] + 128 * (j & 1)) =
+            u32x4_t{__builtin_amdgcn_perm(v[1][d], v[0][d], sel), __builtin_amdgcn_perm(v[3][d], v[2][d], sel),
+                    __builtin_amdgcn_perm(v[5][d], v[4][d], sel), __builtin_amdgcn_perm(v[7][d], v[6][d], sel)};
+    };
+
+    uint32_t fa[4], fb[4];
+    frag_offsets(lane, wk * 128, fa);
+    frag_offsets(lane, wn * 128, fb);
+    frag_t af[2][4], bf[2][4];
+    // Fragment i (0..3: A, 4..7: B) of kk into buffer kk & 1.
+    auto read = [&](int stage, auto KK, auto I) {
+        constexpr int kk = decltype(KK)::value, i = decltype(I)::value;
+        if constexpr (i < 4)
+            af[kk & 1][i] = *reinterpret_cast<const frag_t*>(a_st + stage * STAGE + fa[kk ^ (i & 1)] + 4096 * i);
+        else
+            bf[kk & 1][i - 4] = *reinterpret_cast<const frag_t*>(b_st + stage * STAGE + fb[kk ^ (i & 1)] + 4096 * (i - 4));
+    };
+
+    static_for<2>([&](auto G) { static_for<8>([&](auto I) { load(G, I); }); });
+    advance();
+    static_for<2>([&](auto G) {
+        static_for<8>([&](auto J) { put(0, G, J); });
+        static_for<8>([&](auto I) { load(G, I); });
+    });
+    __syncthreads();
+    static_for<8>([&](auto I) { read(0, std::integral_constant<int, 0>{}, I); });
+
+    int stage = 0;
+    for (int round = 0; item_at(round, cur); ++round) {
+      f32x16_t acc[4][4];
+      static_for<4>([&](auto I) { static_for<4>([&](auto J) { acc[I][J] = f32x16_t{}; }); });
+#pragma unroll 1
+      for (; cur.kt < cur.hi; ++cur.kt) {
+        advance();
+        static_for<4>([&](auto KK) {
+            constexpr int kk = decltype(KK)::value;
+            if constexpr (kk == 3) {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
             }
-        }
+            static_for<16>([&](auto Q) {
+                constexpr int q = decltype(Q)::value, i = q / 4, j = q % 4;
+                acc[i][j] = T::mfma(af[kk & 1][i], bf[kk & 1][j], acc[i][j]);
+                // The next fragments, one a matrix instruction.
+                if constexpr (q < 8)
+                    read(kk == 3 ? 1 - stage : stage, std::integral_constant<int, (kk + 1) & 3>{},
+                         std::integral_constant<int, q>{});
+                // Slot 16 g + 2 j + 1: column j of operand g is turned; slot 16 g +
+                // 16 + 2 i: row i of its next block is loaded. One load every
+                // other slot: four in one slot held the wave up until the address
+                // units had taken them, which cost 970 cycles a step.
+                constexpr int slot = 16 * kk + q, h = slot / 2 % 8;
+                if constexpr (slot % 2 == 1 && kk < 2)
+                    put(1 - stage, std::integral_constant<int, kk>{}, std::integral_constant<int, h>{});
+                if constexpr (slot % 2 == 0 && (kk == 1 || kk == 2))
+                    load(std::integral_constant<int, kk - 1>{}, std::integral_constant<int, h>{});
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        });
+        stage = 1 - stage;
+      }
+      wgrad_close<BITS, DT, 4>(a, plan, cur.mat, cur.split, cur.k0 + 128 * wk, cur.n0 + 128 * wn, lane, acc);
     }
 }
 

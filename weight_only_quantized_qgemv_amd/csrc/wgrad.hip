@@ -29,6 +29,28 @@ hipError_t run_tile(const WgradArgs& a, const GradPlan& p, hipStream_t st)
 }
 
 template <int BITS, int DT>
+hipError_t run_wide(const WgradArgs& a, const GradPlan& p, hipStream_t st)
+{
+    constexpr int BT = 256, LDS = gradtile::wgrad_lds<BT, BT>();
+    const void* kern = reinterpret_cast<const void*>(&gradtile::wgrad_wide_kernel<BITS, DT>);
+    static bool attr_set = false;   // per instantiation; set before its first launch
+    if (!attr_set) {
+        if (hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, LDS); e != hipSuccess)
+            return e;
+        attr_set = true;
+    }
+    int cus = 0;
+    if (hipError_t e = device_cu_count(&cus); e != hipSuccess)
+        return e;
+    const int64_t tiles_n = (a.N + BT - 1) / BT, tiles_k = (a.K + BT - 1) / BT;
+    const int64_t items = tiles_n * tiles_k * a.nmat * p.splits;
+    const int64_t blocks = std::min<int64_t>((items + 7) / 8 * 8, std::max(cus / 8 * 8, 8));
+    hipLaunchKernelGGL((gradtile::wgrad_wide_kernel<BITS, DT>), dim3((unsigned)blocks), dim3(256), LDS, st, a, p,
+                       (int)tiles_n, (int)tiles_k);
+    return hipGetLastError();
+}
+
+template <int BITS, int DT>
 hipError_t run(const WgradArgs& a, const GradPlan& p, hipStream_t st)
 {
     hipError_t e = hipErrorInvalidValue;
@@ -38,7 +60,7 @@ hipError_t run(const WgradArgs& a, const GradPlan& p, hipStream_t st)
                            dim3(256), 0, st, a, p);
         e = hipGetLastError();
     } else if constexpr (DT != DT_F32) {
-        e = p.tile == 1 ? run_tile<BITS, DT, 256>(a, p, st) : run_tile<BITS, DT, 128>(a, p, st);
+        e = p.tile == 1 ? run_wide<BITS, DT>(a, p, st) : run_tile<BITS, DT, 128>(a, p, st);
     }
     if (e != hipSuccess)
         return e;
