@@ -159,6 +159,16 @@ def test_backward_odd_shapes(m, d, f, dt):
     check_backward(case(m, d, f, 4, 32, dt), "silu", "odd")
 
 
+@pytest.mark.parametrize("m,d,f,bits,gs,dt,act", [(70, 2080, 4640, 4, 32, BF16, "silu"),
+                                                  (300, 1024, 1600, 6, 64, F16, "gelu_tanh"),
+                                                  (520, 1536, 768, 8, 128, BF16, "gelu_tanh")])
+def test_many_tiles(m, d, f, bits, gs, dt, act):
+    """Blocks large enough for the persistent tiles, several a compute unit."""
+    c = case(m, d, f, bits, gs, dt)
+    check_backward(c, act, "many tiles")
+    check_forward(c, act, "many tiles")
+
+
 def test_backward_extreme_preactivations():
     """Gates far out on both sides: the derivative's terms vanish or stay, nothing is NaN."""
     c = case(4, 64, 64, 4, 32, F32)

@@ -65,6 +65,14 @@ def test_long_contraction_and_many_rows(bits):
     run_and_check(20, 256, 8200, bits, 64, F16, "long contraction")
 
 
+@pytest.mark.parametrize("m,k,n,bits,gs,dt", [
+    (1, 4096, 4096, 4, 64, BF16), (65, 4128, 4010, 4, 32, F16), (140, 4096, 4104, 8, 128, BF16),
+    (257, 2048, 8201, 2, 64, BF16), (64, 4224, 4096, 3, 32, F16), (200, 8192, 2050, 6, 64, BF16)])
+def test_weights_of_many_tiles(m, k, n, bits, gs, dt):
+    """Weights large enough for the persistent tiles, ragged in every direction."""
+    run_and_check(m, k, n, bits, gs, dt, "many tiles")
+
+
 @pytest.mark.parametrize("dt", [F32, BF16])
 @pytest.mark.parametrize("m,k,n", [(70, 256, 96), (300, 512, 264)])
 def test_misaligned_bases(m, k, n, dt):

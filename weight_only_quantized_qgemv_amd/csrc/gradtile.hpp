@@ -78,6 +78,31 @@ __device__ __forceinline__ void frag_offsets(int lane, int base, uint32_t (&f)[4
         f[kk] = (uint32_t)((base + c) * 128 + (((2 * kk + half) ^ turn_swz(base + c)) << 4));
 }
 
+// The accumulators of the four-wave tiles fill the accumulation registers, and
+// are read from there one by one at a tile's end: left to itself the compiler
+// copies them to vector registers by the tile, which pushes the pipeline's
+// values out to scratch memory inside the steps. acc_settle() first: it lets
+// the last matrix instructions finish (their results are not interlocked
+// against the reads).
+__device__ __forceinline__ void acc_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+__device__ __forceinline__ float acc_read(float v)
+{
+    float r;
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(r) : "a"(v));
+    return r;
+}
+
+// A resource from values that are the same in every lane, said so: kept in
+// vector registers, each of its loads would be a loop over the lanes' values.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const char* p, uint32_t bytes)
+{
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)u);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(u >> 32));
+    return rsrc(reinterpret_cast<const void*>(((uint64_t)hi << 32) | lo),
+                (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes));
+}
+
 // A step's end: at most `VM` of this wave's loads in flight, its LDS accesses
 // done, then the block barrier (bare, with compiler fences around it).
 template <int VM> __device__ __forceinline__ void step_barrier()
@@ -343,12 +368,15 @@ __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPla
 // Tile i, register r: k = kw + 32 i + 8 (r / 4) + 4 half + r % 4 of weight row
 // nw + 32 j + lane % 32: unit i of the wave's four. All the codes are asked
 // for before any is used; a unit is moved down by the half's four codes once.
-template <int BITS, int DT, int FN>
+template <int BITS, int DT, int FN, bool WIDE = false>
 __device__ __forceinline__ void wgrad_close(const WgradArgs& a, const GradPlan& plan, int mat, int split, int64_t kw,
                                             int64_t nw, int lane, const f32x16_t (&acc)[4][FN])
 {
+    // Opaque here, so that the addresses are formed at the tile's end and not
+    // kept in registers through the steps.
+    uint32_t row = (uint32_t)(a.K * BITS / 8);
+    asm volatile("" : "+s"(row), "+v"(lane));
     const int half = lane >> 5;
-    const uint32_t row = (uint32_t)(a.K * BITS / 8);
     // Rows of the tile from nw on; units past K are past the row's codes.
     const int64_t left = a.N - nw;
     const uint32_t rows = left > 32 * FN ? 32 * FN : left > 0 ? (uint32_t)left : 0u;
@@ -387,13 +415,19 @@ __device__ __forceinline__ void wgrad_close(const WgradArgs& a, const GradPlan& 
             float s = 0.0f, b = 0.0f;
             static_for<16>([&](auto R) {
                 constexpr int r = decltype(R)::value, c = 8 * (r >> 2) + (r & 3);
-                s = __builtin_fmaf(CB::template code<c>(bw), acc[i][j][r], s);
-                b += acc[i][j][r];
+                float d;
+                if constexpr (WIDE)
+                    d = acc_read(acc[i][j][r]);
+                else
+                    d = acc[i][j][r];
+                s = __builtin_fmaf(CB::template code<c>(bw), d, s);
+                b += d;
             });
             // The upper half of s for the lower half of b, then both halves' sum.
             const auto x = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, s),
                                                             __builtin_bit_cast(uint32_t, b), false, false);
             v[j][i] = __builtin_bit_cast(float, (uint32_t)x[0]) + __builtin_bit_cast(float, (uint32_t)x[1]);
+            __builtin_amdgcn_sched_barrier(0);   // one tile's values at a time
         });
     });
     // Lanes 0-31 store the scales' sums, lanes 32-63 the biases'.
@@ -609,8 +643,7 @@ __global__ __launch_bounds__(256) void wgrad_wide_kernel(WgradArgs a, GradPlan p
 
     // One 8 x 8 block of each operand a thread: contraction rows 8 ro .. 8 ro + 7
     // of the step, columns 8 o .. 8 o + 7 of the tile. A column's eight values are
-    // one 16-byte chunk of its LDS row: four rows a thread, in 8-byte halves,
-    // took 80 cycles a write (64 KB a step) against 2 steps' time in all.
+    // one 16-byte chunk of its LDS row.
     const int o = tid & 31, ro = tid >> 5;
     const uint32_t xrow = (uint32_t)a.K * 2, yrow = (uint32_t)(a.dy_stride * 2);
     uint32_t off[2];   // of x and dy, in the item being loaded
@@ -624,33 +657,46 @@ __global__ __launch_bounds__(256) void wgrad_wide_kernel(WgradArgs a, GradPlan p
 #pragma unroll
     for (int jj = 0; jj < 4; ++jj)
         at[jj] = (uint32_t)((8 * o + 2 * jj) * 128 + ((ro ^ turn_swz(8 * o + 2 * jj)) << 4));
-    set_off();
-    int ahead_round = 0;
-    // The step being loaded: its 64 rows of x and dy, built once a step in
-    // scalar registers (built at each load, they cost more than the load).
+    // The step being loaded: its 64 rows of x and dy, kept as running pointers
+    // and built into resources once a step (at each load, or from the item's
+    // numbers at each step, that scalar work costs more than the loads).
+    const char *xp, *yp;
+    int64_t left;   // rows from the step's first on
     __amdgpu_buffer_rsrc_t rx, ry;
     auto set_rows = [&]() {
-        const bool any = ahead.kt < ahead.hi;
-        const int64_t m = any ? (int64_t)ahead.kt * STEP : 0, left = any ? a.M - m : 0;
-        const uint32_t rows = (uint32_t)(left < STEP ? left : STEP);
-        rx = rsrc(static_cast<const char*>(a.x) + m * xrow, rows * xrow);
-        ry = rsrc(static_cast<const char*>(ahead.mat ? a.dy[1] : a.dy[0]) + m * yrow, rows * yrow);
+        const uint32_t rows = (uint32_t)(left < STEP ? left > 0 ? left : 0 : STEP);
+        rx = uniform_rsrc(xp, rows * xrow);
+        ry = uniform_rsrc(yp, rows * yrow);
     };
-    set_rows();
-    auto advance = [&]() {   // the load cursor, one step on
-        if (++ahead.kt >= ahead.hi) {
-            if (item_at(++ahead_round, ahead))
-                set_off();
-            else
-                ahead.kt = ahead.hi = 0x3FFFFFFF;   // nothing left: loads read zeros
-        }
+    auto set_item = [&]() {
+        const bool any = ahead.kt < ahead.hi;
+        const int64_t m = any ? (int64_t)ahead.kt * STEP : 0;
+        left = any ? a.M - m : 0;
+        xp = static_cast<const char*>(a.x) + m * xrow;
+        yp = static_cast<const char*>(ahead.mat ? a.dy[1] : a.dy[0]) + m * yrow;
+        set_off();
         set_rows();
+    };
+    set_item();
+    int ahead_round = 0;
+    auto advance = [&]() {   // the load cursor, one step on
+        if (++ahead.kt < ahead.hi) {
+            xp += (int64_t)STEP * xrow;
+            yp += (int64_t)STEP * yrow;
+            left -= STEP;
+            set_rows();
+        } else {
+            if (!item_at(++ahead_round, ahead))
+                ahead.kt = ahead.hi = 0x3FFFFFFF;   // nothing left: loads read zeros
+            set_item();
+        }
     };
     u32x4_t raw[2][8];
     auto load = [&](auto G, auto I) {   // row i of operand g's block
         constexpr int g = decltype(G)::value, i = decltype(I)::value;
+        // (The row goes into the offset that the range is checked with.)
         raw[g][i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-            g == 0 ? rx : ry, off[g], (int)((uint32_t)i * (g == 0 ? xrow : yrow)), 0));
+            g == 0 ? rx : ry, off[g] + (uint32_t)i * (g == 0 ? xrow : yrow), 0, 0));
     };
     // Column j of operand g's block, turned, into a stage.
     auto put = [&](int stage, auto G, auto J) {
@@ -719,7 +765,8 @@ __global__ __launch_bounds__(256) void wgrad_wide_kernel(WgradArgs a, GradPlan p
         });
         stage = 1 - stage;
       }
-      wgrad_close<BITS, DT, 4>(a, plan, cur.mat, cur.split, cur.k0 + 128 * wk, cur.n0 + 128 * wn, lane, acc);
+      acc_settle();
+      wgrad_close<BITS, DT, 4, true>(a, plan, cur.mat, cur.split, cur.k0 + 128 * wk, cur.n0 + 128 * wn, lane, acc);
     }
 }
 
