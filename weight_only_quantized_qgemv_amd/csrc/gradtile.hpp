@@ -186,6 +186,7 @@ __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPla
         uint32_t w[4][NW];
         uint16_t s[4], b[4];
     };
+    constexpr int W_LOADS = 4 * (BITS == 8 ? 1 : NW) + 8;
     Raw raw[2];
     auto load_w = [&](int step, Raw& r) {
         const int p = step >= steps1 ? 1 : 0;
@@ -200,8 +201,13 @@ __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPla
             rsrc(static_cast<const char*>(a.w[p].biases) + (int64_t)n0 * grow, rows * grow);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            r.w[i][0] = __builtin_amdgcn_raw_buffer_load_b32(rw, w_off + (uint32_t)i * wrow, 0, 0);
-            if constexpr (NW == 2)
+            if constexpr (BITS == 8) {
+                const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rw, w_off + (uint32_t)i * wrow, 0, 0));
+                r.w[i][0] = v[0];
+                r.w[i][1] = v[1];
+            } else
+                r.w[i][0] = __builtin_amdgcn_raw_buffer_load_b32(rw, w_off + (uint32_t)i * wrow, 0, 0);
+            if constexpr (NW == 2 && BITS != 8)
                 r.w[i][1] = __builtin_amdgcn_raw_buffer_load_b32(rw, C8::need2(oct) ? w_off + (uint32_t)i * wrow + 4 : OOB, 0, 0);
             r.s[i] = __builtin_amdgcn_raw_buffer_load_b16(rs, g_off + (uint32_t)i * grow, 0, 0);
             r.b[i] = __builtin_amdgcn_raw_buffer_load_b16(rb, g_off + (uint32_t)i * grow, 0, 0);
@@ -247,7 +253,9 @@ __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPla
     // is dequantized into the other stage and that of step kt + 2 is loaded.
     auto run_step = [&](int kt, int a_cur, auto PP) {
         constexpr int P = decltype(PP)::value;
-        // The DMA last: the step's end leaves just these in flight.
+        // The step's end leaves this step's loads in flight, and no older ones:
+        // the DMA of step kt + 1 is there. (Waiting for the weight loads too
+        // put a memory latency into every step.)
         load_w(kt + 2, raw[P]);
         __builtin_amdgcn_sched_barrier(0);
         dma_a(kt + 2, a_cur + 2 >= 3 ? a_cur - 1 : a_cur + 2);
@@ -280,7 +288,7 @@ __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPla
                     turn.put(bn, j, p01[j], p23[j]);
             }
         });
-        step_barrier<A_INSTR>();
+        step_barrier<A_INSTR + W_LOADS>();
     };
     int a_cur = 0;
     for (int kt = lo; kt < hi; kt += 2) {
