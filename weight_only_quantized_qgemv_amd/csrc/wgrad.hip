@@ -99,7 +99,7 @@ GradPlan wgrad_plan(int64_t m, int64_t n, int64_t k, int nmat, int gs, bool tile
     const int64_t step = p.tile == 0 ? WG_M : gradtile::STEP, want = p.tile == 1 ? 256 : 512;
     const int64_t tiles = std::max<int64_t>(count(p.tile == 1 ? 256 : 128), 1);
     const int64_t steps = (m + step - 1) / step;
-    const int64_t splits = std::clamp<int64_t>(std::min(want / tiles, steps / 8), 1, 64);
+    const int64_t splits = std::clamp<int64_t>(std::min(want / tiles, steps / 4), 1, 64);
     p.per_split = std::max<int64_t>((steps + splits - 1) / splits, 1);
     p.splits = (int)std::max<int64_t>((steps + p.per_split - 1) / p.per_split, 1);
     p.partial_bytes = p.splits > 1 ? (size_t)p.splits * (size_t)nmat * 2 * (size_t)n * (size_t)(k / gs) * 4 : 0;

@@ -23,9 +23,7 @@ __global__ __launch_bounds__(256) void wgrad_finish_kernel(const float* __restri
                                                            void* dbiases)
 {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < 2 * count; i += (int64_t)gridDim.x * 256) {
-        float v = 0.0f;
-        for (int s = 0; s < splits; ++s)
-            v += partial[(int64_t)s * per_split + i];
+        const float v = sum_splits(partial, splits, per_split, i);
         if (i < count)
             store_elem<DT>(dscales, i, v);
         else

@@ -42,17 +42,29 @@ __device__ __forceinline__ void xgrad_store(const XgradArgs& a, int64_t i, float
         store_elem<DT>(a.h, i, act * u);
 }
 
-// Sums the splits' partial sums in split order and closes.
+// The sum of element i's partial sums in split order, eight loads in flight.
+__device__ __forceinline__ float sum_splits(const float* partial, int splits, int64_t stride, int64_t i)
+{
+    float v = 0.0f;
+    for (int s = 0; s < splits; s += 8) {
+        float p[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            p[j] = s + j < splits ? partial[(int64_t)(s + j) * stride + i] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v += p[j];
+    }
+    return v;
+}
+
+// Sums the splits' partial sums and closes.
 template <int DT>
 __global__ __launch_bounds__(256) void xgrad_finish_kernel(XgradArgs a, int splits)
 {
     const int64_t total = a.M * a.K;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        float v = 0.0f;
-        for (int s = 0; s < splits; ++s)
-            v += a.partial[(int64_t)s * total + i];
-        xgrad_store<DT>(a, i, v);
-    }
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256)
+        xgrad_store<DT>(a, i, sum_splits(a.partial, splits, total, i));
 }
 
 // Any type, size and alignment: fp32 products on the 32x32x2 matrix
