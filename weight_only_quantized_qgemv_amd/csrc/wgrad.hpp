@@ -55,8 +55,8 @@ __global__ __launch_bounds__(256) void wgrad_f32_kernel(WgradArgs a, GradPlan pl
     __shared__ float xs[WG_M][WG_BK];
     __shared__ float ys[WG_M][WG_BN];
     const int tid = (int)threadIdx.x, lane = tid & 63, half = lane >> 5, c32 = lane & 31, wave = tid >> 6;
-    const int64_t tiles_k = (a.K + WG_BK - 1) / WG_BK;
-    const int64_t n0 = ((int64_t)blockIdx.x / tiles_k) * WG_BN, k0 = ((int64_t)blockIdx.x % tiles_k) * WG_BK;
+    const uint32_t tiles_k = (uint32_t)((a.K + WG_BK - 1) / WG_BK);
+    const int64_t n0 = (int64_t)(blockIdx.x / tiles_k) * WG_BN, k0 = (int64_t)(blockIdx.x % tiles_k) * WG_BK;
     const int mat = (int)blockIdx.z, split = (int)blockIdx.y;
     const int64_t steps = (a.M + WG_M - 1) / WG_M;
     const int64_t lo = (int64_t)split * plan.per_split;
@@ -64,14 +64,21 @@ __global__ __launch_bounds__(256) void wgrad_f32_kernel(WgradArgs a, GradPlan pl
     hi = hi < steps ? hi : steps;
 
     f32x16_t acc[4] = {};
-    float rx[8], ry[8];
+    // No branch around a load (an index past the end is held inside and its
+    // value dropped when it goes to LDS).
+    using St = typename Elem<DT>::storage;
+    St rx[8], ry[8];
+    const int c = tid & 127;
+    const bool k_in = k0 + c < a.K, n_in = n0 + c < a.N;
+    const St* const px = static_cast<const St*>(a.x) + (k_in ? k0 + c : a.K - 1);
+    const St* const py = static_cast<const St*>(a.dy[mat]) + (n_in ? n0 + c : a.N - 1);
     auto fetch = [&](int64_t step) {
-        const int c = tid & 127;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int64_t m = step * WG_M + (tid >> 7) + 2 * i;
-            rx[i] = (m < a.M && k0 + c < a.K) ? load_elem<DT>(a.x, m * a.K + k0 + c) : 0.0f;
-            ry[i] = (m < a.M && n0 + c < a.N) ? load_elem<DT>(a.dy[mat], m * a.dy_stride + n0 + c) : 0.0f;
+            int64_t m = step * WG_M + (tid >> 7) + 2 * i;
+            m = m < a.M ? m : a.M - 1;
+            rx[i] = px[m * a.K];
+            ry[i] = py[m * a.dy_stride];
         }
     };
     if (lo < hi)
@@ -80,8 +87,9 @@ __global__ __launch_bounds__(256) void wgrad_f32_kernel(WgradArgs a, GradPlan pl
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            xs[(tid >> 7) + 2 * i][tid & 127] = rx[i];
-            ys[(tid >> 7) + 2 * i][tid & 127] = ry[i];
+            const bool m_in = step * WG_M + (tid >> 7) + 2 * i < a.M;
+            xs[(tid >> 7) + 2 * i][c] = live_or_zero(m_in && k_in, Elem<DT>::to_f32(rx[i]));
+            ys[(tid >> 7) + 2 * i][c] = live_or_zero(m_in && n_in, Elem<DT>::to_f32(ry[i]));
         }
         __syncthreads();
         if (step + 1 < hi)
@@ -99,17 +107,20 @@ __global__ __launch_bounds__(256) void wgrad_f32_kernel(WgradArgs a, GradPlan pl
     const int64_t n = n0 + 32 * wave + c32;
     const int64_t row_words = a.K * BITS / 32;
     float ps[4], pb[4];
+    // All the codes before any is used; units past the row's end are dropped below.
+    uint32_t w[4][BITS];
+    const uint32_t* const row = a.wq[mat] + (n < a.N ? n : a.N - 1) * row_words;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t w[BITS];
-        const bool live = n < a.N && k0 + 32 * i < a.K;
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < BITS; ++j)
-            w[j] = live ? a.wq[mat][n * row_words + (k0 / 32 + i) * BITS + j] : 0u;
+            w[i][j] = row[(k0 + 32 * i < a.K ? k0 / 32 + i : 0) * BITS + j];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
         float s = 0.0f, b = 0.0f;
         static_for<16>([&](auto R) {
             constexpr int r = decltype(R)::value, c = 8 * (r >> 2) + (r & 3);
-            const uint32_t q = half ? unit_code<BITS, c + 4>(w) : unit_code<BITS, c>(w);
+            const uint32_t q = half ? unit_code<BITS, c + 4>(w[i]) : unit_code<BITS, c>(w[i]);
             s = __builtin_fmaf((float)q, acc[i][r], s);
             b += acc[i][r];
         });

@@ -67,6 +67,13 @@ __global__ __launch_bounds__(256) void xgrad_finish_kernel(XgradArgs a, int spli
         xgrad_store<DT>(a, i, sum_splits(a.partial, splits, total, i));
 }
 
+// v, or zero: by its bits, since a select around a loaded value becomes a branch
+// and a wait for each.
+__device__ __forceinline__ float live_or_zero(bool live, float v)
+{
+    return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & (live ? ~0u : 0u));
+}
+
 // Any type, size and alignment: fp32 products on the 32x32x2 matrix
 // instruction. A block of four waves computes 128 x 128 outputs, 32 n a step:
 // dy goes to LDS as fp32 transposed, the weights dequantized, each thread two
@@ -81,57 +88,75 @@ __global__ __launch_bounds__(256) void xgrad_f32_kernel(XgradArgs a, GradPlan pl
     __shared__ __attribute__((aligned(16))) float bs[XG_N][XG_BK];
     const int tid = (int)threadIdx.x, lane = tid & 63, half = lane >> 5, c32 = lane & 31;
     const int wm = (tid >> 6) >> 1, wk = (tid >> 6) & 1;
-    const int64_t tiles_k = (a.K + XG_BK - 1) / XG_BK;
-    const int64_t m0 = ((int64_t)blockIdx.x / tiles_k) * XG_BM, k0 = ((int64_t)blockIdx.x % tiles_k) * XG_BK;
-    const int64_t row_words = a.K * BITS / 32, groups = a.K / a.gs;
+    const uint32_t tiles_k = (uint32_t)((a.K + XG_BK - 1) / XG_BK);
+    const int64_t m0 = (int64_t)(blockIdx.x / tiles_k) * XG_BM, k0 = (int64_t)(blockIdx.x % tiles_k) * XG_BK;
+    const int gs_log = 31 - __clz(a.gs);   // 32, 64 or 128
+    const int64_t row_words = a.K * BITS / 32, groups = a.K >> gs_log;
     const int64_t steps = (a.N + XG_N - 1) / XG_N;       // of one pair
     const int64_t lo = (int64_t)blockIdx.y * plan.per_split;
     int64_t hi = lo + plan.per_split;
     hi = hi < steps * a.nmat ? hi : steps * a.nmat;
 
     f32x16_t acc[2][2] = {};
-    float ra[16], rb[2][8];
+    // What a step needs, as loaded: no branch around a load (an index past the
+    // end is held inside and its value dropped when it goes to LDS) and nothing
+    // computed from one before the products that cover its latency.
+    using St = typename Elem<DT>::storage;
+    constexpr int NW = C8::NW;
+    St ra[16], rs[2], rbias[2];
+    uint32_t rw[2][NW];
     auto fetch = [&](int64_t step) {
         const int p = step >= steps;
         const int64_t n0 = (step - (p ? steps : 0)) * XG_N;
-        const int64_t n = n0 + (tid & 31);
+        const int64_t n = n0 + (tid & 31) < a.N ? n0 + (tid & 31) : a.N - 1;
+        const St* const dy = static_cast<const St*>(a.dy[p]);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int64_t m = m0 + (tid >> 5) + 8 * i;
-            ra[i] = (m < a.M && n < a.N) ? load_elem<DT>(a.dy[p], m * a.dy_stride + n) : 0.0f;
+            ra[i] = dy[(m < a.M ? m : a.M - 1) * a.dy_stride + n];
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int e = tid + 256 * j;
-            const int64_t r = n0 + (e >> 4), k = k0 + 8 * (e & 15);
-            if (r < a.N && k < a.K) {
-                codes8_at<BITS>(a.w[p].wq + r * row_words, (int)(k >> 3), rb[j]);
-                const int64_t gi = r * groups + k / a.gs;
-                const float s = load_elem<DT>(a.w[p].scales, gi), b = load_elem<DT>(a.w[p].biases, gi);
+            const int64_t r = n0 + (e >> 4) < a.N ? n0 + (e >> 4) : a.N - 1;
+            const int64_t k = k0 + 8 * (e & 15) < a.K ? k0 + 8 * (e & 15) : a.K - 8;
+            const int oct = (int)(k >> 3);
+            const uint32_t* const w = a.w[p].wq + r * row_words + C8::word(oct);
+            rw[j][0] = w[0];
+            if constexpr (NW == 2)
+                rw[j][1] = w[C8::need2(oct) ? 1 : 0];
+            const int64_t gi = r * groups + ((int)k >> gs_log);
+            rs[j] = static_cast<const St*>(a.w[p].scales)[gi];
+            rbias[j] = static_cast<const St*>(a.w[p].biases)[gi];
+        }
+    };
+    auto stage = [&](int64_t step) {
+        const int64_t n0 = (step - (step >= steps ? steps : 0)) * XG_N;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    rb[j][i] = __builtin_fmaf(rb[j][i], s, b);
-            } else {
+        for (int i = 0; i < 16; ++i)
+            as[tid & 31][(tid >> 5) + 8 * i] =
+                live_or_zero(n0 + (tid & 31) < a.N && m0 + (tid >> 5) + 8 * i < a.M, Elem<DT>::to_f32(ra[i]));
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    rb[j][i] = 0.0f;
-            }
+        for (int j = 0; j < 2; ++j) {
+            const int e = tid + 256 * j;
+            const int64_t k = k0 + 8 * (e & 15);
+            const bool live = n0 + (e >> 4) < a.N && k < a.K;
+            float q[8];
+            C8::to_f32(rw[j], (int)((live ? k : a.K - 8) >> 3), q);
+            const float s = Elem<DT>::to_f32(rs[j]), b = Elem<DT>::to_f32(rbias[j]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                q[i] = live ? __builtin_fmaf(q[i], s, b) : 0.0f;
+            f32x4_t* d = reinterpret_cast<f32x4_t*>(&bs[e >> 4][8 * (e & 15)]);
+            d[0] = f32x4_t{q[0], q[1], q[2], q[3]};
+            d[1] = f32x4_t{q[4], q[5], q[6], q[7]};
         }
     };
     if (lo < hi)
         fetch(lo);
     for (int64_t step = lo; step < hi; ++step) {
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            as[tid & 31][(tid >> 5) + 8 * i] = ra[i];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int e = tid + 256 * j;
-            f32x4_t* d = reinterpret_cast<f32x4_t*>(&bs[e >> 4][8 * (e & 15)]);
-            d[0] = f32x4_t{rb[j][0], rb[j][1], rb[j][2], rb[j][3]};
-            d[1] = f32x4_t{rb[j][4], rb[j][5], rb[j][6], rb[j][7]};
-        }
+        stage(step);
         __syncthreads();
         if (step + 1 < hi)
             fetch(step + 1);
@@ -150,21 +175,29 @@ __global__ __launch_bounds__(256) void xgrad_f32_kernel(XgradArgs a, GradPlan pl
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[i], fb[j], acc[i][j], 0, 0, 0);
         }
     }
+    // One loop for each close: chosen inside it, the close's code would lie
+    // between two stores of the partial sums, which then wait for instructions.
+    auto each = [&](auto&& f) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int64_t m = m0 + wm * 64 + 32 * i + 8 * (r >> 2) + 4 * half + (r & 3);
-                const int64_t k = k0 + wk * 64 + 32 * j + c32;
-                if (m < a.M && k < a.K) {
-                    if (plan.splits > 1)
-                        a.partial[((int64_t)blockIdx.y * a.M + m) * a.K + k] = acc[i][j][r];
-                    else
-                        xgrad_store<DT>(a, m * a.K + k, acc[i][j][r]);
+                for (int r = 0; r < 16; ++r) {
+                    const int64_t m = m0 + wm * 64 + 32 * i + 8 * (r >> 2) + 4 * half + (r & 3);
+                    const int64_t k = k0 + wk * 64 + 32 * j + c32;
+                    if (m < a.M && k < a.K)
+                        f(m * a.K + k, acc[i][j][r]);
                 }
-            }
+    };
+    if (plan.splits > 1) {
+        float* const part = a.partial + (int64_t)blockIdx.y * a.M * a.K;
+        each([&](int64_t i, float v) { part[i] = v; });
+    } else if (a.g == nullptr) {
+        each([&](int64_t i, float v) { store_elem<DT>(a.out, i, v); });
+    } else {
+        each([&](int64_t i, float v) { xgrad_store<DT>(a, i, v); });
+    }
 }
 
 } // namespace qp
