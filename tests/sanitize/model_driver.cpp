@@ -14,7 +14,7 @@
 static int launches = 0, failures = 0;
 
 namespace qp {
-size_t ffn_workspace_bytes(int64_t m, int64_t f, int) { return (size_t)m * (size_t)f * 4; }
+size_t ffn_workspace_bytes(int64_t m, int64_t, int64_t f, int) { return (size_t)m * (size_t)f * 4; }
 hipError_t launch_ffn(const FfnArgs&, hipStream_t) { return ++launches, hipSuccess; }
 size_t linear_grad_workspace_bytes(int64_t m, int64_t, int64_t n, int, int) { return (size_t)m * (size_t)n; }
 hipError_t launch_linear_grad(const LinearGradArgs&, hipStream_t) { return ++launches, hipSuccess; }

@@ -89,6 +89,15 @@ def test_forward_odd_shapes(m, d, f, dt):
     check_forward(case(m, d, f, 4, 32, dt), "silu", "odd")
 
 
+@pytest.mark.parametrize("bits,gs,dt", [(2, 32, BF16), (3, 64, F16), (4, 128, BF16), (6, 32, F16), (8, 64, BF16)])
+@pytest.mark.parametrize("m,d,f", [(17, 512, 1152), (64, 1152, 640), (65, 896, 1024), (129, 2048, 512),
+                                   (257, 640, 2176)])
+def test_forward_in_pieces(m, d, f, bits, gs, dt):
+    """Few tiles and long contractions: the products in pieces, equal and not, with ends of 64-
+    and 256-row tiles."""
+    check_forward(case(m, d, f, bits, gs, dt), "gelu_tanh", "pieces")
+
+
 def backward_ref(c, saved, act):
     dt, bits, gs = c["dt"], c["bits"], c["gs"]
     Wg, Wu, Wd = (oh.dense(c[n], bits, gs) for n in ("gate", "up", "down"))

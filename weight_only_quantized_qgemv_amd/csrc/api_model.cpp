@@ -88,9 +88,10 @@ extern "C" {
 
 size_t qffn_workspace_bytes(int64_t m, int64_t d_model, int64_t d_ff, qp_dtype dtype)
 {
-    if (m < 0 || d_model < 0 || d_ff < 0 || !dtype_ok(dtype) || !mul_ok(m, d_ff) || !mul_ok(m * d_ff, 64))
+    if (m < 0 || d_model < 0 || d_ff < 0 || !dtype_ok(dtype) || !mul_ok(m, d_ff) || !mul_ok(m * d_ff, 64) ||
+        !mul_ok(m, d_model) || !mul_ok(m * d_model, 64))
         return 0;
-    return qp::ffn_workspace_bytes(m, d_ff, (int)dtype);
+    return qp::ffn_workspace_bytes(m, d_model, d_ff, (int)dtype);
 }
 
 qp_status qffn(const void* x, qp_dtype x_dtype, int64_t m, int64_t d_model, int64_t d_ff, const uint32_t* gate_wq,
@@ -122,7 +123,7 @@ qp_status qffn(const void* x, qp_dtype x_dtype, int64_t m, int64_t d_model, int6
             return s;
     }
     if (qp_status s = check_workspace(what, workspace, workspace_bytes,
-                                      qp::ffn_workspace_bytes(m, d_ff, (int)x_dtype)); s != QP_OK)
+                                      qp::ffn_workspace_bytes(m, d_model, d_ff, (int)x_dtype)); s != QP_OK)
         return s;
     qp::FfnArgs a{};
     a.x = x; a.dt = (int)x_dtype; a.act = (int)act;

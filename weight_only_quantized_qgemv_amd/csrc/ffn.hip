@@ -55,6 +55,70 @@ hipError_t product(const FfnArgs& a, const void* x, int64_t k, const QWeight& w,
     return launch_qgemm(g, st);
 }
 
+// The sums of a product in pieces: stored, or (gated) both products' sums
+// closed into h, and kept where a backward pass follows. Partial sums
+// [split][matrix][total].
+template <int DT, bool GATED>
+__global__ __launch_bounds__(256) void ffn_join_kernel(const float* __restrict__ partial, int splits, int64_t total,
+                                                       int act, void* saved, void* out)
+{
+    constexpr int NMAT = GATED ? 2 : 1;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const float v = sum_splits(partial, splits, NMAT * total, i);
+        if constexpr (GATED) {
+            const float u = sum_splits(partial + total, splits, NMAT * total, i);
+            if (saved != nullptr) {
+                store_elem<DT>(saved, i, v);
+                store_elem<DT>(saved, total + i, u);
+            }
+            store_elem<DT>(out, i, act_f32(act, v) * u);
+        } else {
+            store_elem<DT>(out, i, v);
+        }
+    }
+}
+
+template <bool GATED>
+hipError_t join(const FfnArgs& a, const float* partial, int splits, int64_t total, void* out, hipStream_t st)
+{
+    const unsigned blocks = (unsigned)std::min<int64_t>((total + 255) / 256, 16384);
+    void* const saved = GATED ? a.saved : nullptr;
+    if (a.dt == DT_F16)
+        hipLaunchKernelGGL((ffn_join_kernel<DT_F16, GATED>), dim3(blocks), dim3(256), 0, st, partial, splits, total,
+                           a.act, saved, out);
+    else
+        hipLaunchKernelGGL((ffn_join_kernel<DT_BF16, GATED>), dim3(blocks), dim3(256), 0, st, partial, splits, total,
+                           a.act, saved, out);
+    return hipGetLastError();
+}
+
+// A product in pieces where the plan and the pointers allow it.
+template <bool GATED>
+hipError_t split_product(const FfnArgs& a, const void* x, int64_t k, const QWeight& w0, const QWeight& w1, int64_t n,
+                         float* partial, void* out, hipStream_t st, bool* done)
+{
+    constexpr int NMAT = GATED ? 2 : 1;
+    FfnSplitArgs s{x, a.dt, a.M, k, n, {w0, w1}, NMAT, a.bits, a.gs, ffn_split(a.M, k, n, NMAT, a.dt), partial};
+    const uintptr_t sb = reinterpret_cast<uintptr_t>(w0.scales) | reinterpret_cast<uintptr_t>(w0.biases) |
+                         reinterpret_cast<uintptr_t>(w1.scales) | reinterpret_cast<uintptr_t>(w1.biases);
+    constexpr int64_t k2GB = int64_t(1) << 31;
+    if (s.plan.splits <= 1 || !aligned16(x) || sb % 4 != 0 || n * (k * a.bits / 8) >= k2GB ||
+        n * (k / a.gs) * 2 >= k2GB - 4 || a.M * k * 2 >= k2GB)
+        return hipSuccess;
+    hipError_t e = hipErrorInvalidValue;
+    switch (a.bits) {
+    case 2: e = launch_ffn_split_b2(s, st); break;
+    case 3: e = launch_ffn_split_b3(s, st); break;
+    case 4: e = launch_ffn_split_b4(s, st); break;
+    case 6: e = launch_ffn_split_b6(s, st); break;
+    case 8: e = launch_ffn_split_b8(s, st); break;
+    }
+    if (e != hipSuccess)
+        return e;
+    *done = true;
+    return join<GATED>(a, partial, s.plan.splits, a.M * n, out, st);
+}
+
 hipError_t gate_up(const GateUpArgs& a, hipStream_t st, bool* done)
 {
     switch (a.bits) {
@@ -72,11 +136,28 @@ size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
 } // namespace
 
-// h, and the up projection's product where the two products are separate
-// launches and the caller does not keep them.
-size_t ffn_workspace_bytes(int64_t m, int64_t f, int dt)
+FfnSplit ffn_split(int64_t m, int64_t k, int64_t n, int nmat, int dt)
 {
-    return 2 * up16((size_t)m * (size_t)f * elem_size(dt));
+    FfnSplit p{m <= 128 ? 64 : 256, 1, 0, 0};
+    if (dt == DT_F32 || m <= 16 || k % 64 != 0 || n == 0 || m * n * 4 * nmat >= (int64_t(1) << 31))
+        return p;
+    const int64_t cols = p.tile == 64 ? 256 : 128;
+    const int64_t tiles = ((m + p.tile - 1) / p.tile) * ((n * nmat + cols - 1) / cols), steps = k / 64;
+    const int64_t splits = std::min(256 / tiles, steps / 4);
+    if (splits <= 1)
+        return p;
+    p.per_split = (int)((steps + splits - 1) / splits);
+    p.splits = (int)((steps + p.per_split - 1) / p.per_split);
+    p.partial_bytes = (size_t)p.splits * (size_t)nmat * (size_t)m * (size_t)n * 4;
+    return p;
+}
+
+// h, and the up projection's product where the two products are separate
+// launches and the caller does not keep them; then one product's partial sums.
+size_t ffn_workspace_bytes(int64_t m, int64_t d, int64_t f, int dt)
+{
+    return 2 * up16((size_t)m * (size_t)f * elem_size(dt)) +
+           std::max(ffn_split(m, d, f, 2, dt).partial_bytes, ffn_split(m, f, d, 1, dt).partial_bytes);
 }
 
 hipError_t launch_ffn(const FfnArgs& a, hipStream_t st)
@@ -85,8 +166,12 @@ hipError_t launch_ffn(const FfnArgs& a, hipStream_t st)
     char* const h = static_cast<char*>(a.workspace);
     char* const g = a.saved != nullptr ? static_cast<char*>(a.saved) : h;
     char* const u = a.saved != nullptr ? g + (size_t)a.M * (size_t)a.F * elem_size(a.dt) : h + hb;
+    float* const partial = reinterpret_cast<float*>(h + 2 * hb);
     bool done = false;
-    if (a.F > 0 && a.D > 0) {
+    if (a.F > 0 && a.D > 0)
+        if (hipError_t e = split_product<true>(a, a.x, a.D, a.gate, a.up, a.F, partial, h, st, &done); e != hipSuccess)
+            return e;
+    if (a.F > 0 && a.D > 0 && !done) {
         GateUpArgs k{a.x, a.dt, a.act, a.M, a.D, a.F, a.gate, a.up, a.bits, a.gs, h, a.saved};
         if (hipError_t e = gate_up(k, st, &done); e != hipSuccess)
             return e;
@@ -101,6 +186,11 @@ hipError_t launch_ffn(const FfnArgs& a, hipStream_t st)
     }
     if (a.D == 0)
         return hipSuccess;
+    done = false;
+    if (a.F > 0)
+        if (hipError_t e = split_product<false>(a, h, a.F, a.down, a.down, a.D, partial, a.y, st, &done);
+            e != hipSuccess || done)
+            return e;
     return product(a, h, a.F, a.down, a.D, a.y, st);
 }
 

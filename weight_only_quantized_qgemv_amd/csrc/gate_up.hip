@@ -139,16 +139,71 @@ hipError_t run(const GateUpArgs& a, hipStream_t st, bool* done)
     if (a.K % gemm::BK != 0 || !dwords || a.M <= 16)
         return hipSuccess;
     *done = true;
-    if (a.M <= 64)
+    // Measured with 4-bit codes, the whole block's time. Up to 128 rows tiles of
+    // 64: 128 rows of a 2048 x 5632 block 113 us, with tiles of 256 x 128 124.
+    // 256 x 256 tiles where there are more than 128, so that half as wide ones
+    // would not fit the 256 CUs at once: 512 rows of 4096 x 14336 (224 tiles)
+    // 326 us, half as wide 355; 256 rows (112 tiles) 300 against 278. Their
+    // stages fit the LDS up to 4-bit codes.
+    if (a.M <= 128)
         return run_tiles<BITS, DT, 64, 256, 256, 1>(a, st);
     if constexpr (BITS <= 4) {
-        if (((a.M + 255) / 256) * ((a.N + 127) / 128) >= 384)
+        if (((a.M + 255) / 256) * ((a.N + 127) / 128) > 128)
             return run_tiles<BITS, DT, 256, 256, 512, 2>(a, st);
     }
     return run_tiles<BITS, DT, 256, 128, 256, 2>(a, st);
 }
 
+template <int BITS, int DT, int BM, int BN, int WMW, int NMAT>
+hipError_t run_split(const FfnSplitArgs& a, hipStream_t st)
+{
+    constexpr int NA = 3, NC = 4, NT = 256;
+    constexpr int LDS = gemm::lds_bytes<BITS, BM, BN, NT, NA, NC>();
+    static_assert(LDS <= 160 * 1024, "LDS budget");
+    const void* kern = reinterpret_cast<const void*>(
+        &gemm::qgemm_tile_kernel<BITS, DT, BM, BN, NT, WMW, NMAT, false, NA, NC, 0, true>);
+    static bool attr_set = false;   // per instantiation; set before its first launch
+    if (!attr_set) {
+        if (hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, LDS); e != hipSuccess)
+            return e;
+        attr_set = true;
+    }
+    GemmArgs g{};
+    g.x = a.x;
+    for (int t = 0; t < 2; ++t) {
+        const QWeight& w = a.w[t < NMAT ? t : 0];
+        g.wq[t] = w.wq; g.scales[t] = w.scales; g.biases[t] = w.biases;
+    }
+    g.M = (int)a.M; g.N = (int)a.N; g.K = (int)a.K; g.gs = a.gs;
+    g.x_bytes = (uint32_t)(a.M * a.K * 2);
+    g.sb_bytes = (uint32_t)((a.N * (a.K / a.gs) * 2 + 3) & ~int64_t(3));
+    g.tiles_n = (int)((a.N + BN / NMAT - 1) / (BN / NMAT));
+    g.tiles = (int)((a.M + BM - 1) / BM) * g.tiles_n;
+    g.per_xcd = (g.tiles + 7) / 8;
+    g.partial = a.partial;
+    g.per_split = a.plan.per_split;
+    hipLaunchKernelGGL((gemm::qgemm_tile_kernel<BITS, DT, BM, BN, NT, WMW, NMAT, false, NA, NC, 0, true>),
+                       dim3(g.per_xcd * 8, (unsigned)a.plan.splits), dim3(NT), LDS, st, g);
+    return hipGetLastError();
+}
+
+template <int DT> hipError_t run_split_dt(const FfnSplitArgs& a, hipStream_t st)
+{
+    if (a.plan.tile == 64)
+        return a.nmat == 2 ? run_split<QP_BITS, DT, 64, 256, 1, 2>(a, st) : run_split<QP_BITS, DT, 64, 256, 1, 1>(a, st);
+    return a.nmat == 2 ? run_split<QP_BITS, DT, 256, 128, 2, 2>(a, st) : run_split<QP_BITS, DT, 256, 128, 2, 1>(a, st);
+}
+
 } // namespace
+
+hipError_t QP_CAT(launch_ffn_split_b, QP_BITS)(const FfnSplitArgs& a, hipStream_t st)
+{
+    switch (a.dt) {
+    case DT_F16: return run_split_dt<DT_F16>(a, st);
+    case DT_BF16: return run_split_dt<DT_BF16>(a, st);
+    }
+    return hipErrorInvalidValue;
+}
 
 hipError_t QP_CAT(launch_gate_up_b, QP_BITS)(const GateUpArgs& a, hipStream_t st, bool* done)
 {

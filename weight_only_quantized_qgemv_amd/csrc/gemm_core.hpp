@@ -67,6 +67,11 @@ struct GemmArgs {
     // are kept ([M, N] each, y_bytes), or null.
     int act;
     void* saved[2];
+    // Split form: block (x, y) contracts steps y * per_split .. of its tile and
+    // stores fp32 sums to partial [y][matrix][M][N] (4 NMAT M N bytes below
+    // 2^31 a split); y, act and saved are the joining launch's.
+    float* partial;
+    int per_split;
 };
 
 namespace gemm {
@@ -253,9 +258,10 @@ template <int BITS> struct GemmCodes {
 };
 
 template <int BITS, int DT, int BM, int BN, int THREADS, int WMW, int NMAT, bool ROUTED, int NA,
-          int NC, int MODE = 0>
+          int NC, int MODE = 0, bool SPLIT = false>
 __global__ __launch_bounds__(THREADS) void qgemm_tile_kernel(GemmArgs ga)
 {
+    static_assert(!SPLIT || (!ROUTED && MODE == 0), "split form: dense affine tiles");
     static_assert(MODE == 0 || (MxFmt<MODE>::BITS == BITS && NMAT == 1 && !ROUTED),
                   "microscaled modes: dense single-matrix tiles");
     using T = MfmaTraits<DT>;
@@ -407,23 +413,25 @@ __global__ __launch_bounds__(THREADS) void qgemm_tile_kernel(GemmArgs ga)
         rsb[i] = rsb_of(NMAT == 1 ? 0 : (r / BNO), MODE == 0 && j >= BN / 64);
     }
     const uint32_t gshift = (uint32_t)__builtin_ctz((unsigned)ga.gs);
+    // Steps are counted from the block's first.
+    const int kt0 = SPLIT ? (int)blockIdx.y * ga.per_split : 0;
     auto dma_a = [&](int kt, int stage) {
 #pragma unroll
         for (int i = 0; i < A_INSTR; ++i)
             dma16(rx, a_st + stage * A_STAGE + (wave * A_INSTR + i) * 1024,
-                  a_goff[i] + (uint32_t)kt * BK * 2);
+                  a_goff[i] + (uint32_t)(kt0 + kt) * BK * 2);
     };
     auto dma_c = [&](int kt, int stage) {
 #pragma unroll
         for (int i = 0; i < C_INSTR; ++i) {
             char* dst = c_st + stage * C_STAGE + (wave * C_INSTR + i) * 1024;
-            const uint32_t off = c_goff[i] + (uint32_t)kt * CL::RB;
+            const uint32_t off = c_goff[i] + (uint32_t)(kt0 + kt) * CL::RB;
             if constexpr (CL::CS == 12)
                 dma12(rw[i], dst, off);
             else
                 dma16(rw[i], dst, off);
         }
-        const uint32_t g0 = ((uint32_t)kt * BK) >> gshift;
+        const uint32_t g0 = ((uint32_t)(kt0 + kt) * BK) >> gshift;
 #pragma unroll
         for (int i = 0; i < SB_INSTR; ++i) {
             // Rows past N: an offset past the end (reads zeros).
@@ -486,8 +494,8 @@ __global__ __launch_bounds__(THREADS) void qgemm_tile_kernel(GemmArgs ga)
     // first group: with 32-wide groups (base even) both groups of the step,
     // else the step's one group in half base & 1.
     auto load_units = [&](int kt, int stage) {
-        const uint32_t g0 = ((uint32_t)kt * BK) >> gshift;
-        const uint32_t gu = ((uint32_t)kt * BK + half * 32) >> gshift;
+        const uint32_t g0 = ((uint32_t)(kt0 + kt) * BK) >> gshift;
+        const uint32_t gu = ((uint32_t)(kt0 + kt) * BK + half * 32) >> gshift;
         if constexpr (MODE != 0) {
             // The row's scale bytes of the step sit in one aligned dword, from
             // byte (b_gbase + g0) & 3 on; the lane's unit takes byte gu - g0
@@ -593,7 +601,9 @@ __global__ __launch_bounds__(THREADS) void qgemm_tile_kernel(GemmArgs ga)
     // Prologue: the DMA of steps 1 - NC .. -1 of the loop below (activations
     // of steps 0 .. NA-2, codes / scales of steps 0 .. NC-2, in the loop's
     // order, so the loop's in-flight counts hold from its first step).
-    const int KT = K / BK;
+    int KT = K / BK;
+    if constexpr (SPLIT)
+        KT = KT - kt0 < ga.per_split ? KT - kt0 : ga.per_split;
 #pragma unroll
     for (int s = 1 - NC; s < 0; ++s) {
         if (s + NA - 1 >= 0)
@@ -656,7 +666,9 @@ __global__ __launch_bounds__(THREADS) void qgemm_tile_kernel(GemmArgs ga)
 
     // Epilogue: lane l, register r of a 32 x 32 tile holds
     // row 8 * (r / 4) + 4 * (l / 32) + r % 4, column l % 32.
-    const __amdgpu_buffer_rsrc_t ry = rsrc(ga.y, ga.y_bytes);
+    const __amdgpu_buffer_rsrc_t ry = SPLIT
+        ? rsrc(ga.partial + (size_t)blockIdx.y * NMAT * (size_t)ga.M * (size_t)N, 4u * NMAT * (uint32_t)ga.M * (uint32_t)N)
+        : rsrc(ga.y, ga.y_bytes);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         // Output row (dense) or pair (routed) of each register's tile row.
@@ -675,6 +687,16 @@ __global__ __launch_bounds__(THREADS) void qgemm_tile_kernel(GemmArgs ga)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 float v = acc[i][j][r];
+                if constexpr (SPLIT) {
+                    const uint32_t at = (orow[r] >= 0 && col < N)
+                        ? ((uint32_t)orow[r] * (uint32_t)N + (uint32_t)col) * 4 : OOB;
+                    static_for<NMAT>([&](auto MAT) {
+                        __builtin_amdgcn_raw_buffer_store_b32(
+                            __builtin_bit_cast(uint32_t, (float)acc[i][j + FNO * (int)MAT][r]), ry,
+                            at == OOB ? OOB : at + 4u * (uint32_t)MAT * (uint32_t)ga.M * (uint32_t)N, 0, 0);
+                    });
+                    continue;
+                }
                 const uint32_t off = (orow[r] >= 0 && col < N)
                     ? ((uint32_t)orow[r] * (uint32_t)N + (uint32_t)col) * 2 : OOB;
                 if constexpr (NMAT == 2 && ROUTED)

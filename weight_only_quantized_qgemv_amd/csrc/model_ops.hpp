@@ -31,7 +31,7 @@ struct FfnArgs {
     void* y;                // [M, D] of dt
     void* workspace;        // >= ffn_workspace_bytes, 16-byte aligned
 };
-size_t ffn_workspace_bytes(int64_t m, int64_t f, int dt);
+size_t ffn_workspace_bytes(int64_t m, int64_t d, int64_t f, int dt);
 hipError_t launch_ffn(const FfnArgs& a, hipStream_t stream);
 
 // h = act(gate product) * (up product) in one launch, without or with storing
@@ -45,8 +45,28 @@ struct GateUpArgs {
     void* h;                // [M, N]
     void* saved;            // [2, M, N] or null
 };
+// The block's products with the contraction in pieces, for batches whose tiles
+// are too few to fill the GPU: x [M, K] times one or two matrices of N rows, as
+// fp32 sums partial [splits][matrices][M][N] of per_split 64-wide steps each.
+struct FfnSplit {
+    int tile;               // activation rows of a tile, 64 or 256
+    int splits;             // 1: not in pieces
+    int per_split;
+    size_t partial_bytes;
+};
+FfnSplit ffn_split(int64_t m, int64_t k, int64_t n, int nmat, int dt);
+struct FfnSplitArgs {
+    const void* x;
+    int dt;
+    int64_t M, K, N;
+    QWeight w[2];
+    int nmat, bits, gs;
+    FfnSplit plan;
+    float* partial;
+};
 #define QP_GATEUP_DECL(B) \
-    hipError_t launch_gate_up_b##B(const GateUpArgs& a, hipStream_t stream, bool* done);
+    hipError_t launch_gate_up_b##B(const GateUpArgs& a, hipStream_t stream, bool* done); \
+    hipError_t launch_ffn_split_b##B(const FfnSplitArgs& a, hipStream_t stream);
 QP_GATEUP_DECL(2)
 QP_GATEUP_DECL(3)
 QP_GATEUP_DECL(4)
