@@ -98,6 +98,31 @@ def test_forward_in_pieces(m, d, f, bits, gs, dt):
     check_forward(case(m, d, f, bits, gs, dt), "gelu_tanh", "pieces")
 
 
+@pytest.mark.parametrize("dt", [F32, F16, BF16])
+@pytest.mark.parametrize("m,d,f,gs", [(1, 256, 448, 64), (12, 256, 448, 64), (40, 256, 448, 64), (150, 1120, 352, 32),
+                                      (33, 2144, 288, 32)])
+def test_forward_misaligned(m, d, f, gs, dt):
+    """Activations, scales and biases one element off every wider alignment."""
+    c = case(m, d, f, 3, gs, dt)
+    log(f"qffn misaligned: m={m} d={d} f={f} gs={gs} dt={dt}")
+
+    def off(t):
+        flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=dev())
+        flat[1:] = t.reshape(-1).to(dev())
+        return flat[1:].view(t.shape)
+
+    (y, by), (g, bg), (u, bu) = forward_ref(c, "silu")
+    ws = [(c[n][0].to(dev()), off(c[n][1]), off(c[n][2])) for n in ("gate", "up", "down")]
+    saved = off(torch.zeros((2, m, f), dtype=c["x"].dtype))
+    for kept in (None, saved):
+        out = off(torch.zeros((m, d), dtype=c["x"].dtype))
+        qp.qffn(off(c["x"]), *ws, 3, gs, act="silu", saved=kept, out=out)
+        torch.cuda.synchronize()
+        oh.check(out, y, by, "y")
+    oh.check(saved[0], g, bg, "g")
+    oh.check(saved[1], u, bu, "u")
+
+
 def backward_ref(c, saved, act):
     dt, bits, gs = c["dt"], c["bits"], c["gs"]
     Wg, Wu, Wd = (oh.dense(c[n], bits, gs) for n in ("gate", "up", "down"))

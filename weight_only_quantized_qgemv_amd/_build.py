@@ -28,7 +28,7 @@ UNITS = ([("api.cpp", "api", {}), ("quantize.hip", "quantize", {}), ("moe.hip", 
           ("ffn.hip", "ffn", {}), ("grad.hip", "grad", {}), ("embedding.hip", "embedding", {}),
           ("logits.hip", "logits", {})]
          + [("qgemv.hip", f"qgemv_b{b}", {"QP_BITS": b}) for b in BITS]
-         + [(f"{f}.hip", f"{f}_b{b}", {"QP_BITS": b}) for f in ("xgrad", "wgrad", "gate_up") for b in BITS]
+         + [(f"{f}.hip", f"{f}_b{b}", {"QP_BITS": b}) for f in ("xgrad", "wgrad", "gate_up", "ffn_any") for b in BITS]
          + [("moe_compute.hip", f"moe_b{b}_n{n}", {"QP_BITS": b, "QP_NMAT": n})
             for b in BITS for n in (1, 2)])
 

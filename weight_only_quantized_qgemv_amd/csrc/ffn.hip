@@ -43,18 +43,6 @@ hipError_t gate(const FfnArgs& a, const void* g, const void* u, void* h, hipStre
     return hipGetLastError();
 }
 
-// y = x W^T on qmatmul's kernels. The tile kernel reads activations in 16-byte
-// pieces; other alignments take the decode kernels, which test for it.
-hipError_t product(const FfnArgs& a, const void* x, int64_t k, const QWeight& w, int64_t n, void* y, hipStream_t st)
-{
-    if (k == 0)
-        return launch_fill_zero(y, a.dt, a.M * n, st);
-    GemvArgs g{x, a.dt, a.M, k, n, w.wq, w.scales, w.biases, a.bits, a.gs, y};
-    if (a.M <= 16 || a.dt == DT_F32 || !aligned16(x))
-        return launch_qgemv(g, st);
-    return launch_qgemm(g, st);
-}
-
 // The sums of a product in pieces: stored, or (gated) both products' sums
 // closed into h, and kept where a backward pass follows. Partial sums
 // [split][matrix][total].
@@ -83,13 +71,52 @@ hipError_t join(const FfnArgs& a, const float* partial, int splits, int64_t tota
 {
     const unsigned blocks = (unsigned)std::min<int64_t>((total + 255) / 256, 16384);
     void* const saved = GATED ? a.saved : nullptr;
-    if (a.dt == DT_F16)
+    if (!GATED && a.dt == DT_F32)
+        hipLaunchKernelGGL((ffn_join_kernel<DT_F32, false>), dim3(blocks), dim3(256), 0, st, partial, splits, total,
+                           a.act, saved, out);
+    else if (a.dt == DT_F16)
         hipLaunchKernelGGL((ffn_join_kernel<DT_F16, GATED>), dim3(blocks), dim3(256), 0, st, partial, splits, total,
                            a.act, saved, out);
     else
         hipLaunchKernelGGL((ffn_join_kernel<DT_BF16, GATED>), dim3(blocks), dim3(256), 0, st, partial, splits, total,
                            a.act, saved, out);
     return hipGetLastError();
+}
+
+// Whether ffn_any's kernel takes a product: the decode kernels, which qmatmul
+// runs such shapes on, stream the weights once for every few rows (fp32, 4096 x
+// 14336, 4-bit, the three products: 1 row 133 us against 165, 2 rows 227 against
+// 165, 32 rows 3890 against 174).
+bool any_product(const FfnArgs& a, const void* x, int64_t k, const QWeight& w)
+{
+    if (a.dt == DT_F32)
+        return a.M > 1;
+    const uintptr_t sb = reinterpret_cast<uintptr_t>(w.scales) | reinterpret_cast<uintptr_t>(w.biases);
+    return a.M > 16 && (k % 64 != 0 || !aligned16(x) || sb % 4 != 0);
+}
+
+// y = x W^T: ffn_any's kernel, or qmatmul's.
+hipError_t product(const FfnArgs& a, const void* x, int64_t k, const QWeight& w, int64_t n, float* partial, void* y,
+                   hipStream_t st)
+{
+    if (k == 0)
+        return launch_fill_zero(y, a.dt, a.M * n, st);
+    if (any_product(a, x, k, w)) {
+        FfnAnyArgs g{x, a.dt, a.M, k, n, w, a.gs, ffn_any_plan(a.M, k, n), partial, y};
+        hipError_t e = hipErrorInvalidValue;
+        switch (a.bits) {
+        case 2: e = launch_ffn_any_b2(g, st); break;
+        case 3: e = launch_ffn_any_b3(g, st); break;
+        case 4: e = launch_ffn_any_b4(g, st); break;
+        case 6: e = launch_ffn_any_b6(g, st); break;
+        case 8: e = launch_ffn_any_b8(g, st); break;
+        }
+        if (e != hipSuccess || g.plan.splits == 1)
+            return e;
+        return join<false>(a, partial, g.plan.splits, a.M * n, y, st);
+    }
+    GemvArgs g{x, a.dt, a.M, k, n, w.wq, w.scales, w.biases, a.bits, a.gs, y};
+    return a.M <= 16 ? launch_qgemv(g, st) : launch_qgemm(g, st);
 }
 
 // A product in pieces where the plan and the pointers allow it.
@@ -152,12 +179,27 @@ FfnSplit ffn_split(int64_t m, int64_t k, int64_t n, int nmat, int dt)
     return p;
 }
 
+FfnSplit ffn_any_plan(int64_t m, int64_t k, int64_t n)
+{
+    // Pieces of at least eight steps until there are about two blocks a CU.
+    FfnSplit p{m <= 32 ? 32 : m <= 64 ? 64 : 128, 1, (int)(k / 32), 0};
+    if (m == 0 || n == 0 || k == 0)
+        return p;
+    const int64_t tiles = ((m + p.tile - 1) / p.tile) * ((n + 127) / 128), steps = k / 32;
+    const int64_t splits = std::clamp<int64_t>(std::min(512 / tiles, steps / 8), 1, 64);
+    p.per_split = (int)((steps + splits - 1) / splits);
+    p.splits = (int)((steps + p.per_split - 1) / p.per_split);
+    p.partial_bytes = p.splits > 1 ? (size_t)p.splits * (size_t)m * (size_t)n * 4 : 0;
+    return p;
+}
+
 // h, and the up projection's product where the two products are separate
 // launches and the caller does not keep them; then one product's partial sums.
 size_t ffn_workspace_bytes(int64_t m, int64_t d, int64_t f, int dt)
 {
     return 2 * up16((size_t)m * (size_t)f * elem_size(dt)) +
-           std::max(ffn_split(m, d, f, 2, dt).partial_bytes, ffn_split(m, f, d, 1, dt).partial_bytes);
+           std::max(std::max(ffn_split(m, d, f, 2, dt).partial_bytes, ffn_split(m, f, d, 1, dt).partial_bytes),
+                    std::max(ffn_any_plan(m, d, f).partial_bytes, ffn_any_plan(m, f, d).partial_bytes));
 }
 
 hipError_t launch_ffn(const FfnArgs& a, hipStream_t st)
@@ -177,9 +219,9 @@ hipError_t launch_ffn(const FfnArgs& a, hipStream_t st)
             return e;
     }
     if (a.F > 0 && !done) {
-        if (hipError_t e = product(a, a.x, a.D, a.gate, a.F, g, st); e != hipSuccess)
+        if (hipError_t e = product(a, a.x, a.D, a.gate, a.F, partial, g, st); e != hipSuccess)
             return e;
-        if (hipError_t e = product(a, a.x, a.D, a.up, a.F, u, st); e != hipSuccess)
+        if (hipError_t e = product(a, a.x, a.D, a.up, a.F, partial, u, st); e != hipSuccess)
             return e;
         if (hipError_t e = gate(a, g, u, h, st); e != hipSuccess)
             return e;
@@ -191,7 +233,7 @@ hipError_t launch_ffn(const FfnArgs& a, hipStream_t st)
         if (hipError_t e = split_product<false>(a, h, a.F, a.down, a.down, a.D, partial, a.y, st, &done);
             e != hipSuccess || done)
             return e;
-    return product(a, h, a.F, a.down, a.D, a.y, st);
+    return product(a, h, a.F, a.down, a.D, partial, a.y, st);
 }
 
 } // namespace qp

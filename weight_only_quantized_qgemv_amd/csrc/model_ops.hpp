@@ -49,9 +49,9 @@ struct GateUpArgs {
 // are too few to fill the GPU: x [M, K] times one or two matrices of N rows, as
 // fp32 sums partial [splits][matrices][M][N] of per_split 64-wide steps each.
 struct FfnSplit {
-    int tile;               // activation rows of a tile, 64 or 256
+    int tile;               // activation rows of a tile
     int splits;             // 1: not in pieces
-    int per_split;
+    int per_split;          // steps of a piece
     size_t partial_bytes;
 };
 FfnSplit ffn_split(int64_t m, int64_t k, int64_t n, int nmat, int dt);
@@ -64,7 +64,21 @@ struct FfnSplitArgs {
     FfnSplit plan;
     float* partial;
 };
+// y = x W^T for any type, size and alignment (ffn_any.hip), in pieces of 32-wide
+// steps where the plan asks for it.
+FfnSplit ffn_any_plan(int64_t m, int64_t k, int64_t n);
+struct FfnAnyArgs {
+    const void* x;
+    int dt;
+    int64_t M, K, N;
+    QWeight w;
+    int gs;
+    FfnSplit plan;
+    float* partial;
+    void* y;
+};
 #define QP_GATEUP_DECL(B) \
+    hipError_t launch_ffn_any_b##B(const FfnAnyArgs& a, hipStream_t stream); \
     hipError_t launch_gate_up_b##B(const GateUpArgs& a, hipStream_t stream, bool* done); \
     hipError_t launch_ffn_split_b##B(const FfnSplitArgs& a, hipStream_t stream);
 QP_GATEUP_DECL(2)
