@@ -70,20 +70,43 @@ hipError_t QP_CAT(launch_xgrad_b, QP_BITS)(const XgradArgs& a, const GradPlan& p
 }
 
 #if QP_BITS == 4
+// The plan takes the least of an estimate, in us, over the tiles and the pieces
+// of the contraction: rounds of resident blocks times a piece's steps, the
+// partial sums' way out and back (8 TB/s: mostly caches), a launch for their
+// sum, and what a block costs besides its steps. Measured against it, 4-bit,
+// bf16, contraction 14336 to 4096 columns: 64 rows tile 64 27 us, 128 32, 256
+// 41; 128 rows 40, 36.6, 44; 1024 rows 218, 167, 131; contraction 4096, 512
+// rows: 49, 37.8, 43.7.
 GradPlan xgrad_plan(int64_t m, int64_t n, int64_t k, int nmat, bool tile_kernels)
 {
-    // Pieces of the contraction until there are about two blocks a CU, none
-    // shorter than four steps (77 rows of a 1024 x 2816 block's backward: 55.7 us
-    // at eight, 50.8 at four, 56.9 at two).
+    struct Tile {
+        int tile;
+        int64_t bm, bn, step, resident;
+        double us, fixed;
+    };
+    constexpr Tile kTiles[] = {{1, 256, 256, gradtile::STEP, 256, 1.25, 12.0}, {2, 128, 128, gradtile::STEP, 512, 1.3, 3.0},
+                               {3, 64, 128, gradtile::STEP, 512, 0.95, 2.0}, {0, XG_BM, XG_BK, XG_N, 512, 4.0, 3.0}};
     GradPlan p{};
-    p.tile = !tile_kernels ? 0 : m > 128 ? 1 : m > 64 ? 2 : 3;
-    const int64_t bm = p.tile == 1 ? 256 : p.tile == 3 ? 64 : 128, bn = p.tile == 1 ? 256 : 128;
-    const int64_t step = p.tile == 0 ? XG_N : gradtile::STEP, want = p.tile == 1 ? 256 : 512;
-    const int64_t tiles = std::max<int64_t>(((m + bm - 1) / bm) * ((k + bn - 1) / bn), 1);
-    const int64_t steps = nmat * ((n + step - 1) / step);
-    const int64_t splits = std::clamp<int64_t>(std::min(want / tiles, steps / 4), 1, 64);
-    p.per_split = std::max<int64_t>((steps + splits - 1) / splits, 1);
-    p.splits = (int)std::max<int64_t>((steps + p.per_split - 1) / p.per_split, 1);
+    double best = -1.0;
+    for (const Tile& t : kTiles) {
+        if ((t.tile != 0) != tile_kernels)
+            continue;
+        const int64_t tiles = std::max<int64_t>(((m + t.bm - 1) / t.bm) * ((k + t.bn - 1) / t.bn), 1);
+        const int64_t steps = nmat * ((n + t.step - 1) / t.step);
+        for (int64_t want = 1; want <= 64 && (want == 1 || 4 * want <= steps); ++want) {
+            const int64_t per = std::max<int64_t>((steps + want - 1) / want, 1);
+            const int64_t splits = std::max<int64_t>((steps + per - 1) / per, 1);
+            double us = (double)((tiles * splits + t.resident - 1) / t.resident) * (double)per * t.us + t.fixed;
+            if (splits > 1)
+                us += 4.0 + (double)splits * (double)m * (double)k * 8.0 / 8e6;
+            if (best < 0.0 || us < best) {
+                best = us;
+                p.tile = t.tile;
+                p.per_split = per;
+                p.splits = (int)splits;
+            }
+        }
+    }
     p.partial_bytes = p.splits > 1 ? (size_t)p.splits * (size_t)m * (size_t)k * 4 : 0;
     return p;
 }
