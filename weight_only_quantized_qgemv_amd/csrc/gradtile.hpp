@@ -107,6 +107,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const char* p, ui
                 (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes));
 }
 
+// A scheduling barrier's mask: everything but memory loads may cross it.
+constexpr int kNotLoads = 0x38F;
+
 // A step's end: at most `VM` of this wave's loads in flight, its LDS accesses
 // done, then the block barrier (bare, with compiler fences around it).
 template <int VM> __device__ __forceinline__ void step_barrier()
@@ -165,14 +168,15 @@ __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPla
         a_n[i] = 8 * ((lane & 7) ^ turn_swz(r));
         a_off[i] = (uint32_t)r < a_rows ? (uint32_t)r * arow + (uint32_t)a_n[i] * 2 : OOB;
     }
-    auto dma_a = [&](int step, int stage) {
+    // DMA instructions from .. to - 1 of a step's.
+    auto dma_a = [&](int step, int stage, int from, int to) {
         const int p = step >= steps1 ? 1 : 0;
         const int n0 = (step - p * steps1) * STEP;
         // The range ends after the last row's N values, in whole chunks.
         const __amdgpu_buffer_rsrc_t ra = rsrc(static_cast<const char*>(a.dy[p]) + m0 * a.dy_stride * 2,
                                                (a_rows - 1) * arow + ((uint32_t)a.N + 7) / 8 * 16);
 #pragma unroll
-        for (int i = 0; i < A_INSTR; ++i) {
+        for (int i = from; i < to; ++i) {
             const uint32_t off = n0 + a_n[i] < (int)a.N && step < hi ? a_off[i] + (uint32_t)n0 * 2 : OOB;
             dma16(ra, a_st + stage * A_STAGE + (wave * A_INSTR + i) * 1024, off);
         }
@@ -192,7 +196,8 @@ __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPla
     };
     constexpr int W_LOADS = 4 * (BITS == 8 ? 1 : NW) + 8;
     Raw raw[2];
-    auto load_w = [&](int step, Raw& r) {
+    // Rows from .. to - 1 of a step's block.
+    auto load_w = [&](int step, Raw& r, int from, int to) {
         const int p = step >= steps1 ? 1 : 0;
         const int n0 = (step - p * steps1) * STEP;
         int64_t left = step < hi ? a.N - n0 : 0;             // rows past the step's read zeros
@@ -204,7 +209,7 @@ __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPla
         const __amdgpu_buffer_rsrc_t rb =
             rsrc(static_cast<const char*>(a.w[p].biases) + (int64_t)n0 * grow, rows * grow);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = from; i < to; ++i) {
             if constexpr (BITS == 8) {
                 const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rw, w_off + (uint32_t)i * wrow, 0, 0));
                 r.w[i][0] = v[0];
@@ -239,10 +244,10 @@ __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPla
     frag_offsets(lane, wm * WM, fa);
     frag_offsets(lane, wn * WN, fb);
 
-    load_w(lo, raw[0]);
-    load_w(lo + 1, raw[1]);
-    dma_a(lo, 0);
-    dma_a(lo + 1, 1);
+    load_w(lo, raw[0], 0, 4);
+    load_w(lo + 1, raw[1], 0, 4);
+    dma_a(lo, 0, 0, A_INSTR);
+    dma_a(lo + 1, 1, 0, A_INSTR);
     {
         uint32_t p01[8], p23[8];
         dequant2(raw[0], 0, p01);
@@ -257,19 +262,25 @@ __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPla
     // is dequantized into the other stage and that of step kt + 2 is loaded.
     auto run_step = [&](int kt, int a_cur, auto PP) {
         constexpr int P = decltype(PP)::value;
-        // The step's end leaves this step's loads in flight, and no older ones:
-        // the DMA of step kt + 1 is there. (Waiting for the weight loads too
-        // put a memory latency into every step.)
-        load_w(kt + 2, raw[P]);
-        __builtin_amdgcn_sched_barrier(0);
-        dma_a(kt + 2, a_cur + 2 >= 3 ? a_cur - 1 : a_cur + 2);
-        __builtin_amdgcn_sched_barrier(0);
         const char* as = a_st + a_cur * A_STAGE;
         const char* bs = b_st + P * B_STAGE;
         char* bn = b_st + (1 - P) * B_STAGE;
+        const int a_new = a_cur + 2 >= 3 ? a_cur - 1 : a_cur + 2;
         uint32_t p01[8], p23[8];
         static_for<4>([&](auto KK) {
             constexpr int kk = decltype(KK)::value;
+            // The step's loads a share a kk (only loads are held there): all at
+            // its start, they keep the matrix instructions waiting until the
+            // address units have taken them. The step's end leaves them in
+            // flight, and no older ones: the DMA of step kt + 1 is there.
+            // (Waiting for the weight loads too put a memory latency into every
+            // step.)
+            __builtin_amdgcn_sched_barrier(kNotLoads);
+            if constexpr (kk < 2)
+                load_w(kt + 2, raw[P], 2 * kk, 2 * kk + 2);
+            else
+                dma_a(kt + 2, a_new, (kk - 2) * A_INSTR / 2, (kk - 1) * A_INSTR / 2);
+            __builtin_amdgcn_sched_barrier(kNotLoads);
             frag_t af[FM], bf[FN];
 #pragma unroll
             for (int i = 0; i < FM; ++i)
