@@ -19,10 +19,11 @@
 //  - steps of 64 contraction elements; two LDS stages of every turned operand,
 //    whose raw loads run two steps ahead in registers; the activation operand
 //    of dx, contiguous as it is, comes by DMA three stages deep.
-// Both are bound by the work beside the matrix instructions, which are busy 54
-// to 60% of the time: a step of 256 x 256 outputs has 2048 cycles of them on
-// each SIMD and takes about 2800. 14336 x 4096, 4-bit, bf16, 2048 / 4096 / 8192
-// rows: dx 240 / 419 / 845 us, dW 237 / 427 / 825 us (1004 to 1166 TFLOP/s).
+// Both are bound by the work beside the matrix instructions, which are busy 60
+// to 62% of the time: a step of 256 x 256 outputs has 2048 cycles of them on
+// each SIMD (and, with eight waves, as many of LDS reads and writes). 14336 x
+// 4096, 4-bit, bf16, 2048 / 4096 / 8192 rows: dx 231 / 403 / 822 us, dW 237 / 427
+// / 825 us (998 to 1194 TFLOP/s).
 #pragma once
 
 #include "codes8.hpp"
@@ -271,7 +272,8 @@ __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPla
             constexpr int kk = decltype(KK)::value;
             // The step's loads a share a kk (only loads are held there): all at
             // its start, they keep the matrix instructions waiting until the
-            // address units have taken them. The step's end leaves them in
+            // address units have taken them (the backward pass of a 4096 x 14336
+            // block at 2048 rows 1457 us, now 1416). The step's end leaves them in
             // flight, and no older ones: the DMA of step kt + 1 is there.
             // (Waiting for the weight loads too put a memory latency into every
             // step.)
