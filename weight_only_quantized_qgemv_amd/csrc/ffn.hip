@@ -185,16 +185,27 @@ FfnSplit ffn_split(int64_t m, int64_t k, int64_t n, int nmat, int dt)
 
 FfnSplit ffn_any_plan(int64_t m, int64_t k, int64_t n)
 {
-    // Pieces of at least eight steps until there are about two blocks a CU. The
-    // tile that the rows fit: 33 rows of 4096 x 14336, 4-bit, fp32, 256 us with
-    // tiles of 64, 459 with tiles of 128.
+    // The tile that the rows fit: 33 rows of 4096 x 14336, 4-bit, fp32, 256 us with
+    // tiles of 64, 459 with tiles of 128. The pieces that an estimate, in us,
+    // finds quickest: rounds of two blocks a CU (one alone takes about half the
+    // time a step), the partial sums' way out and back, and a launch for their sum.
     FfnSplit p{m <= 32 ? 32 : m <= 64 ? 64 : 128, 1, (int)(k / 32), 0};
     if (m == 0 || n == 0 || k == 0)
         return p;
     const int64_t tiles = ((m + p.tile - 1) / p.tile) * ((n + 127) / 128), steps = k / 32;
-    const int64_t splits = std::clamp<int64_t>(std::min(512 / tiles, steps / 8), 1, 64);
-    p.per_split = (int)((steps + splits - 1) / splits);
-    p.splits = (int)((steps + p.per_split - 1) / p.per_split);
+    const double step_us = p.tile == 32 ? 1.5 : p.tile == 64 ? 2.4 : 4.4;
+    double best = -1.0;
+    for (int64_t want = 1; want <= 64 && (want == 1 || 2 * want <= steps); ++want) {
+        const int64_t per = (steps + want - 1) / want, splits = (steps + per - 1) / per, blocks = tiles * splits;
+        double us = (blocks <= 256 ? 0.55 : (double)((blocks + 511) / 512)) * (double)per * step_us;
+        if (splits > 1)
+            us += 4.0 + (double)splits * (double)m * (double)n * 8.0 / 8e6;
+        if (best < 0.0 || us < best) {
+            best = us;
+            p.per_split = (int)per;
+            p.splits = (int)splits;
+        }
+    }
     p.partial_bytes = p.splits > 1 ? (size_t)p.splits * (size_t)m * (size_t)n * 4 : 0;
     return p;
 }
