@@ -14,6 +14,8 @@ namespace qp {
 namespace {
 
 inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+size_t elem_size(int dt) { return dt == DT_F32 ? 4 : 2; }
+size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
 // h[i] = act(g[i]) u[i], rounded once; h may be g's own memory.
 template <int DT>
@@ -119,19 +121,68 @@ hipError_t product(const FfnArgs& a, const void* x, int64_t k, const QWeight& w,
     return a.M <= 16 ? launch_qgemv(g, st) : launch_qgemm(g, st);
 }
 
+// Rows of 16-bit elements copied to longer rows, zeros behind: array blockIdx.y,
+// two elements a thread.
+struct PadArgs {
+    const uint16_t* in[5];
+    uint32_t* out[5];
+    int64_t rows[5];
+    uint32_t cols[5], pairs[5];   // elements in a row, pairs in an output row
+};
+__global__ __launch_bounds__(256) void ffn_pad_kernel(PadArgs a)
+{
+    const int j = (int)blockIdx.y;
+    const uint32_t pairs = a.pairs[j], cols = a.cols[j];
+    const int64_t total = a.rows[j] * pairs;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const uint32_t r = (uint32_t)i / pairs, c = 2 * ((uint32_t)i - r * pairs);   // total is below 2^30
+        const uint16_t* const p = a.in[j] + (int64_t)r * cols + c;
+        const uint32_t lo = c < cols ? p[0] : 0u, hi = c + 1 < cols ? p[1] : 0u;
+        a.out[j][i] = lo | (hi << 16);
+    }
+}
+
 // A product in pieces where the plan and the pointers allow it.
 template <bool GATED>
 hipError_t split_product(const FfnArgs& a, const void* x, int64_t k, const QWeight& w0, const QWeight& w1, int64_t n,
                          float* partial, void* out, hipStream_t st, bool* done)
 {
     constexpr int NMAT = GATED ? 2 : 1;
-    FfnSplitArgs s{x, a.dt, a.M, k, n, {w0, w1}, NMAT, a.bits, a.gs, ffn_split(a.M, k, n, NMAT, a.dt), partial};
+    FfnSplitArgs s{x, a.dt, a.M, k, n, k, {w0, w1}, NMAT, a.bits, a.gs, ffn_split(a.M, k, n, NMAT, a.dt), partial};
+    const FfnSplit& p = s.plan;
     const uintptr_t sb = reinterpret_cast<uintptr_t>(w0.scales) | reinterpret_cast<uintptr_t>(w0.biases) |
                          reinterpret_cast<uintptr_t>(w1.scales) | reinterpret_cast<uintptr_t>(w1.biases);
+    const int64_t kk = p.kp > 0 ? p.kp : k, groups = kk / a.gs;
     constexpr int64_t k2GB = int64_t(1) << 31;
-    if (s.plan.splits <= 1 || !aligned16(x) || sb % 4 != 0 || n * (k * a.bits / 8) >= k2GB ||
-        n * (k / a.gs) * 2 >= k2GB - 4 || a.M * k * 2 >= k2GB)
+    if (p.per_split == 0 || (p.kp == 0 && (!aligned16(x) || sb % 4 != 0)) || n * (k * a.bits / 8) >= k2GB ||
+        n * groups * 2 >= k2GB - 4 || a.M * kk * 2 >= k2GB)
         return hipSuccess;
+    if (p.kp > 0) {
+        PadArgs pad{};
+        char* to = reinterpret_cast<char*>(partial) + up16(p.partial_bytes);
+        int arrays = 0;
+        auto add = [&](const void* from, int64_t rows, int64_t cols, int64_t cols_p) {
+            pad.in[arrays] = static_cast<const uint16_t*>(from);
+            pad.out[arrays] = reinterpret_cast<uint32_t*>(to);
+            pad.rows[arrays] = rows;
+            pad.cols[arrays] = (uint32_t)cols;
+            pad.pairs[arrays++] = (uint32_t)(cols_p / 2);
+            const void* const at = to;
+            to += up16((size_t)rows * (size_t)cols_p * 2);
+            return at;
+        };
+        s.x = add(x, a.M, k, kk);
+        s.K = kk;
+        for (int t = 0; t < NMAT; ++t) {
+            s.w[t].scales = add(s.w[t].scales, n, k / a.gs, groups);
+            s.w[t].biases = add(s.w[t].biases, n, k / a.gs, groups);
+        }
+        const int64_t most = std::max(a.M * kk, n * groups) / 2;
+        hipLaunchKernelGGL(ffn_pad_kernel, dim3((unsigned)std::min<int64_t>((most + 255) / 256, 4096), (unsigned)arrays),
+                           dim3(256), 0, st, pad);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess)
+            return e;
+    }
     hipError_t e = hipErrorInvalidValue;
     switch (a.bits) {
     case 2: e = launch_ffn_split_b2(s, st); break;
@@ -143,7 +194,7 @@ hipError_t split_product(const FfnArgs& a, const void* x, int64_t k, const QWeig
     if (e != hipSuccess)
         return e;
     *done = true;
-    return join<GATED>(a, partial, s.plan.splits, a.M * n, out, st);
+    return join<GATED>(a, partial, p.splits, a.M * n, out, st);
 }
 
 hipError_t gate_up(const GateUpArgs& a, hipStream_t st, bool* done)
@@ -158,28 +209,35 @@ hipError_t gate_up(const GateUpArgs& a, hipStream_t st, bool* done)
     return hipErrorInvalidValue;
 }
 
-size_t elem_size(int dt) { return dt == DT_F32 ? 4 : 2; }
-size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
-
 } // namespace
 
 // Tiles of 64 x 256 up to 128 rows, 256 x 128 beyond, and as many pieces as fill
 // the 256 CUs once, at least four steps each. 4096 x 14336, 4-bit, the whole
 // block, without pieces and with: 64 rows 254 and 74 us, 256 rows 277 and 126, 512
 // rows 354 and 210. Filling the CUs twice: 64 rows 83 us.
+// A contraction of whole 32-wide groups but not whole 64-wide steps (groups of 32
+// then) is filled up with zeros: x, the scales and the biases in a copy, the codes
+// where they lie, the next row's times zero (5600 x 2080, 4-bit, bf16, 253 rows 222
+// us on ffn_any's kernel, 83 so; 2048 rows 1354 and 297). Below 64 the weights'
+// roundings do not average out, and ffn_any's kernel takes the product.
 FfnSplit ffn_split(int64_t m, int64_t k, int64_t n, int nmat, int dt)
 {
-    FfnSplit p{m <= 128 ? 64 : 256, 1, 0, 0};
-    if (dt == DT_F32 || m <= 16 || k % 64 != 0 || n == 0 || m * n * 4 * nmat >= (int64_t(1) << 31))
+    FfnSplit p{m <= 128 ? 64 : 256, 1, 0, 0, 0, 0};
+    const bool pad = k % 64 == 32 && k > 64;
+    if (dt == DT_F32 || m <= 16 || (k % 64 != 0 && !pad) || k == 0 || n == 0 || m * n * 4 * nmat >= (int64_t(1) << 31))
         return p;
     const int64_t cols = p.tile == 64 ? 256 : 128;
-    const int64_t tiles = ((m + p.tile - 1) / p.tile) * ((n * nmat + cols - 1) / cols), steps = k / 64;
+    const int64_t tiles = ((m + p.tile - 1) / p.tile) * ((n * nmat + cols - 1) / cols), steps = (k + 63) / 64;
     const int64_t splits = std::min(256 / tiles, steps / 4);
-    if (splits <= 1)
+    if (splits <= 1 && !pad)
         return p;
-    p.per_split = (int)((steps + splits - 1) / splits);
+    p.per_split = (int)((steps + std::max<int64_t>(splits, 1) - 1) / std::max<int64_t>(splits, 1));
     p.splits = (int)((steps + p.per_split - 1) / p.per_split);
     p.partial_bytes = (size_t)p.splits * (size_t)nmat * (size_t)m * (size_t)n * 4;
+    if (pad) {
+        p.kp = k + 32;
+        p.pad_bytes = up16((size_t)m * (size_t)p.kp * 2) + 2 * (size_t)nmat * up16((size_t)n * (size_t)(p.kp / 32) * 2);
+    }
     return p;
 }
 
@@ -189,7 +247,7 @@ FfnSplit ffn_any_plan(int64_t m, int64_t k, int64_t n)
     // tiles of 64, 459 with tiles of 128. The pieces that an estimate, in us,
     // finds quickest: rounds of two blocks a CU (one alone takes about half the
     // time a step), the partial sums' way out and back, and a launch for their sum.
-    FfnSplit p{m <= 32 ? 32 : m <= 64 ? 64 : 128, 1, (int)(k / 32), 0};
+    FfnSplit p{m <= 32 ? 32 : m <= 64 ? 64 : 128, 1, (int)(k / 32), 0, 0, 0};
     if (m == 0 || n == 0 || k == 0)
         return p;
     const int64_t tiles = ((m + p.tile - 1) / p.tile) * ((n + 127) / 128), steps = k / 32;
@@ -211,11 +269,13 @@ FfnSplit ffn_any_plan(int64_t m, int64_t k, int64_t n)
 }
 
 // h, and the up projection's product where the two products are separate
-// launches and the caller does not keep them; then one product's partial sums.
+// launches and the caller does not keep them; then one product's partial sums
+// and filled-up operands.
 size_t ffn_workspace_bytes(int64_t m, int64_t d, int64_t f, int dt)
 {
+    auto bytes = [](const FfnSplit& p) { return up16(p.partial_bytes) + p.pad_bytes; };
     return 2 * up16((size_t)m * (size_t)f * elem_size(dt)) +
-           std::max(std::max(ffn_split(m, d, f, 2, dt).partial_bytes, ffn_split(m, f, d, 1, dt).partial_bytes),
+           std::max(std::max(bytes(ffn_split(m, d, f, 2, dt)), bytes(ffn_split(m, f, d, 1, dt))),
                     std::max(ffn_any_plan(m, d, f).partial_bytes, ffn_any_plan(m, f, d).partial_bytes));
 }
 

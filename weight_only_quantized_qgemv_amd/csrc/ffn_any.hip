@@ -1,6 +1,6 @@
 // ffn_any.hip — the gated block's products for what the other kernels do not
-// take: fp32 activations of more than a few rows, and 16-bit ones whose rows
-// are not whole 64-wide steps or 16-byte aligned. y = x W^T on the fp32 32x32x2
+// take: fp32 activations of more than one row, and 16-bit ones of more than 16
+// rows that are not 16-byte aligned or contract over 32. y = x W^T on the fp32 32x32x2
 // matrix instruction, any size and alignment, nothing rounded before y.
 // Compiled once per bit width (QP_BITS).
 #include <algorithm>

@@ -182,6 +182,7 @@ hipError_t run_split(const FfnSplitArgs& a, hipStream_t st)
     g.per_xcd = (g.tiles + 7) / 8;
     g.partial = a.partial;
     g.per_split = a.plan.per_split;
+    g.wk = (int)a.wk;
     hipLaunchKernelGGL((gemm::qgemm_tile_kernel<BITS, DT, BM, BN, NT, WMW, NMAT, false, NA, NC, 0, true>),
                        dim3(g.per_xcd * 8, (unsigned)a.plan.splits), dim3(NT), LDS, st, g);
     return hipGetLastError();

@@ -70,8 +70,10 @@ struct GemmArgs {
     // Split form: block (x, y) contracts steps y * per_split .. of its tile and
     // stores fp32 sums to partial [y][matrix][M][N] (4 NMAT M N bytes below
     // 2^31 a split); y, act and saved are the joining launch's.
+    // A code row is wk codes long, K or less: past it, x and the scales and
+    // biases hold zeros.
     float* partial;
-    int per_split;
+    int per_split, wk;
 };
 
 namespace gemm {
@@ -305,7 +307,7 @@ __global__ __launch_bounds__(THREADS) void qgemm_tile_kernel(GemmArgs ga)
 
     const int K = ga.K, N = ga.N;
     const uint32_t xrow_bytes = (uint32_t)K * 2;
-    const uint32_t wrow_bytes = (uint32_t)K * BITS / 8;
+    const uint32_t wrow_bytes = (uint32_t)(SPLIT ? ga.wk : K) * BITS / 8;
     const uint32_t groups = (uint32_t)(K / ga.gs);
 
     // Tile of this block, XCD by XCD. The routed form is persistent: its

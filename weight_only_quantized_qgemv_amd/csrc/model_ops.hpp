@@ -51,14 +51,16 @@ struct GateUpArgs {
 struct FfnSplit {
     int tile;               // activation rows of a tile
     int splits;             // 1: not in pieces
-    int per_split;          // steps of a piece
+    int per_split;          // steps of a piece (ffn_split: 0 where the product is another path's)
     size_t partial_bytes;
+    int64_t kp;             // ffn_split: the contraction filled up to whole 64-wide steps, 0: as it is
+    size_t pad_bytes;       // and what the filled-up x, scales and biases take
 };
 FfnSplit ffn_split(int64_t m, int64_t k, int64_t n, int nmat, int dt);
 struct FfnSplitArgs {
     const void* x;
     int dt;
-    int64_t M, K, N;
+    int64_t M, K, N, wk;    // codes in a row of the weights: K, or less (gemm_core.hpp)
     QWeight w[2];
     int nmat, bits, gs;
     FfnSplit plan;
