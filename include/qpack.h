@@ -68,7 +68,7 @@ typedef QP_ENUM(qp_status) {
     QP_ERR_DTYPE_MISMATCH = 3, /* activation dtype != scales dtype */
     QP_ERR_SHAPE = 4,          /* K % group_size != 0, K*bits % 32 != 0, gate/up mismatch */
     QP_ERR_ALIGN = 5,          /* a pointer not aligned to its element size */
-    QP_ERR_WORKSPACE = 6,      /* MoE workspace too small */
+    QP_ERR_WORKSPACE = 6,      /* workspace too small */
     QP_ERR_HIP = 7             /* a HIP launch failed */
 } qp_status;
 
