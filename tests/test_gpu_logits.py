@@ -171,3 +171,28 @@ def test_long_history_and_offsets_are_held_inside():
     wild = torch.tensor([-50, 15000, n + 1000], dtype=torch.int32)
     assert oh.same_bits(got, qp.qlogits_adjust(z.to(dev()), history=h.to(dev()), offsets=wild.to(dev()),
                                                frequency=freq.to(dev())))
+
+
+def test_far_offsets_are_held_inside():
+    """Starts and ends near the ends of 32 bits, of tokens and of biases: a row whose offsets
+    leave nothing inside is an empty one, and a start below zero is zero."""
+    v, n, top = 600, 900, 2 ** 31 - 1
+    g = oh.rng(6)
+    z = torch.randn((6, v), generator=g)
+    h = torch.randint(0, v, (n,), generator=g).to(torch.int32)
+    # Offsets of row r are off[r] and off[r + 1].
+    off = [top, top - 5, top - 1000, -2 ** 31, 40, top, top - 511]
+    cut = [(min(max(a, 0), n), min(max(b, 0), n)) for a, b in zip(off, off[1:])]
+    hists = [h[a:b].tolist() for a, b in cut]
+    assert [len(x) for x in hists] == [0, 0, 0, 40, 860, 0]
+    rep = f32([1.1, 1.2, 1.3, 1.4, 1.5, 1.6])
+    bias = torch.randn(n, generator=g)
+    biases = [list(zip(h[a:b].tolist(), bias[a:b].tolist())) for a, b in cut]
+    offs = torch.tensor(off, dtype=torch.int32).to(dev())
+    log("logits: offsets near the ends of 32 bits")
+    got = qp.qlogits_adjust(z.to(dev()), history=h.to(dev()), offsets=offs,
+                            prompt_lens=torch.tensor([top, -2 ** 31, 0, 7, top, 5], dtype=torch.int32).to(dev()),
+                            repetition=torch.tensor(rep).to(dev()), frequency=torch.tensor([0.25] * 6).to(dev()),
+                            bias=(h.to(dev()), bias.to(dev()), offs))
+    ref, mag = reference(z, hists, [top, 0, 0, 7, top, 5], rep, [0.25] * 6, [0.0] * 6, biases, None)
+    compare(got, ref, mag, F32, "far offsets")

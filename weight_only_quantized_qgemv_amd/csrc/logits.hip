@@ -19,6 +19,7 @@
 
 #include "common.hpp"
 #include "model_ops.hpp"
+#include "span.hpp"
 
 namespace qp {
 
@@ -68,31 +69,27 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a, int tile
     const float rep = a.repetition != nullptr ? a.repetition[row] : 1.0f;
     const float freq = a.frequency != nullptr ? a.frequency[row] : 0.0f;
     const float pres = a.presence != nullptr ? a.presence[row] : 0.0f;
-    int lo = 0, hi = 0, b0 = 0, b1 = 0;
-    int64_t made = 0;
+    Span tokens{0, 0}, entries{0, 0};
+    uint32_t made = 0;   // the first token that is not the prompt's
     if (hist) {
-        lo = a.offsets[row];
-        hi = a.offsets[row + 1];
-        lo = lo < 0 ? 0 : lo;
-        hi = hi < (int)a.history_len ? hi : (int)a.history_len;
-        made = (int64_t)lo + (a.prompt_lens != nullptr ? a.prompt_lens[row] : 0);
+        tokens = held_span(a.offsets[row], a.offsets[row + 1], a.history_len);
+        const int32_t prompt = a.prompt_lens != nullptr ? a.prompt_lens[row] : 0;
+        made = prompt > 0 ? (uint32_t)prompt : 0u;
     }
-    if (bias) {
-        b0 = a.bias_offsets[row];
-        b1 = a.bias_offsets[row + 1];
-        b0 = b0 < 0 ? 0 : b0;
-        b1 = b1 < (int)a.bias_len ? b1 : (int)a.bias_len;
-    }
-    constexpr int U = 4;
+    if (bias)
+        entries = held_span(a.bias_offsets[row], a.bias_offsets[row + 1], a.bias_len);
+    const int32_t* const history = a.history + tokens.first;   // all indices below count from the row's first
+    const int32_t* const bias_ids = a.bias_ids + entries.first;
+    constexpr uint32_t U = 4;
     int32_t t[U], tb = -1;
-    auto fetch = [&](int i) {
+    auto fetch = [&](uint32_t i) {
 #pragma unroll
-        for (int j = 0; j < U; ++j)
-            t[j] = i + j * kThreads < hi ? a.history[i + j * kThreads] : -1;
+        for (uint32_t j = 0; j < U; ++j)
+            t[j] = i + j * kThreads < tokens.count ? history[i + j * kThreads] : -1;
     };
-    fetch(lo + tid);
-    if (b0 + tid < b1)
-        tb = a.bias_ids[b0 + tid];
+    fetch((uint32_t)tid);
+    if ((uint32_t)tid < entries.count)
+        tb = bias_ids[tid];
     auto clear = [&]() {
 #pragma unroll
         for (int j = 0; j < 2 * kSets; ++j)
@@ -109,11 +106,11 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a, int tile
     if (hist) {
         clear();
         __syncthreads();
-        for (int i = lo + tid; i < hi; i += U * kThreads) {
-            if (i != lo + tid)
+        for (uint32_t i = (uint32_t)tid; i < tokens.count; i += U * kThreads) {
+            if (i != (uint32_t)tid)
                 fetch(i);
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
+            for (uint32_t j = 0; j < U; ++j) {
                 const uint32_t v = (uint32_t)t[j] - (uint32_t)v0;
                 if (t[j] >= v0 && v < (uint32_t)n) {
                     if (i + j * kThreads >= made)
@@ -157,12 +154,12 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a, int tile
         __syncthreads();   // the counts have been read
         clear();
         __syncthreads();
-        for (int i = b0 + tid; i < b1; i += kThreads) {
-            if (i != b0 + tid)
-                tb = a.bias_ids[i];
+        for (uint32_t i = (uint32_t)tid; i < entries.count; i += kThreads) {
+            if (i != (uint32_t)tid)
+                tb = bias_ids[i];
             const uint32_t v = (uint32_t)tb - (uint32_t)v0;
             if (tb >= v0 && v < (uint32_t)n)
-                atomicMax(&slot[v], (uint32_t)(i - b0) + 1u);
+                atomicMax(&slot[v], i + 1u);
         }
         __syncthreads();
 #pragma unroll
@@ -172,7 +169,7 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a, int tile
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (e[j] != 0)
-                    z[s][j] += a.bias_values[(int64_t)b0 + e[j] - 1];
+                    z[s][j] += a.bias_values[entries.first + e[j] - 1];
         }
     }
     St* out = static_cast<St*>(a.out) + row * a.out_stride + v0;
