@@ -195,7 +195,12 @@ __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPla
         uint32_t w[4][NW];
         uint16_t s[4], b[4];
     };
-    constexpr int W_LOADS = 4 * (BITS == 8 ? 1 : NW) + 8;
+    // Loads a step, which its end counts: at 6 and 8 bits a row's two words,
+    // which are always both needed, are one load by their form here, so that
+    // no merging of the compiler's changes the count (at 3 bits the second has
+    // an offset of its own, and two loads stay two).
+    constexpr bool PAIR = BITS == 6 || BITS == 8;
+    constexpr int W_LOADS = 4 * (PAIR ? 1 : NW) + 8;
     Raw raw[2];
     // Rows from .. to - 1 of a step's block.
     auto load_w = [&](int step, Raw& r, int from, int to) {
@@ -211,13 +216,13 @@ __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPla
             rsrc(static_cast<const char*>(a.w[p].biases) + (int64_t)n0 * grow, rows * grow);
 #pragma unroll
         for (int i = from; i < to; ++i) {
-            if constexpr (BITS == 8) {
+            if constexpr (PAIR) {
                 const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rw, w_off + (uint32_t)i * wrow, 0, 0));
                 r.w[i][0] = v[0];
                 r.w[i][1] = v[1];
             } else
                 r.w[i][0] = __builtin_amdgcn_raw_buffer_load_b32(rw, w_off + (uint32_t)i * wrow, 0, 0);
-            if constexpr (NW == 2 && BITS != 8)
+            if constexpr (NW == 2 && !PAIR)
                 r.w[i][1] = __builtin_amdgcn_raw_buffer_load_b32(rw, C8::need2(oct) ? w_off + (uint32_t)i * wrow + 4 : OOB, 0, 0);
             r.s[i] = __builtin_amdgcn_raw_buffer_load_b16(rs, g_off + (uint32_t)i * grow, 0, 0);
             r.b[i] = __builtin_amdgcn_raw_buffer_load_b16(rb, g_off + (uint32_t)i * grow, 0, 0);
