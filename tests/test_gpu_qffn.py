@@ -288,3 +288,15 @@ def test_against_differences(act):
         # The saved products' own rounding moves the point the gradient is taken at.
         tol += 1e-5 * float((got.abs() * dr.abs()).sum())
         assert abs(float((got * dr).sum()) - fd) <= tol, (name, float((got * dr).sum()), fd, tol)
+
+
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("bits", [2, 3, 6, 8])
+@pytest.mark.parametrize("m,d,f", [(17, 96, 160), (40, 1120, 352), (130, 352, 1120), (300, 160, 2080), (64, 2080, 96)])
+def test_forward_filled_up_contractions(m, d, f, bits, dt):
+    """Both contractions of 64 n + 32, at the widths whose rows of codes end inside a 16-byte
+    piece (2 and 6) and at those that do not. Every code occurs, the last row's last ones too."""
+    c = case(m, d, f, bits, 32, dt)
+    for n in ("gate", "up", "down"):
+        assert (oh.codes(c[n][0], bits)[-1, -32:] != 0).any()
+    check_forward(c, "silu", "filled up")

@@ -124,10 +124,11 @@ hipError_t product(const FfnArgs& a, const void* x, int64_t k, const QWeight& w,
 // Rows of 16-bit elements copied to longer rows, zeros behind: array blockIdx.y,
 // two elements a thread.
 struct PadArgs {
-    const uint16_t* in[5];
-    uint32_t* out[5];
-    int64_t rows[5];
-    uint32_t cols[5], pairs[5];   // elements in a row, pairs in an output row
+    static constexpr int MAX = 7;   // x, and two matrices' scales, biases and codes
+    const uint16_t* in[MAX];
+    uint32_t* out[MAX];
+    int64_t rows[MAX];
+    uint32_t cols[MAX], pairs[MAX];   // elements in a row, pairs in an output row
 };
 __global__ __launch_bounds__(256) void ffn_pad_kernel(PadArgs a)
 {
@@ -142,6 +143,10 @@ __global__ __launch_bounds__(256) void ffn_pad_kernel(PadArgs a)
     }
 }
 
+// Whether a row of 64 n + 32 codes ends inside one of the pieces (16 bytes, at 3
+// bits 12) that the tile kernel takes a step's codes in: at 2 and 6 bits.
+constexpr bool ends_in_piece(int bits) { return 4 * bits % (bits == 3 ? 12 : 16) != 0; }
+
 // A product in pieces where the plan and the pointers allow it.
 template <bool GATED>
 hipError_t split_product(const FfnArgs& a, const void* x, int64_t k, const QWeight& w0, const QWeight& w1, int64_t n,
@@ -154,7 +159,7 @@ hipError_t split_product(const FfnArgs& a, const void* x, int64_t k, const QWeig
                          reinterpret_cast<uintptr_t>(w1.scales) | reinterpret_cast<uintptr_t>(w1.biases);
     const int64_t kk = p.kp > 0 ? p.kp : k, groups = kk / a.gs;
     constexpr int64_t k2GB = int64_t(1) << 31;
-    if (p.per_split == 0 || (p.kp == 0 && (!aligned16(x) || sb % 4 != 0)) || n * (k * a.bits / 8) >= k2GB ||
+    if (p.per_split == 0 || (p.kp == 0 && (!aligned16(x) || sb % 4 != 0)) || n * (kk * a.bits / 8) >= k2GB ||
         n * groups * 2 >= k2GB - 4 || a.M * kk * 2 >= k2GB)
         return hipSuccess;
     if (p.kp > 0) {
@@ -173,11 +178,18 @@ hipError_t split_product(const FfnArgs& a, const void* x, int64_t k, const QWeig
         };
         s.x = add(x, a.M, k, kk);
         s.K = kk;
+        int64_t most = std::max(a.M * kk, n * groups) / 2;
         for (int t = 0; t < NMAT; ++t) {
             s.w[t].scales = add(s.w[t].scales, n, k / a.gs, groups);
             s.w[t].biases = add(s.w[t].biases, n, k / a.gs, groups);
+            // Left where they lie, the last row's last piece would reach past
+            // the codes' end. As 16-bit elements: 32 codes are 4, 12 of them.
+            if (ends_in_piece(a.bits)) {
+                s.w[t].wq = static_cast<const uint32_t*>(add(s.w[t].wq, n, k * a.bits / 16, kk * a.bits / 16));
+                s.wk = kk;
+                most = std::max(most, n * kk * a.bits / 32);
+            }
         }
-        const int64_t most = std::max(a.M * kk, n * groups) / 2;
         hipLaunchKernelGGL(ffn_pad_kernel, dim3((unsigned)std::min<int64_t>((most + 255) / 256, 4096), (unsigned)arrays),
                            dim3(256), 0, st, pad);
         if (hipError_t e = hipGetLastError(); e != hipSuccess)
@@ -217,9 +229,11 @@ hipError_t gate_up(const GateUpArgs& a, hipStream_t st, bool* done)
 // rows 354 and 210. Filling the CUs twice: 64 rows 83 us.
 // A contraction of whole 32-wide groups but not whole 64-wide steps (groups of 32
 // then) is filled up with zeros: x, the scales and the biases in a copy, the codes
-// where they lie, the next row's times zero (5600 x 2080, 4-bit, bf16, 253 rows 222
-// us on ffn_any's kernel, 83 so; 2048 rows 1354 and 297). Below 64 the weights'
-// roundings do not average out, and ffn_any's kernel takes the product.
+// where they lie, the next row's times zero, or (2 and 6 bits) in a copy too
+// (5600 x 2080, 4-bit, bf16, 253 rows 222 us on ffn_any's kernel, 79 so; 2048 rows
+// 1354 and 280; at 6 bits, with the codes' copy, 96 and 311). Below 64 the weights'
+// roundings do not average out, and ffn_any's kernel takes the product. The room
+// is for 6-bit codes: the sizes alone decide it.
 FfnSplit ffn_split(int64_t m, int64_t k, int64_t n, int nmat, int dt)
 {
     FfnSplit p{m <= 128 ? 64 : 256, 1, 0, 0, 0, 0};
@@ -236,7 +250,8 @@ FfnSplit ffn_split(int64_t m, int64_t k, int64_t n, int nmat, int dt)
     p.partial_bytes = (size_t)p.splits * (size_t)nmat * (size_t)m * (size_t)n * 4;
     if (pad) {
         p.kp = k + 32;
-        p.pad_bytes = up16((size_t)m * (size_t)p.kp * 2) + 2 * (size_t)nmat * up16((size_t)n * (size_t)(p.kp / 32) * 2);
+        p.pad_bytes = up16((size_t)m * (size_t)p.kp * 2) +
+                      (size_t)nmat * (2 * up16((size_t)n * (size_t)(p.kp / 32) * 2) + up16((size_t)n * (size_t)(p.kp / 4 * 3)));
     }
     return p;
 }

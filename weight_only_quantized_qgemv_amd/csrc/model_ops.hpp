@@ -54,7 +54,7 @@ struct FfnSplit {
     int per_split;          // steps of a piece (ffn_split: 0 where the product is another path's)
     size_t partial_bytes;
     int64_t kp;             // ffn_split: the contraction filled up to whole 64-wide steps, 0: as it is
-    size_t pad_bytes;       // and what the filled-up x, scales and biases take
+    size_t pad_bytes;       // and what the filled-up x, scales, biases and codes take
 };
 FfnSplit ffn_split(int64_t m, int64_t k, int64_t n, int nmat, int dt);
 struct FfnSplitArgs {
