@@ -380,8 +380,9 @@ qp_status qgemv_moe_ffn(const void* a, qp_dtype a_dtype, const int32_t* ids,
  *   y        device, x_dtype [m, d_model] (output)
  *   workspace device, >= qffn_workspace_bytes(m, d_model, d_ff, dtype), 16-byte aligned
  * d_model and d_ff must be multiples of group_size; sb_dtype must equal
- * x_dtype. fp32 accumulation; h (and g and u where they are kept) is rounded
- * to x_dtype between the products. m == 0 is a no-op; d_ff == 0 writes zeros.
+ * x_dtype. fp32 accumulation; h is formed from the fp32 g and u, whether they
+ * are kept or not, and rounded to x_dtype as the down projection's operand; g and
+ * u are rounded where they are kept. m == 0 is a no-op; d_ff == 0 writes zeros.
  */
 size_t qffn_workspace_bytes(int64_t m, int64_t d_model, int64_t d_ff, qp_dtype dtype);
 qp_status qffn(const void* x, qp_dtype x_dtype, int64_t m, int64_t d_model, int64_t d_ff,

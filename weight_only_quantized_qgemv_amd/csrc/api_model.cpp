@@ -132,7 +132,11 @@ qp_status qffn(const void* x, qp_dtype x_dtype, int64_t m, int64_t d_model, int6
     a.up = {up_wq, up_scales, up_biases};
     a.down = {down_wq, down_scales, down_biases};
     a.bits = bits; a.gs = group_size;
-    a.saved = saved; a.y = y; a.workspace = workspace;
+    if (saved) {
+        a.saved[0] = saved;
+        a.saved[1] = static_cast<char*>(saved) + (size_t)m * (size_t)d_ff * es;
+    }
+    a.y = y; a.workspace = workspace;
     return hip_result(qp::launch_ffn(a, stream), what);
 }
 

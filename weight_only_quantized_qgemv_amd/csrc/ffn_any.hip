@@ -1,7 +1,8 @@
 // ffn_any.hip — the gated block's products for what the other kernels do not
 // take: fp32 activations of more than one row, and 16-bit ones of more than 16
-// rows that are not 16-byte aligned or contract over 32. y = x W^T on the fp32 32x32x2
-// matrix instruction, any size and alignment, nothing rounded before y.
+// rows that contract over 32 or whose weights take 2 GB or more. y = x W^T on the
+// fp32 32x32x2 matrix instruction, any size and alignment, nothing rounded
+// before y (or before the fp32 sums that another launch closes).
 // Compiled once per bit width (QP_BITS).
 #include <algorithm>
 
@@ -123,8 +124,8 @@ __global__ __launch_bounds__(256) void ffn_any_kernel(FfnAnyArgs a)
                     f(m * a.N + n, acc[i][r]);
             }
     };
-    if (a.plan.splits > 1) {
-        float* const part = a.partial + (int64_t)blockIdx.y * a.M * a.N;
+    if (a.partial != nullptr) {
+        float* const part = a.partial + (int64_t)blockIdx.y * a.partial_stride;
         each([&](int64_t i, float v) { part[i] = v; });
     } else {
         each([&](int64_t i, float v) { store_elem<DT>(a.y, i, v); });

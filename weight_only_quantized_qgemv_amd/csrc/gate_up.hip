@@ -3,7 +3,8 @@
 // both projections, the activation and the product in one launch, for 16-bit
 // activations: the row kernel at one and two rows (rowstream.hpp), the skinny
 // matrix-core kernel up to 16 (skinny.hpp), the tile kernel beyond
-// (gemm_core.hpp), which also keeps the two products for a backward pass.
+// (gemm_core.hpp). Each closes h from its fp32 sums, and stores the two products
+// beside it where a backward pass follows: h is the same with and without them.
 // Compiled once per bit width (QP_BITS).
 #include <algorithm>
 
@@ -31,6 +32,7 @@ hipError_t run_rows(const GateUpArgs& a, hipStream_t st)
     k.M = (int)a.M; k.N = (int)a.N; k.K = (int)a.K; k.gs = a.gs;
     k.units_row = (uint32_t)(a.K / 32);
     k.act = a.act;
+    k.saved[0] = a.saved[0]; k.saved[1] = a.saved[1];
     const int64_t blocks = std::min<int64_t>((a.N + ROWS - 1) / ROWS, 4096);
     if ((a.K / a.gs) % 2 == 0 && reinterpret_cast<uintptr_t>(a.gate.scales) % 4 == 0 &&
         reinterpret_cast<uintptr_t>(a.gate.biases) % 4 == 0 && reinterpret_cast<uintptr_t>(a.up.scales) % 4 == 0 &&
@@ -76,6 +78,7 @@ hipError_t run_skinny(const GateUpArgs& a, hipStream_t st)
     k.out_bytes = (uint32_t)(a.M * a.N * 2);
     k.x_bytes = (uint32_t)(a.M * a.K * 2);
     k.act = a.act;
+    k.saved[0] = a.saved[0]; k.saved[1] = a.saved[1];
     SkinnyShape sh{};
     dim3 grid;
     skinny_dense_shape(a.N, a.K, &sh, &grid);
@@ -109,8 +112,7 @@ hipError_t run_tiles(const GateUpArgs& a, hipStream_t st)
     g.tiles = (int)((a.M + BM - 1) / BM) * g.tiles_n;
     g.per_xcd = (g.tiles + 7) / 8;
     g.act = a.act;
-    g.saved[0] = a.saved;
-    g.saved[1] = a.saved != nullptr ? static_cast<char*>(a.saved) + a.M * a.N * 2 : nullptr;
+    g.saved[0] = a.saved[0]; g.saved[1] = a.saved[1];
     hipLaunchKernelGGL((gemm::qgemm_tile_kernel<BITS, DT, BM, BN, NT, WMW, 2, false, NA, NC>), dim3(g.per_xcd * 8),
                        dim3(NT), LDS, st, g);
     return hipGetLastError();
@@ -123,11 +125,12 @@ hipError_t run(const GateUpArgs& a, hipStream_t st, bool* done)
     if (!aligned16(a.x) || a.N * (a.K * BITS / 8) >= k2GB || a.N * (a.K / a.gs) * 2 >= k2GB - 4 ||
         a.M * a.N * 2 >= k2GB || a.M * a.K * 2 >= k2GB || a.K >= (1 << 30))
         return hipSuccess;
-    if (a.saved == nullptr && a.M <= 16) {
-        if (a.M == 1)
-            return run_rows_upl<BITS, DT, 1>(a, st, done);
-        if (a.M == 2) {
-            hipError_t e = run_rows_upl<BITS, DT, 2>(a, st, done);
+    if (a.M <= 16) {
+        // The row kernel where its registers hold the rows' slices. One row beyond
+        // (the whole block, 4-bit, d_ff 8192): 9216 39.9 us on the skinny kernel,
+        // two products and a third launch 40.1; 16384 61.9 and 64.2; 17408 65 and 702.
+        if (a.M <= 2) {
+            hipError_t e = a.M == 1 ? run_rows_upl<BITS, DT, 1>(a, st, done) : run_rows_upl<BITS, DT, 2>(a, st, done);
             if (e != hipSuccess || *done)
                 return e;
         }
@@ -136,7 +139,7 @@ hipError_t run(const GateUpArgs& a, hipStream_t st, bool* done)
     }
     const bool dwords = (reinterpret_cast<uintptr_t>(a.gate.scales) | reinterpret_cast<uintptr_t>(a.gate.biases) |
                          reinterpret_cast<uintptr_t>(a.up.scales) | reinterpret_cast<uintptr_t>(a.up.biases)) % 4 == 0;
-    if (a.K % gemm::BK != 0 || !dwords || a.M <= 16)
+    if (a.K % gemm::BK != 0 || !dwords)
         return hipSuccess;
     *done = true;
     // Measured with 4-bit codes, the whole block's time. Up to 128 rows tiles of

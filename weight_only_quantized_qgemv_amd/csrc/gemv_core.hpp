@@ -101,7 +101,8 @@ struct GemvKernelArgs {
     uint32_t out_bytes;      // size of `out` in bytes (< 2^31)
     uint32_t x_bytes;        // bytes of activations reachable from `x` (< 2^31; read
                              // by the matrix-core kernel's table DMA)
-    int act;                 // activation of the gated form (0: SiLU; act.hpp), read by
+    int act;                 // activation of the gated form (0: SiLU; act.hpp), and where
+    void* saved[2];          // its two products are kept (of out's shape), or null: read by
                              // the skinny matrix-core kernel
 };
 

@@ -27,7 +27,7 @@ struct FfnArgs {
     int64_t M, D, F;
     QWeight gate, up, down; // [F, D], [F, D], [D, F]
     int bits, gs;
-    void* saved;            // [2, M, F] of dt (the gate's product, then the up's), or null
+    void* saved[2];         // [M, F] of dt each (the gate's product, the up's), or null
     void* y;                // [M, D] of dt
     void* workspace;        // >= ffn_workspace_bytes, 16-byte aligned
 };
@@ -43,7 +43,7 @@ struct GateUpArgs {
     QWeight gate, up;
     int bits, gs;
     void* h;                // [M, N]
-    void* saved;            // [2, M, N] or null
+    void* saved[2];         // [M, N] each, or null
 };
 // The block's products with the contraction in pieces, for batches whose tiles
 // are too few to fill the GPU: x [M, K] times one or two matrices of N rows, as
@@ -67,7 +67,8 @@ struct FfnSplitArgs {
     float* partial;
 };
 // y = x W^T for any type, size and alignment (ffn_any.hip), in pieces of 32-wide
-// steps where the plan asks for it.
+// steps where the plan asks for it: as fp32 sums to `partial` [splits], pieces
+// partial_stride elements apart, or (null) as y.
 FfnSplit ffn_any_plan(int64_t m, int64_t k, int64_t n);
 struct FfnAnyArgs {
     const void* x;
@@ -77,6 +78,7 @@ struct FfnAnyArgs {
     int gs;
     FfnSplit plan;
     float* partial;
+    int64_t partial_stride;
     void* y;
 };
 #define QP_GATEUP_DECL(B) \

@@ -47,6 +47,7 @@ struct RowStreamArgs {
     const void* up_scales;
     const void* up_biases;
     int act;
+    void* saved[2];             // where the two products are kept ([M, N] each), or null
 };
 
 template <int DT> struct RowStreamPair;
@@ -308,10 +309,17 @@ __global__ __launch_bounds__(64 * WPB) void qgemv_rowstream_kernel(RowStreamArgs
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
                     if (r0 + slot * D + d < a.N && m < a.M) {
+                        const int64_t at = (int64_t)m * a.N + r0 + slot * D + d;
                         float v = acc[d * MT + m];
-                        if constexpr (NMAT == 2)
-                            v = act_f32(a.act, v) * acc[(D + d) * MT + m];
-                        y[(int64_t)m * a.N + r0 + slot * D + d] = E::from_f32(v);
+                        if constexpr (NMAT == 2) {
+                            const float u = acc[(D + d) * MT + m];
+                            if (a.saved[0] != nullptr) {   // uniform
+                                static_cast<St*>(a.saved[0])[at] = E::from_f32(v);
+                                static_cast<St*>(a.saved[1])[at] = E::from_f32(u);
+                            }
+                            v = act_f32(a.act, v) * u;
+                        }
+                        y[at] = E::from_f32(v);
                     }
         }
     }

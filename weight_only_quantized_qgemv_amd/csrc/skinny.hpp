@@ -670,13 +670,18 @@ __global__ __launch_bounds__(64 * kSkinnyMaxWaves) void qgemv_skinny_kernel(Gemv
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int m = 4 * g + r;
-                float v = tot[0][r];
-                if constexpr (NMAT == 2)
-                    v = act_f32(a.act, tot[0][r]) * tot[1][r];
                 uint32_t off = OOB;
                 if (m < rows && n < r_hi) {
                     const uint32_t pr = a.perm != nullptr ? (uint32_t)a.perm[start + m] : (uint32_t)(start + m);
                     off = (pr * (uint32_t)R + (uint32_t)n) * (uint32_t)SB;
+                }
+                float v = tot[0][r];
+                if constexpr (NMAT == 2) {
+                    if (a.saved[0] != nullptr) {   // uniform
+                        buffer_store_elem<DT>(E::from_f32(tot[0][r]), make_rsrc(a.saved[0], a.out_bytes), off);
+                        buffer_store_elem<DT>(E::from_f32(tot[1][r]), make_rsrc(a.saved[1], a.out_bytes), off);
+                    }
+                    v = act_f32(a.act, tot[0][r]) * tot[1][r];
                 }
                 buffer_store_elem<DT>(E::from_f32(v), ro, off);
             }
