@@ -300,3 +300,27 @@ def test_forward_filled_up_contractions(m, d, f, bits, dt):
     for n in ("gate", "up", "down"):
         assert (oh.codes(c[n][0], bits)[-1, -32:] != 0).any()
     check_forward(c, "silu", "filled up")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("dt", [F32, F16, BF16])
+@pytest.mark.parametrize("m,d,f", [(4, 64, 64), (40, 96, 160), (300, 128, 192)])
+def test_backward_far_preactivations_against_the_formula(m, d, f, dt, act):
+    """Gates at the ends of the type's range, one column each (so a row each of the gate's and
+    up's gradients): every gradient against the 64-bit form. dy is small enough, and u there
+    one half, so that nothing leaves the range."""
+    c = case(m, d, f, 4, 32, dt)
+    top, small = (60000.0, 1e-3) if dt == F16 else (3e38, 1e-30)
+    c["dy"] = (c["dy"].double() * small).to(c["dy"].dtype)
+    far = [-top, -top / 4, -1e4, -200.0, -88.0, -20.0, -0.0, 0.0, 20.0, 88.0, 200.0, 1e4, top / 4, top]
+    saved = saved_of(c)
+    saved[0, :, :len(far)] = torch.tensor(far, dtype=torch.float64).to(saved.dtype)
+    saved[1, :, :len(far)] = 0.5
+    log(f"qffn_backward far pre-activations: m={m} d={d} f={f} dt={dt} {act}")
+    dx, *pairs = run_backward(c, saved, act)
+    torch.cuda.synchronize()
+    outs = [dx] + [t for p in pairs for t in p]
+    names = ["dx"] + [f"{w} {p}" for w in ("gate", "up", "down") for p in ("scales", "biases")]
+    for y, (ref, bound), name in zip(outs, backward_ref(c, saved, act), names):
+        assert torch.isfinite(ref).all() and torch.isfinite(bound).all()
+        oh.check(y, ref, bound, f"far {name}")
