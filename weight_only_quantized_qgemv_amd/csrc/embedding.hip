@@ -87,7 +87,7 @@ template <int DT> __device__ __forceinline__ void store8(void* p, int64_t i, boo
 template <int BITS, int DT>
 __global__ __launch_bounds__(256) void embedding_kernel(EmbedArgs a, bool vec)
 {
-    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int64_t t = (blockIdx.x + (int64_t)blockIdx.y * gridDim.x) * blockDim.y + threadIdx.y;
     if (t >= a.T)
         return;
     const int64_t id = a.ids[t];
@@ -351,7 +351,7 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedGradArgs a, GradTab
     constexpr int RB = DT == DT_F32 ? 4 : 8;
     const int lane = (int)threadIdx.x & 63;
     const int64_t col_tiles = (a.K / 8 + 63) / 64;
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t item = (blockIdx.x + (int64_t)blockIdx.y * gridDim.x) * 4 + (threadIdx.x >> 6);
     const int64_t w = item / col_tiles, p0 = w * kWindow;
     if (p0 >= a.T)
         return;
@@ -431,7 +431,7 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedGradArgs a, GradTab
     }
 }
 
-// The run that starts in window blockIdx.x and crosses its end: its windows'
+// The run that starts in window w, the block's, and crosses its end: its windows'
 // sums (the first in the slot of a window's last run, the others in that of
 // its first). 512 / (2 G) groups of threads take a contiguous share of the
 // windows each, in order, and their sums are added in order: a run of
@@ -443,7 +443,9 @@ __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(EmbedGradArgs 
     __shared__ float part[kJoinThreads];
     __shared__ int s_len;
     const int tid = (int)threadIdx.x, lane = tid & 63;
-    const int64_t w = blockIdx.x, end = (w + 1) * kWindow;   // end < T
+    const int64_t w = blockIdx.x + (int64_t)blockIdx.y * gridDim.x, end = (w + 1) * kWindow;
+    if (end >= a.T)
+        return;
     const int32_t id = g.id[end];
     if (id < 0 || g.id[end - 1] != id)
         return;
@@ -502,7 +504,7 @@ template <int BITS, int DT> hipError_t lookup(const EmbedArgs& a, hipStream_t st
     while (tx < 256 && tx < a.K / 8)
         tx *= 2;
     const int ty = 256 / tx;
-    hipLaunchKernelGGL((embedding_kernel<BITS, DT>), dim3((unsigned)((a.T + ty - 1) / ty)), dim3(tx, ty), 0, st, a,
+    hipLaunchKernelGGL((embedding_kernel<BITS, DT>), wide_grid((a.T + ty - 1) / ty, 256), dim3(tx, ty), 0, st, a,
                        aligned16(a.out));
     return hipGetLastError();
 }
@@ -527,11 +529,11 @@ template <int BITS, int DT> hipError_t grad(const EmbedGradArgs& a, hipStream_t 
     if (hipError_t e = a.V < Key<uint32_t>::PAST ? order(uint32_t{}) : order(uint64_t{}); e != hipSuccess || a.T == 0)
         return e;
     const int64_t windows = window_count(a.T), items = windows * ((a.K / 8 + 63) / 64);
-    hipLaunchKernelGGL((embed_sum_kernel<BITS, DT>), dim3((unsigned)((items + 3) / 4)), dim3(256), 0, st, a, g,
+    hipLaunchKernelGGL((embed_sum_kernel<BITS, DT>), wide_grid((items + 3) / 4, 256), dim3(256), 0, st, a, g,
                        aligned16(a.dout));
     if (hipError_t e = hipGetLastError(); e != hipSuccess || windows == 1)
         return e;
-    hipLaunchKernelGGL((embed_join_kernel<DT>), dim3((unsigned)(windows - 1)), dim3(kJoinThreads), 0, st, a, g);
+    hipLaunchKernelGGL((embed_join_kernel<DT>), wide_grid(windows - 1, kJoinThreads), dim3(kJoinThreads), 0, st, a, g);
     return hipGetLastError();
 }
 

@@ -135,6 +135,8 @@ __global__ __launch_bounds__(256) void ffn_any_kernel(FfnAnyArgs a)
 template <int DT> hipError_t run(const FfnAnyArgs& a, hipStream_t st)
 {
     const int64_t bm = a.plan.tile, tiles = ((a.M + bm - 1) / bm) * ((a.N + AN_N - 1) / AN_N);
+    if (!grid_fits(tiles, 256))
+        return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)tiles, (unsigned)a.plan.splits);
     if (bm == 32)
         hipLaunchKernelGGL((ffn_any_kernel<QP_BITS, DT, 1, 4>), grid, dim3(256), 0, st, a);

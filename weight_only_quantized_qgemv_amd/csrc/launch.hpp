@@ -35,6 +35,18 @@ inline hipError_t device_cu_count(int* cus)
     return e;
 }
 
+// HIP counts a grid's threads along a dimension in 32 bits: a launch of 2^32 or
+// more runs a part of its blocks and reports success.
+constexpr int64_t kGridThreads = (int64_t(1) << 32) - 1;
+inline bool grid_fits(int64_t blocks, int threads) { return blocks <= kGridThreads / threads; }
+// A grid of so many blocks in x and, where one dimension does not hold them, y:
+// block x + y gridDim.x; the kernel drops those past the last.
+inline dim3 wide_grid(int64_t blocks, int threads)
+{
+    const int64_t most = kGridThreads / threads, y = (blocks + most - 1) / most;
+    return y <= 1 ? dim3((unsigned)blocks) : dim3((unsigned)((blocks + y - 1) / y), (unsigned)y);
+}
+
 struct GemvArgs {
     const void* x;          // [M, K] activations
     int dt;                 // element type of x, scales, biases and y

@@ -40,8 +40,11 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a, int tile
     using St = typename E::storage;
     constexpr int NV = 8 * (int)sizeof(St) / 16;
     __shared__ __attribute__((aligned(16))) uint32_t slot[kTile];
-    const int64_t row = (int64_t)blockIdx.x / tiles;
-    const int v0 = ((int)((int64_t)blockIdx.x % tiles)) * kTile;
+    const int64_t block = blockIdx.x + (int64_t)blockIdx.y * gridDim.x;
+    const int64_t row = block / tiles;
+    if (row >= a.rows)
+        return;
+    const int v0 = (int)(block % tiles) * kTile;
     const int n = (int)(a.vocab - v0 < kTile ? a.vocab - v0 : kTile);
     const int tid = (int)threadIdx.x;
     const bool hist = a.history != nullptr, bias = a.bias_ids != nullptr;
@@ -205,7 +208,7 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a, int tile
 template <int DT> hipError_t run(const LogitsArgs& a, hipStream_t st)
 {
     const int64_t tiles = (a.vocab + kTile - 1) / kTile;
-    hipLaunchKernelGGL((logits_kernel<DT>), dim3((unsigned)(tiles * a.rows)), dim3(kThreads), 0, st, a, (int)tiles);
+    hipLaunchKernelGGL((logits_kernel<DT>), wide_grid(tiles * a.rows, kThreads), dim3(kThreads), 0, st, a, (int)tiles);
     return hipGetLastError();
 }
 

@@ -23,6 +23,8 @@ hipError_t run_tile(const WgradArgs& a, const GradPlan& p, hipStream_t st)
     }
     const int64_t tiles_k = (a.K + BT - 1) / BT, tiles = (a.N + BT - 1) / BT * tiles_k;
     const int per_xcd = (int)((tiles * a.nmat + 7) / 8);
+    if (!grid_fits((int64_t)per_xcd * 8, 2 * BT))
+        return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((gradtile::wgrad_tile_kernel<BITS, DT, BT, BT>), dim3((unsigned)per_xcd * 8, (unsigned)p.splits),
                        dim3(2 * BT), LDS, st, a, p, (int)tiles_k, (int)tiles, per_xcd);
     return hipGetLastError();
@@ -56,6 +58,8 @@ hipError_t run(const WgradArgs& a, const GradPlan& p, hipStream_t st)
     hipError_t e = hipErrorInvalidValue;
     if (p.tile == 0) {
         const int64_t tiles = ((a.N + WG_BN - 1) / WG_BN) * ((a.K + WG_BK - 1) / WG_BK);
+        if (!grid_fits(tiles, 256))
+            return hipErrorInvalidConfiguration;
         hipLaunchKernelGGL((wgrad_f32_kernel<BITS, DT>), dim3((unsigned)tiles, (unsigned)p.splits, (unsigned)a.nmat),
                            dim3(256), 0, st, a, p);
         e = hipGetLastError();

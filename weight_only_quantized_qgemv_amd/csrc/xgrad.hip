@@ -31,6 +31,8 @@ hipError_t run_tile(const XgradArgs& a, const GradPlan& p, hipStream_t st)
     }
     const int64_t tiles_k = (a.K + BN - 1) / BN, tiles = (a.M + BM - 1) / BM * tiles_k;
     const int per_xcd = (int)((tiles + 7) / 8);
+    if (!grid_fits((int64_t)per_xcd * 8, 2 * BN))
+        return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((gradtile::xgrad_tile_kernel<BITS, DT, BM, BN, WMW>), dim3((unsigned)per_xcd * 8, (unsigned)p.splits),
                        dim3(2 * BN), LDS, st, a, p, (int)tiles_k, (int)tiles, per_xcd);
     return hipGetLastError();
@@ -42,6 +44,8 @@ hipError_t run(const XgradArgs& a, const GradPlan& p, hipStream_t st)
     hipError_t e = hipErrorInvalidValue;
     if (p.tile == 0) {
         const int64_t tiles = ((a.M + XG_BM - 1) / XG_BM) * ((a.K + XG_BK - 1) / XG_BK);
+        if (!grid_fits(tiles, 256))
+            return hipErrorInvalidConfiguration;
         hipLaunchKernelGGL((xgrad_f32_kernel<BITS, DT>), dim3((unsigned)tiles, (unsigned)p.splits), dim3(256), 0, st,
                            a, p);
         e = hipGetLastError();
