@@ -442,7 +442,8 @@ qp_status qmatmul_backward(const void* x, const void* dy, qp_dtype x_dtype, int6
 /*
  * Lookup in a packed embedding table, with a factor:
  *   out[t, i] = factor * (q[v, i] * s'[v, i/gs] + b'[v, i/gs]),  v = ids[t]
- *   ids      device, int32 [n_tokens]; an id outside [0, n_rows) gives a row of zeros
+ *   ids      device, int32 [n_tokens], n_tokens below 2^29; an id outside [0, n_rows)
+ *            gives a row of zeros
  *   wq, scales, biases  device, the table [n_rows, k] as in qmatmul
  *   out      device, sb_dtype [n_tokens, k] (output), rounded once from fp32
  */
@@ -461,7 +462,7 @@ qp_status qembedding(const int32_t* ids, int64_t n_tokens, const uint32_t* wq, c
  *   workspace device, >= qembedding_backward_workspace_bytes(...), 16-byte aligned
  * Tokens are sorted by id on the device and a row's tokens are summed in token
  * order in fp32, rounded once: deterministic. Ids outside [0, n_rows) add nothing.
- * n_tokens is at most 2^29.
+ * n_tokens is below 2^29.
  */
 size_t qembedding_backward_workspace_bytes(int64_t n_tokens, int64_t k, int32_t bits,
                                            int32_t group_size);

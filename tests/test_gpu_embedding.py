@@ -156,3 +156,17 @@ def test_grad_against_differences():
         mine = got[i].cpu().double()
         mag = float((dout.double().abs() * 3.0 * 15).sum())
         assert abs(float((mine * d).sum()) - fd) <= 1e-5 * mag, (i, float((mine * d).sum()), fd)
+
+
+@pytest.mark.parametrize("v", [300, 2 ** 21 + 5])
+@pytest.mark.parametrize("t", [111 * 2048, 111 * 2048 + 1, 113 * 2048 - 7, 2 ** 18 + 2049])
+def test_grad_many_tokens(t, v):
+    """On both sides of the number of sorted chunks from which runs are merged, with runs that
+    are whole, short and odd in number; ids outside the table among them."""
+    k = 32
+    ids = torch.randint(-1, 301, (t,), generator=oh.rng(t)).to(torch.int32)
+    if v > 300:
+        ids[::1000] = v - 1
+        ids[1::1000] = v
+    log(f"embedding grad t={t} v={v} k={k}")
+    check_grad(ids, table(v, k, 2, 32, F16), 2, 32, F16, 1.0, "many tokens")

@@ -32,6 +32,30 @@ def test_embedding_of_more_than_2_24_tokens():
     del out
 
 
+@pytest.mark.parametrize("same", [False, True])
+def test_embedding_gradient_of_2_27_tokens(same):
+    """2^27 + 2049 tokens: sums of ones, exact in fp32 below 2^24 each. With one id for most
+    tokens a single run crosses most windows."""
+    need(60)
+    t, v, k, bits, gs = 2 ** 27 + 2049, 4001, 32, 8, 32
+    log(f"embedding gradient of {t} tokens, one id: {same}")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    wq = torch.zeros((v, k * bits // 32), dtype=torch.int32, device=dev())
+    wq[:, 0] = 3                                  # column 0 has code 3, the others 0
+    ids = torch.randint(-1, v + 1, (t,), generator=g, device=dev(), dtype=torch.int32)
+    if same:
+        ids[torch.rand(t, generator=g, device=dev()) < 0.9] = 77
+    live = (ids >= 0) & (ids < v)
+    count = torch.bincount(ids[live].long(), minlength=v).double()
+    # Every token adds 2^-10 at column 0: sums of up to 2^27 tokens, fp32 partial sums in order.
+    dout = torch.zeros((t, k), dtype=torch.bfloat16, device=dev())
+    dout[:, 0] = 2.0 ** -10
+    ds, db = qp.qembedding_backward(ids, dout, wq, bits, gs)
+    for got, want in ((ds, 3 * count * 2.0 ** -10), (db, count * 2.0 ** -10)):
+        bound = want * 2.0 ** -8 + want * oh.gamma(64)   # half an ulp of bf16, and partial sums of windows
+        assert ((got[:, 0].double() - want).abs() <= bound).all()
+
+
 def test_logits_of_more_than_2_23_rows():
     rows, v = 2 ** 23 + 3, 32
     log(f"logits of {rows} rows of {v}")

@@ -8,7 +8,8 @@
 // ids are sorted by (id, token), each by one block (a bitonic network, eight
 // keys a thread: strides below 8 in registers, below 512 across the lanes, the
 // three others through LDS); a token's place in the whole order is its place
-// in its chunk plus, for every other chunk, the count of smaller keys there.
+// in its chunk plus, for every other chunk, the count of smaller keys there, or
+// (many chunks) comes from merging sorted runs in pairs.
 // A wave then takes a window of kWindow places x 512 columns, whatever runs of
 // equal ids lie in it, so all waves move the same bytes: it streams the rows,
 // and where a run ends in its window it meets the codes and is stored. The
@@ -116,8 +117,11 @@ constexpr int kSortThreads = kChunk / 8;
 constexpr int kWindow = 16;     // places summed by one wave
 constexpr int kFillBlocks = 512;
 
+constexpr int64_t kMergeFrom = 112;   // chunks from which runs are merged
+
 struct GradTables {
     void* keys;           // [chunks * kChunk] (id, token in chunk), sorted by chunk (two chunks or more)
+    uint64_t* merged;     // [chunks * kChunk] the merges' other buffer (kMergeFrom chunks or more)
     int32_t* token;       // [T] tokens in the order of (id, token)
     int32_t* id;          // [T] their ids (-1: outside the table; these come last)
     float* partial;       // [2 windows][2 G]: of the run a window begins with, and of the one it ends with
@@ -135,6 +139,7 @@ size_t tables(int64_t t, int64_t groups, char* p, GradTables* out)
     };
     GradTables g{};
     g.keys = take(chunks > 1 ? (size_t)chunks * kChunk * 8 : 0);
+    g.merged = reinterpret_cast<uint64_t*>(take(chunks >= kMergeFrom ? (size_t)chunks * kChunk * 8 : 0));
     g.token = reinterpret_cast<int32_t*>(take((size_t)t * 4));
     g.id = reinterpret_cast<int32_t*>(take((size_t)t * 4));
     g.partial = reinterpret_cast<float*>(take(t > kWindow ? (size_t)window_count(t) * 4 * (size_t)groups * 4 : 0));
@@ -297,7 +302,9 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(const int32_t*
     for (int e = 0; e < 8; ++e) {
         const int place = 8 * tid + e;
         const uint32_t id = (uint32_t)(k[e] >> SHIFT);
-        if (chunks > 1) {
+        if (chunks >= kMergeFrom) {   // 64-bit keys: the token in the place of its chunk's one
+            static_cast<K*>(g.keys)[base + place] = k[e] + (K)base;
+        } else if (chunks > 1) {
             static_cast<K*>(g.keys)[base + place] = k[e];
         } else if (id != Key<K>::PAST) {
             g.token[place] = (int)((uint32_t)k[e] & (kChunk - 1));
@@ -340,6 +347,73 @@ __global__ __launch_bounds__(256) void embed_rank_kernel(int chunks, GradTables 
         return;
     g.token[rank] = c * kChunk + (int)((uint32_t)key & (kChunk - 1));
     g.id[rank] = id == kOutside<K> ? -1 : (int32_t)id;
+}
+
+// One pass over sorted runs of `run` keys (whole chunks; the last may be shorter):
+// runs 2 i and 2 i + 1 become one. All keys differ. A block makes one chunk of
+// the result: how much of it comes from either run is found by bisection on the
+// diagonal, those keys come to LDS, and each one's place there is its own plus
+// the count of smaller keys of the other part. The last pass leaves the tokens
+// and ids that the sums read. Ranking every key against every chunk takes time
+// as the square of the chunks. The whole gradient of 64 columns: 2^17 tokens (64
+// chunks) 111 us so, 143 by merging in six passes; 2^18 203 and 186; 2^20 1616 and
+// 382; at 2^29, the most a call takes, a ranking would run for minutes.
+template <bool LAST>
+__global__ __launch_bounds__(256) void embed_merge_kernel(const uint64_t* __restrict__ in, uint64_t* __restrict__ out,
+                                                          int64_t total, int64_t run, GradTables g)
+{
+    __shared__ uint64_t part[kChunk];
+    const int tid = (int)threadIdx.x;
+    const int64_t at = (int64_t)blockIdx.x * kChunk;          // the result's chunk
+    const int64_t a0 = at / (2 * run) * (2 * run);            // the pair's runs: from a0 and b0, la and lb long
+    const int64_t la = total - a0 < run ? total - a0 : run, b0 = a0 + la;
+    const int64_t lb = total - b0 < run ? total - b0 : run;
+    // Of the first d keys of the merged pair, those of its first run.
+    auto taken = [&](int64_t d) {
+        int64_t lo = d > lb ? d - lb : 0, hi = d < la ? d : la;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) / 2;
+            if (in[a0 + mid] < in[b0 + d - 1 - mid])
+                lo = mid + 1;
+            else
+                hi = mid;
+        }
+        return lo;
+    };
+    const int64_t d0 = at - a0, i0 = taken(d0), i1 = taken(d0 + kChunk);
+    const int na = (int)(i1 - i0);
+    const int64_t j0 = d0 - i0;
+#pragma unroll
+    for (int e = 0; e < kChunk / 256; ++e) {
+        const int x = tid + 256 * e;
+        part[x] = x < na ? in[a0 + i0 + x] : in[b0 + j0 + (x - na)];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kChunk / 256; ++e) {
+        const int x = tid + 256 * e;
+        const uint64_t key = part[x];
+        int lo = x < na ? na : 0;                             // count the other part's smaller keys
+        const int from = lo;
+        int hi = x < na ? kChunk : na;
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (part[mid] < key)
+                lo = mid + 1;
+            else
+                hi = mid;
+        }
+        const int64_t place = at + (x < na ? x : x - na) + (lo - from);
+        if constexpr (LAST) {
+            const uint32_t id = (uint32_t)(key >> Key<uint64_t>::SHIFT);
+            if (id != Key<uint64_t>::PAST) {
+                g.token[place] = (int32_t)(uint32_t)key;
+                g.id[place] = id == kOutside<uint64_t> ? -1 : (int32_t)id;
+            }
+        } else {
+            out[place] = key;
+        }
+    }
 }
 
 // Wave: the places of window w, 512 columns (lane l columns 8 l .. 8 l + 7 of
@@ -523,10 +597,25 @@ template <int BITS, int DT> hipError_t grad(const EmbedGradArgs& a, hipStream_t 
                            g, static_cast<char*>(a.dscales), static_cast<char*>(a.dbiases), zbytes);
         if (hipError_t e = hipGetLastError(); e != hipSuccess || chunks <= 1)
             return e;
+        if (chunks >= kMergeFrom) {
+            const int64_t total = (int64_t)chunks * kChunk;
+            uint64_t *in = static_cast<uint64_t*>(g.keys), *out = g.merged;
+            for (int64_t run = kChunk; run < total; run *= 2) {
+                if (2 * run < total)
+                    hipLaunchKernelGGL(embed_merge_kernel<false>, dim3(chunks), dim3(256), 0, st, in, out, total, run, g);
+                else
+                    hipLaunchKernelGGL(embed_merge_kernel<true>, dim3(chunks), dim3(256), 0, st, in, out, total, run, g);
+                if (hipError_t e = hipGetLastError(); e != hipSuccess)
+                    return e;
+                std::swap(in, out);
+            }
+            return hipSuccess;
+        }
         hipLaunchKernelGGL(embed_rank_kernel<K>, dim3((unsigned)chunks * (kChunk / 256)), dim3(256), 0, st, chunks, g);
         return hipGetLastError();
     };
-    if (hipError_t e = a.V < Key<uint32_t>::PAST ? order(uint32_t{}) : order(uint64_t{}); e != hipSuccess || a.T == 0)
+    const bool narrow = a.V < Key<uint32_t>::PAST && chunks < kMergeFrom;
+    if (hipError_t e = narrow ? order(uint32_t{}) : order(uint64_t{}); e != hipSuccess || a.T == 0)
         return e;
     const int64_t windows = window_count(a.T), items = windows * ((a.K / 8 + 63) / 64);
     hipLaunchKernelGGL((embed_sum_kernel<BITS, DT>), wide_grid((items + 3) / 4, 256), dim3(256), 0, st, a, g,
