@@ -324,3 +324,23 @@ def test_backward_far_preactivations_against_the_formula(m, d, f, dt, act):
     for y, (ref, bound), name in zip(outs, backward_ref(c, saved, act), names):
         assert torch.isfinite(ref).all() and torch.isfinite(bound).all()
         oh.check(y, ref, bound, f"far {name}")
+
+
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("m,d,f", [(40, 256, 448), (300, 1024, 640), (5, 4096, 96)])
+def test_backward_alignment_changes_nothing(m, d, f, dt):
+    c = case(m, d, f, 4, 32, dt)
+    saved = saved_of(c)
+    want = run_backward(c, saved, "silu")
+
+    def off(t):
+        flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=dev())
+        flat[1:] = t.reshape(-1).to(dev())
+        return flat[1:].view(t.shape)
+
+    ws = [tuple(off(t) for t in c[n]) for n in ("gate", "up", "down")]
+    log(f"qffn_backward at other addresses: m={m} d={d} f={f} dt={dt}")
+    got = qp.qffn_backward(off(c["x"]), off(c["dy"]), off(saved), *ws, c["bits"], c["gs"], act="silu")
+    torch.cuda.synchronize()
+    assert oh.same_bits(got[0], want[0])
+    assert all(oh.same_bits(a, b) for p, q in zip(got[1:], want[1:]) for a, b in zip(p, q))

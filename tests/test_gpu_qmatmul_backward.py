@@ -155,3 +155,27 @@ def test_against_differences(bits, gs):
         fd = (loss(*up) - loss(*down)) / (2 * eps)
         got = float((out[i].cpu().double() * dirs[i]).sum())
         assert abs(got - fd) <= float((bound * dirs[i].abs()).sum()) + 1e-9 * mag / eps, (i, got, fd)
+
+
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("m,k,n", [(70, 256, 96), (130, 512, 265), (300, 512, 264), (33, 4096, 4160)])
+def test_alignment_changes_nothing(m, k, n, dt):
+    """One kernel for a shape: the same bits wherever the operands lie, all of them off
+    16-byte addresses or one alone (the input gradient does not read x at all)."""
+    x, dy, w = case(m, k, n, 4, 32, dt)
+    wd = oh.cuda(w)
+
+    def shifted(t):
+        flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=dev())
+        flat[1:] = t.flatten().to(dev())
+        return flat[1:].view(t.shape)
+
+    xd, dyd = x.to(dev()), dy.to(dev())
+    want = qp.qmatmul_backward(xd, dyd, *wd, 4, 32)
+    log(f"qmatmul_backward at other addresses: m={m} k={k} n={n} dt={dt}")
+    for xx, yy, ww in ((shifted(x), dyd, wd), (xd, shifted(dy), wd),
+                       (shifted(x), shifted(dy), tuple(shifted(t) for t in wd))):
+        got = qp.qmatmul_backward(xx, yy, *ww, 4, 32)
+        only_x = qp.qmatmul_backward(xx, yy, *ww, 4, 32, weight_grads=False)
+        torch.cuda.synchronize()
+        assert all(oh.same_bits(a, b) for a, b in zip(got, want)) and oh.same_bits(only_x[0], want[0])

@@ -80,6 +80,22 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restric
     }
 }
 
+// The tile kernels read 16-bit rows in 16-byte pieces: rows p [m, n] as they lie
+// where they are such, else in a copy at `to`, zeros between; *stride their distance.
+hipError_t pieces_of_rows(const void*& p, int64_t m, int64_t n, char* to, int64_t* stride, hipStream_t st)
+{
+    *stride = n;
+    if (n % 8 == 0 && aligned16(p))
+        return hipSuccess;
+    *stride = up8(n);
+    const unsigned blocks = (unsigned)std::min<int64_t>((m * (*stride / 8) + 255) / 256, 16384);
+    hipLaunchKernelGGL(pad_rows_kernel, dim3(blocks), dim3(256), 0, st, static_cast<const uint16_t*>(p), m, n, *stride,
+                       reinterpret_cast<uint16_t*>(to));
+    p = to;
+    return hipGetLastError();
+}
+size_t piece_bytes(int64_t m, int64_t n) { return up16((size_t)m * (size_t)up8(n) * 2); }
+
 // Zeros for a weight's gradients (no rows to sum over).
 hipError_t zero_grads(void* ds, void* db, int dt, int64_t count, hipStream_t st)
 {
@@ -92,14 +108,13 @@ hipError_t zero_grads(void* ds, void* db, int dt, int64_t count, hipStream_t st)
 
 } // namespace
 
-// The partial sums of one product at a time, then (16-bit rows that are not
-// whole 16-byte pieces) dy in padded rows.
+// Room for copies of dy and x, then the partial sums of one product at a time.
 size_t linear_grad_workspace_bytes(int64_t m, int64_t k, int64_t n, int gs, int dt)
 {
     if (m == 0 || k == 0 || n == 0)
         return 0;
-    const size_t pad = dt != DT_F32 && n % 8 != 0 ? (size_t)m * (size_t)up8(n) * 2 : 0;
-    return up16(std::max(xgrad_bytes(m, n, k, 1), wgrad_bytes(m, n, k, 1, gs))) + pad;
+    return (tile_sizes(n, k, dt) ? piece_bytes(m, n) + piece_bytes(m, k) : 0) +
+           std::max(xgrad_bytes(m, n, k, 1), wgrad_bytes(m, n, k, 1, gs));
 }
 
 hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t st)
@@ -111,21 +126,20 @@ hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t st)
                 return e;
         return zero_grads(a.dscales, a.dbiases, a.dt, N * (K / a.gs), st);
     }
-    const void* dy = a.dy;
-    int64_t stride = N;
-    bool tiles = tile_sizes(N, K, a.dt) && aligned16(a.x);
-    if (tiles && N % 8 != 0) {
-        uint16_t* const pad = reinterpret_cast<uint16_t*>(
-            static_cast<char*>(a.workspace) + up16(std::max(xgrad_bytes(M, N, K, 1), wgrad_bytes(M, N, K, 1, a.gs))));
-        stride = up8(N);
-        const unsigned blocks = (unsigned)std::min<int64_t>((M * (stride / 8) + 255) / 256, 16384);
-        hipLaunchKernelGGL(pad_rows_kernel, dim3(blocks), dim3(256), 0, st, static_cast<const uint16_t*>(a.dy), M, N,
-                           stride, pad);
-        if (hipError_t e = hipGetLastError(); e != hipSuccess)
+    const void *dy = a.dy, *xs = a.x;
+    int64_t stride = N, xstride = K;
+    const bool tiles = tile_sizes(N, K, a.dt);
+    char* room = static_cast<char*>(a.workspace);
+    if (tiles) {
+        if (hipError_t e = pieces_of_rows(dy, M, N, room, &stride, st); e != hipSuccess)
             return e;
-        dy = pad;
+        room += piece_bytes(M, N);
+        if (a.dscales != nullptr)   // x is not read otherwise
+            if (hipError_t e = pieces_of_rows(xs, M, K, room, &xstride, st); e != hipSuccess)
+                return e;
+        room += piece_bytes(M, K);
     }
-    tiles = tiles && aligned16(dy);
+    float* const partial = reinterpret_cast<float*>(room);
     if (a.dx != nullptr) {
         XgradArgs x{};
         x.dy[0] = x.dy[1] = dy;
@@ -136,14 +150,14 @@ hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t st)
         x.M = M; x.N = N; x.K = K;
         x.bits = a.bits; x.gs = a.gs;
         x.out = a.dx;
-        x.partial = static_cast<float*>(a.workspace);
+        x.partial = partial;
         if (hipError_t e = xgrad(x, xgrad_plan(M, N, K, 1, tiles && averages(N)), st); e != hipSuccess)
             return e;
     }
     if (a.dscales == nullptr)
         return hipSuccess;
     WgradArgs w{};
-    w.x = a.x;
+    w.x = xs;
     w.dy[0] = w.dy[1] = dy;
     w.dy_stride = stride;
     w.wq[0] = w.wq[1] = a.w.wq;
@@ -153,11 +167,12 @@ hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t st)
     w.bits = a.bits; w.gs = a.gs;
     w.dscales[0] = a.dscales;
     w.dbiases[0] = a.dbiases;
-    w.partial = static_cast<float*>(a.workspace);
+    w.partial = partial;
     return wgrad(w, wgrad_plan(M, N, K, 1, a.gs, tiles), st);
 }
 
-// dg, du and h, then the partial sums of one product at a time.
+// dg, du and h, room for copies of dy and x, then the partial sums of one product
+// at a time.
 size_t ffn_grad_workspace_bytes(int64_t m, int64_t d, int64_t f, int gs, int dt)
 {
     if (m == 0 || d == 0 || f == 0)
@@ -165,7 +180,8 @@ size_t ffn_grad_workspace_bytes(int64_t m, int64_t d, int64_t f, int gs, int dt)
     size_t part = std::max(xgrad_bytes(m, d, f, 1), xgrad_bytes(m, f, d, 2));
     part = std::max(part, std::max(wgrad_bytes(m, f, d, 2, gs), wgrad_bytes(m, f, d, 1, gs)));
     part = std::max(part, wgrad_bytes(m, d, f, 1, gs));
-    return 3 * up16((size_t)m * (size_t)f * elem_size(dt)) + part;
+    return 3 * up16((size_t)m * (size_t)f * elem_size(dt)) +
+           (tile_sizes(d, f, dt) ? 2 * piece_bytes(m, d) : 0) + part;
 }
 
 hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t st)
@@ -186,14 +202,26 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t st)
     char* const dg = static_cast<char*>(a.workspace);
     char* const du = dg + step;
     char* const h = du + step;
-    float* const partial = reinterpret_cast<float*>(h + step);
+    char* room = h + step;
 
-    const bool sizes = tile_sizes(D, F, a.dt), dy_tiles = sizes && aligned16(a.dy);
+    const bool tiles = tile_sizes(D, F, a.dt);
+    const void *dy = a.dy, *xs = a.x;
+    if (tiles) {
+        int64_t stride = D;   // whole pieces: it stays
+        if (hipError_t e = pieces_of_rows(dy, M, D, room, &stride, st); e != hipSuccess)
+            return e;
+        room += piece_bytes(M, D);
+        if (a.dgate[0] != nullptr || a.dup[0] != nullptr)   // x is not read otherwise
+            if (hipError_t e = pieces_of_rows(xs, M, D, room, &stride, st); e != hipSuccess)
+                return e;
+        room += piece_bytes(M, D);
+    }
+    float* const partial = reinterpret_cast<float*>(room);
 
     XgradArgs x{};
     x.dt = a.dt; x.act = a.act; x.M = M; x.bits = a.bits; x.gs = a.gs;
     x.partial = partial;
-    x.dy[0] = x.dy[1] = a.dy;
+    x.dy[0] = x.dy[1] = dy;
     x.dy_stride = D;
     x.w[0] = x.w[1] = a.down;
     x.nmat = 1;
@@ -202,7 +230,7 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t st)
     x.u = static_cast<const char*>(a.saved) + mf;
     x.dg = dg; x.du = du;
     x.h = a.ddown[0] != nullptr ? h : nullptr;
-    if (hipError_t e = xgrad(x, xgrad_plan(M, D, F, 1, dy_tiles && averages(D)), st); e != hipSuccess)
+    if (hipError_t e = xgrad(x, xgrad_plan(M, D, F, 1, tiles && averages(D)), st); e != hipSuccess)
         return e;
     if (a.dx != nullptr) {
         x.g = x.u = nullptr;
@@ -212,13 +240,13 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t st)
         x.nmat = 2;
         x.N = F; x.K = D;
         x.out = a.dx;
-        if (hipError_t e = xgrad(x, xgrad_plan(M, F, D, 2, sizes && averages(F)), st); e != hipSuccess)
+        if (hipError_t e = xgrad(x, xgrad_plan(M, F, D, 2, tiles && averages(F)), st); e != hipSuccess)
             return e;
     }
     WgradArgs w{};
     w.dt = a.dt; w.M = M; w.bits = a.bits; w.gs = a.gs;
     w.partial = partial;
-    w.x = a.x;
+    w.x = xs;
     w.N = F; w.K = D;
     w.dy_stride = F;
     w.nmat = 0;
@@ -234,7 +262,7 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t st)
     add(dg, a.gate, a.dgate);
     add(du, a.up, a.dup);
     if (w.nmat > 0)
-        if (hipError_t e = wgrad(w, wgrad_plan(M, F, D, w.nmat, a.gs, sizes && aligned16(a.x)), st); e != hipSuccess)
+        if (hipError_t e = wgrad(w, wgrad_plan(M, F, D, w.nmat, a.gs, tiles), st); e != hipSuccess)
             return e;
     if (a.ddown[0] == nullptr)
         return hipSuccess;
@@ -242,8 +270,8 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t st)
     w.N = D; w.K = F;
     w.dy_stride = D;
     w.nmat = 0;
-    add(static_cast<const char*>(a.dy), a.down, a.ddown);
-    return wgrad(w, wgrad_plan(M, D, F, 1, a.gs, dy_tiles), st);
+    add(static_cast<const char*>(dy), a.down, a.ddown);
+    return wgrad(w, wgrad_plan(M, D, F, 1, a.gs, tiles), st);
 }
 
 } // namespace qp
