@@ -399,7 +399,7 @@ __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPla
 // nw + 32 j + lane % 32: unit i of the wave's four. All the codes are asked
 // for before any is used; a unit is moved down by the half's four codes once.
 template <int BITS, int DT, int FN, bool WIDE = false>
-__device__ __forceinline__ void wgrad_close(const WgradArgs& a, const GradPlan& plan, int mat, int split, int64_t kw,
+__device__ __forceinline__ void wgrad_close(const WgradArgs& a, int splits, int mat, int split, int64_t kw,
                                             int64_t nw, int lane, const f32x16_t (&acc)[4][FN])
 {
     // Opaque here, so that the addresses are formed at the tile's end and not
@@ -463,7 +463,7 @@ __device__ __forceinline__ void wgrad_close(const WgradArgs& a, const GradPlan& 
     // Lanes 0-31 store the scales' sums, lanes 32-63 the biases'.
     using St = typename Elem<DT>::storage;
     const int64_t groups = a.K / a.gs, count = a.N * groups, at = (nw + (lane & 31)) * groups + kw / a.gs;
-    const bool parts = plan.splits > 1;
+    const bool parts = splits > 1;
     float* const pd = parts ? a.partial + (((int64_t)split * a.nmat + mat) * 2 + half) * count + at : nullptr;
     St* const sd = parts ? nullptr : static_cast<St*>(half ? a.dbiases[mat] : a.dscales[mat]) + at;
     const int per = a.gs / 32;                                      // units of a group
@@ -604,7 +604,7 @@ __global__ __launch_bounds__(2 * BN) void wgrad_tile_kernel(WgradArgs a, GradPla
             run_step(kt + 1, std::integral_constant<int, 1>{});
     }
 
-    wgrad_close<BITS, DT, FN>(a, plan, mat, (int)blockIdx.y, k0 + 128 * wk, n0 + wn * WN, lane, acc);
+    wgrad_close<BITS, DT, FN>(a, plan.splits, mat, (int)blockIdx.y, k0 + 128 * wk, n0 + wn * WN, lane, acc);
 }
 
 // The same product with four waves of 128 k x 128 n, one on each SIMD: a
@@ -618,9 +618,9 @@ __global__ __launch_bounds__(2 * BN) void wgrad_tile_kernel(WgradArgs a, GradPla
 // The blocks are persistent (one a CU) and the pipeline runs on from one tile
 // to the next: loads and turning are two steps and one step ahead of the
 // products, in whatever tile that is, so only the sums at a tile's end stand
-// still.
+// still. There are tiles for every CU (wgrad_plan), so the contraction is whole.
 struct WideItem {
-    int mat, split, kt, hi;   // weight, piece of the contraction, next step, its end
+    int mat, kt;   // weight, next step
     int64_t n0, k0;
 };
 
@@ -635,7 +635,7 @@ __device__ __forceinline__ void band_order(int tile, int tiles_n, int tiles_k, i
 }
 
 template <int BITS, int DT>
-__global__ __launch_bounds__(256) void wgrad_wide_kernel(WgradArgs a, GradPlan plan, int tiles_n, int tiles_k)
+__global__ __launch_bounds__(256) void wgrad_wide_kernel(WgradArgs a, int tiles_n, int tiles_k)
 {
     using T = MfmaTraits<DT>;
     using frag_t = typename T::frag_t;
@@ -648,22 +648,20 @@ __global__ __launch_bounds__(256) void wgrad_wide_kernel(WgradArgs a, GradPlan p
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wk = wave >> 1, wn = wave & 1;
     const int steps = (int)((a.M + STEP - 1) / STEP);
-    // Items: tiles of every weight, split by split, XCD by XCD.
-    const int tiles = tiles_n * tiles_k, items = tiles * a.nmat * plan.splits, per_xcd = (items + 7) / 8;
+    // Items: tiles of every weight, XCD by XCD.
+    const int tiles = tiles_n * tiles_k, items = tiles * a.nmat, per_xcd = (items + 7) / 8;
     const int local = (int)(blockIdx.x / 8), stride = (int)(gridDim.x / 8), first = (int)(blockIdx.x % 8) * per_xcd;
     auto item_at = [&](int round, WideItem& it) {
         const int l = local + round * stride;
         if (l >= per_xcd || first + l >= items)
             return false;
-        const int i = first + l, t = i % (tiles * a.nmat);
-        it.split = i / (tiles * a.nmat);
-        it.mat = t / tiles;
+        const int i = first + l;
+        it.mat = i / tiles;
         int tn, tk;
-        band_order(t % tiles, tiles_n, tiles_k, tn, tk);
+        band_order(i % tiles, tiles_n, tiles_k, tn, tk);
         it.n0 = (int64_t)tn * BT;
         it.k0 = (int64_t)tk * BT;
-        it.kt = it.split * (int)plan.per_split;
-        it.hi = it.kt + (int)plan.per_split < steps ? it.kt + (int)plan.per_split : steps;
+        it.kt = 0;
         return true;
     };
     WideItem cur, ahead;   // the item being multiplied, and that being loaded
@@ -699,7 +697,7 @@ __global__ __launch_bounds__(256) void wgrad_wide_kernel(WgradArgs a, GradPlan p
         ry = uniform_rsrc(yp, rows * yrow);
     };
     auto set_item = [&]() {
-        const bool any = ahead.kt < ahead.hi;
+        const bool any = ahead.kt < steps;
         const int64_t m = any ? (int64_t)ahead.kt * STEP : 0;
         left = any ? a.M - m : 0;
         xp = static_cast<const char*>(a.x) + m * xrow;
@@ -710,14 +708,14 @@ __global__ __launch_bounds__(256) void wgrad_wide_kernel(WgradArgs a, GradPlan p
     set_item();
     int ahead_round = 0;
     auto advance = [&]() {   // the load cursor, one step on
-        if (++ahead.kt < ahead.hi) {
+        if (++ahead.kt < steps) {
             xp += (int64_t)STEP * xrow;
             yp += (int64_t)STEP * yrow;
             left -= STEP;
             set_rows();
         } else {
             if (!item_at(++ahead_round, ahead))
-                ahead.kt = ahead.hi = 0x3FFFFFFF;   // nothing left: loads read zeros
+                ahead.kt = 0x3FFFFFFF;   // nothing left: loads read zeros
             set_item();
         }
     };
@@ -765,7 +763,7 @@ __global__ __launch_bounds__(256) void wgrad_wide_kernel(WgradArgs a, GradPlan p
       f32x16_t acc[4][4];
       static_for<4>([&](auto I) { static_for<4>([&](auto J) { acc[I][J] = f32x16_t{}; }); });
 #pragma unroll 1
-      for (; cur.kt < cur.hi; ++cur.kt) {
+      for (; cur.kt < steps; ++cur.kt) {
         advance();
         static_for<4>([&](auto KK) {
             constexpr int kk = decltype(KK)::value;
@@ -798,7 +796,7 @@ __global__ __launch_bounds__(256) void wgrad_wide_kernel(WgradArgs a, GradPlan p
         stage = 1 - stage;
       }
       acc_settle();
-      wgrad_close<BITS, DT, 4, true>(a, plan, cur.mat, cur.split, cur.k0 + 128 * wk, cur.n0 + 128 * wn, lane, acc);
+      wgrad_close<BITS, DT, 4, true>(a, 1, cur.mat, 0, cur.k0 + 128 * wk, cur.n0 + 128 * wn, lane, acc);
     }
 }
 

@@ -31,7 +31,7 @@ hipError_t run_tile(const WgradArgs& a, const GradPlan& p, hipStream_t st)
 }
 
 template <int BITS, int DT>
-hipError_t run_wide(const WgradArgs& a, const GradPlan& p, hipStream_t st)
+hipError_t run_wide(const WgradArgs& a, hipStream_t st)
 {
     constexpr int BT = 256, LDS = gradtile::wgrad_lds<BT, BT>();
     const void* kern = reinterpret_cast<const void*>(&gradtile::wgrad_wide_kernel<BITS, DT>);
@@ -45,9 +45,9 @@ hipError_t run_wide(const WgradArgs& a, const GradPlan& p, hipStream_t st)
     if (hipError_t e = device_cu_count(&cus); e != hipSuccess)
         return e;
     const int64_t tiles_n = (a.N + BT - 1) / BT, tiles_k = (a.K + BT - 1) / BT;
-    const int64_t items = tiles_n * tiles_k * a.nmat * p.splits;
+    const int64_t items = tiles_n * tiles_k * a.nmat;
     const int64_t blocks = std::min<int64_t>((items + 7) / 8 * 8, std::max(cus / 8 * 8, 8));
-    hipLaunchKernelGGL((gradtile::wgrad_wide_kernel<BITS, DT>), dim3((unsigned)blocks), dim3(256), LDS, st, a, p,
+    hipLaunchKernelGGL((gradtile::wgrad_wide_kernel<BITS, DT>), dim3((unsigned)blocks), dim3(256), LDS, st, a,
                        (int)tiles_n, (int)tiles_k);
     return hipGetLastError();
 }
@@ -64,7 +64,7 @@ hipError_t run(const WgradArgs& a, const GradPlan& p, hipStream_t st)
                            dim3(256), 0, st, a, p);
         e = hipGetLastError();
     } else if constexpr (DT != DT_F32) {
-        e = p.tile == 1 ? run_wide<BITS, DT>(a, p, st) : run_tile<BITS, DT, 128>(a, p, st);
+        e = p.tile == 1 ? run_wide<BITS, DT>(a, st) : run_tile<BITS, DT, 128>(a, p, st);
     }
     if (e != hipSuccess)
         return e;
@@ -97,17 +97,16 @@ hipError_t QP_CAT(launch_wgrad_b, QP_BITS)(const WgradArgs& a, const GradPlan& p
 #if QP_BITS == 4
 // The wide kernel where its 256 x 256 tiles reach every CU: 2048 rows of a 14336
 // x 4096 weight 232 us, tiles of 128 304; 1024 rows of 4096 x 2048 (128 tiles)
-// 27.2 and 25.4. Pieces of the rows, at least four steps each, until there are
-// one (wide) or two blocks a CU.
+// 27.2 and 25.4. The others in pieces of the rows, at least four steps each, until
+// there are two blocks a CU.
 GradPlan wgrad_plan(int64_t m, int64_t n, int64_t k, int nmat, int gs, bool tile_kernels)
 {
     GradPlan p{};
     auto count = [&](int64_t b) { return nmat * ((n + b - 1) / b) * ((k + b - 1) / b); };
     p.tile = !tile_kernels ? 0 : count(256) >= 256 ? 1 : 2;
-    const int64_t step = p.tile == 0 ? WG_M : gradtile::STEP, want = p.tile == 1 ? 256 : 512;
-    const int64_t tiles = std::max<int64_t>(count(p.tile == 1 ? 256 : 128), 1);
-    const int64_t steps = (m + step - 1) / step;
-    const int64_t splits = std::clamp<int64_t>(std::min(want / tiles, steps / 4), 1, 64);
+    const int64_t step = p.tile == 0 ? WG_M : gradtile::STEP, steps = (m + step - 1) / step;
+    const int64_t splits = p.tile == 1
+        ? 1 : std::clamp<int64_t>(std::min(512 / std::max<int64_t>(count(128), 1), steps / 4), 1, 64);
     p.per_split = std::max<int64_t>((steps + splits - 1) / splits, 1);
     p.splits = (int)std::max<int64_t>((steps + p.per_split - 1) / p.per_split, 1);
     p.partial_bytes = p.splits > 1 ? (size_t)p.splits * (size_t)nmat * 2 * (size_t)n * (size_t)(k / gs) * 4 : 0;
