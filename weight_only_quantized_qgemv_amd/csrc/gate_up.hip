@@ -93,12 +93,9 @@ hipError_t run_tiles(const GateUpArgs& a, hipStream_t st)
     static_assert(LDS <= 160 * 1024, "LDS budget");
     const void* kern = reinterpret_cast<const void*>(
         &gemm::qgemm_tile_kernel<BITS, DT, BM, BN, NT, WMW, 2, false, NA, NC>);
-    static bool attr_set = false;   // per instantiation; set before its first launch
-    if (!attr_set) {
-        if (hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, LDS); e != hipSuccess)
-            return e;
-        attr_set = true;
-    }
+    static std::atomic<uint64_t> lds{0};   // per instantiation
+    if (hipError_t e = allow_lds(lds, kern, LDS); e != hipSuccess)
+        return e;
     GemmArgs g{};
     g.x = a.x;
     g.wq[0] = a.gate.wq; g.scales[0] = a.gate.scales; g.biases[0] = a.gate.biases;
@@ -165,12 +162,9 @@ hipError_t run_split(const FfnSplitArgs& a, hipStream_t st)
     static_assert(LDS <= 160 * 1024, "LDS budget");
     const void* kern = reinterpret_cast<const void*>(
         &gemm::qgemm_tile_kernel<BITS, DT, BM, BN, NT, WMW, NMAT, false, NA, NC, 0, true>);
-    static bool attr_set = false;   // per instantiation; set before its first launch
-    if (!attr_set) {
-        if (hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, LDS); e != hipSuccess)
-            return e;
-        attr_set = true;
-    }
+    static std::atomic<uint64_t> lds{0};   // per instantiation
+    if (hipError_t e = allow_lds(lds, kern, LDS); e != hipSuccess)
+        return e;
     GemmArgs g{};
     g.x = a.x;
     for (int t = 0; t < 2; ++t) {

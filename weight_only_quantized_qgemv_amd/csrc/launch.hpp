@@ -35,6 +35,22 @@ inline hipError_t device_cu_count(int* cus)
     return e;
 }
 
+// Lets a kernel use so much dynamic LDS on the current device, asked of the runtime
+// once per kernel and device: `done` is the kernel's own record, one bit a device.
+inline hipError_t allow_lds(std::atomic<uint64_t>& done, const void* kern, int bytes)
+{
+    int dev = 0;
+    if (hipError_t e = hipGetDevice(&dev); e != hipSuccess)
+        return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;   // others are asked for every time
+    if (done.load(std::memory_order_acquire) & bit)
+        return hipSuccess;
+    if (hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes); e != hipSuccess)
+        return e;
+    done.fetch_or(bit, std::memory_order_release);
+    return hipSuccess;
+}
+
 // HIP counts a grid's threads along a dimension in 32 bits: a launch of 2^32 or
 // more runs a part of its blocks and reports success.
 constexpr int64_t kGridThreads = (int64_t(1) << 32) - 1;

@@ -121,16 +121,15 @@ hipError_t run_gemm_tiles(const MoeArgs& a, const MoeRouting& r, hipStream_t st)
     static_assert(LDS <= 160 * 1024, "LDS budget");
     const void* kern = reinterpret_cast<const void*>(
         &gemm::qgemm_tile_kernel<BITS, DT, BM, BN, NT, 1, NMAT, true, NA, NC>);
-    static bool attr_set = false; // per instantiation; set before its first launch
-    static int per_cu = 0;        // blocks of this kernel one CU holds at once
-    if (!attr_set) {
-        hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
-        if (e != hipSuccess)
+    static std::atomic<uint64_t> lds{0};   // per instantiation
+    if (hipError_t e = allow_lds(lds, kern, LDS); e != hipSuccess)
+        return e;
+    static std::atomic<int> held{0};       // blocks of this kernel one CU holds at once
+    int per_cu = held.load(std::memory_order_relaxed);
+    if (per_cu == 0) {
+        if (hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, kern, NT, LDS); e != hipSuccess)
             return e;
-        e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, kern, NT, LDS);
-        if (e != hipSuccess)
-            return e;
-        attr_set = true;
+        held.store(per_cu, std::memory_order_relaxed);
     }
     const int64_t P = a.n_tokens * a.top_k;
     GemmArgs g{};

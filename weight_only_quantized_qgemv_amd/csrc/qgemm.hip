@@ -20,13 +20,9 @@ hipError_t run_gemm(const GemvArgs& a, hipStream_t st)
     static_assert(LDS <= 160 * 1024, "LDS budget");
     const void* kern = reinterpret_cast<const void*>(
         &gemm::qgemm_tile_kernel<BITS, DT, BM, BN, NT, 2, 1, false, NA, NC>);
-    static bool attr_set = false; // per instantiation; set before its first launch
-    if (!attr_set) {
-        hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
-        if (e != hipSuccess)
-            return e;
-        attr_set = true;
-    }
+    static std::atomic<uint64_t> lds{0};   // per instantiation
+    if (hipError_t e = allow_lds(lds, kern, LDS); e != hipSuccess)
+        return e;
     GemmArgs g{};
     g.x = a.x;
     g.wq[0] = g.wq[1] = a.wq;
@@ -75,13 +71,9 @@ hipError_t run_gemm_mx(const GemvMxArgs& a, hipStream_t st)
     static_assert(LDS <= 160 * 1024, "LDS budget");
     const void* kern = reinterpret_cast<const void*>(
         &gemm::qgemm_tile_kernel<BITS, DT, BM, BN, NT, 2, 1, false, NA, NC, MODE>);
-    static bool attr_set = false; // per instantiation; set before its first launch
-    if (!attr_set) {
-        hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
-        if (e != hipSuccess)
-            return e;
-        attr_set = true;
-    }
+    static std::atomic<uint64_t> lds{0};   // per instantiation
+    if (hipError_t e = allow_lds(lds, kern, LDS); e != hipSuccess)
+        return e;
     GemmArgs g{};
     g.x = a.x;
     g.wq[0] = g.wq[1] = a.wq;

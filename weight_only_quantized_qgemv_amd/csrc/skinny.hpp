@@ -40,6 +40,7 @@
 #include "act.hpp"
 #include "codepair.hpp"
 #include "gemv_core.hpp"
+#include "launch.hpp"
 
 namespace qp {
 
@@ -695,19 +696,14 @@ __global__ __launch_bounds__(64 * kSkinnyMaxWaves) void qgemv_skinny_kernel(Gemv
 
 namespace qp {
 
-// Launch one instance (the LDS size is set once per instance).
+// Launch one instance (its LDS size is allowed once per instance and device).
 template <int BITS, int DT, int NMAT, int GU>
 hipError_t skinny_launch_one(const GemvKernelArgs& k, const SkinnyShape& sh, dim3 grid, hipStream_t st)
 {
-    static bool attr_set = false;   // per instantiation; set before its first launch
-    if (!attr_set) {
-        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&qgemv_skinny_kernel<BITS, DT, NMAT, GU>),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)skinny_lds_bytes(kSkinnyMaxWaves, NMAT));
-        if (e != hipSuccess)
-            return e;
-        attr_set = true;
-    }
+    static std::atomic<uint64_t> lds{0};   // per instantiation
+    if (hipError_t e = allow_lds(lds, reinterpret_cast<const void*>(&qgemv_skinny_kernel<BITS, DT, NMAT, GU>),
+                                 (int)skinny_lds_bytes(kSkinnyMaxWaves, NMAT)); e != hipSuccess)
+        return e;
     const int waves = sh.ks * sh.wr;
     hipLaunchKernelGGL((qgemv_skinny_kernel<BITS, DT, NMAT, GU>), grid, dim3(64 * waves),
                        skinny_lds_bytes(waves, NMAT), st, k, sh);

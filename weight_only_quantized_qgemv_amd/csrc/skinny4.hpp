@@ -349,15 +349,10 @@ __global__ __launch_bounds__(64 * kSkinnyMaxWaves) void qgemv_skinny4_kernel(Gem
 template <int BITS, int DT, int GU>
 hipError_t skinny4_launch_one(const GemvKernelArgs& k, const SkinnyShape& sh, dim3 grid, hipStream_t st)
 {
-    static bool attr_set = false;   // per instantiation; set before its first launch
-    if (!attr_set) {
-        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&qgemv_skinny4_kernel<BITS, DT, GU>),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)(kSkinnyMaxWaves * skinny4_wave_lds()));
-        if (e != hipSuccess)
-            return e;
-        attr_set = true;
-    }
+    static std::atomic<uint64_t> lds{0};   // per instantiation
+    if (hipError_t e = allow_lds(lds, reinterpret_cast<const void*>(&qgemv_skinny4_kernel<BITS, DT, GU>),
+                                 (int)(kSkinnyMaxWaves * skinny4_wave_lds())); e != hipSuccess)
+        return e;
     const int waves = sh.ks * sh.wr;
     hipLaunchKernelGGL((qgemv_skinny4_kernel<BITS, DT, GU>), grid, dim3(64 * waves), waves * skinny4_wave_lds(), st, k, sh);
     return hipGetLastError();

@@ -15,12 +15,9 @@ hipError_t run_tile(const WgradArgs& a, const GradPlan& p, hipStream_t st)
     constexpr int LDS = gradtile::wgrad_lds<BT, BT>();
     static_assert(LDS <= 160 * 1024, "LDS budget");
     const void* kern = reinterpret_cast<const void*>(&gradtile::wgrad_tile_kernel<BITS, DT, BT, BT>);
-    static bool attr_set = false;   // per instantiation; set before its first launch
-    if (!attr_set) {
-        if (hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, LDS); e != hipSuccess)
-            return e;
-        attr_set = true;
-    }
+    static std::atomic<uint64_t> lds{0};   // per instantiation
+    if (hipError_t e = allow_lds(lds, kern, LDS); e != hipSuccess)
+        return e;
     const int64_t tiles_k = (a.K + BT - 1) / BT, tiles = (a.N + BT - 1) / BT * tiles_k;
     const int per_xcd = (int)((tiles * a.nmat + 7) / 8);
     if (!grid_fits((int64_t)per_xcd * 8, 2 * BT))
@@ -35,12 +32,9 @@ hipError_t run_wide(const WgradArgs& a, hipStream_t st)
 {
     constexpr int BT = 256, LDS = gradtile::wgrad_lds<BT, BT>();
     const void* kern = reinterpret_cast<const void*>(&gradtile::wgrad_wide_kernel<BITS, DT>);
-    static bool attr_set = false;   // per instantiation; set before its first launch
-    if (!attr_set) {
-        if (hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, LDS); e != hipSuccess)
-            return e;
-        attr_set = true;
-    }
+    static std::atomic<uint64_t> lds{0};   // per instantiation
+    if (hipError_t e = allow_lds(lds, kern, LDS); e != hipSuccess)
+        return e;
     int cus = 0;
     if (hipError_t e = device_cu_count(&cus); e != hipSuccess)
         return e;

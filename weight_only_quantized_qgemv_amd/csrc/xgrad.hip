@@ -23,12 +23,9 @@ hipError_t run_tile(const XgradArgs& a, const GradPlan& p, hipStream_t st)
     constexpr int LDS = gradtile::xgrad_lds<BM, BN>();
     static_assert(LDS <= 160 * 1024, "LDS budget");
     const void* kern = reinterpret_cast<const void*>(&gradtile::xgrad_tile_kernel<BITS, DT, BM, BN, WMW>);
-    static bool attr_set = false;   // per instantiation; set before its first launch
-    if (!attr_set) {
-        if (hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, LDS); e != hipSuccess)
-            return e;
-        attr_set = true;
-    }
+    static std::atomic<uint64_t> lds{0};   // per instantiation
+    if (hipError_t e = allow_lds(lds, kern, LDS); e != hipSuccess)
+        return e;
     const int64_t tiles_k = (a.K + BN - 1) / BN, tiles = (a.M + BM - 1) / BM * tiles_k;
     const int per_xcd = (int)((tiles + 7) / 8);
     if (!grid_fits((int64_t)per_xcd * 8, 2 * BN))
