@@ -344,3 +344,31 @@ def test_backward_alignment_changes_nothing(m, d, f, dt):
     torch.cuda.synchronize()
     assert oh.same_bits(got[0], want[0])
     assert all(oh.same_bits(a, b) for p, q in zip(got[1:], want[1:]) for a, b in zip(p, q))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("dt", [F32, F16, BF16])
+def test_backward_single_pairs_through_the_c_abi(dt, act):
+    """Each weight's gradients asked for alone, with the pointers that they do not need null or
+    absent: the same bits as with everything, and the down pair's without the weights read."""
+    c = case(50, 256, 320, 4, 64, dt)
+    saved = saved_of(c).to(dev())
+    want = run_backward(c, saved.cpu(), act)
+    x, dy = c["x"].to(dev()), c["dy"].to(dev())
+    ws = [t for n in ("gate", "up", "down") for t in oh.cuda(c[n])]
+    work = torch.empty(qp.qffn_backward_workspace_bytes(50, 256, 320, 4, 64, x.dtype), dtype=torch.uint8, device=dev())
+    log(f"qffn_backward, one pair at a time: dt={dt} {act}")
+    for i in range(3):
+        pair = [torch.full_like(t, 7.0) for t in want[1 + i]]
+        grads = [None] * 6
+        grads[2 * i], grads[2 * i + 1] = (t.data_ptr() for t in pair)
+        # dh overwrites dg and du: with the down pair alone they stay as they were.
+        work.fill_(1)
+        qp.check(qp.lib().qffn_backward(
+            x.data_ptr() if i < 2 else None, dy.data_ptr(), saved.data_ptr(), dt, 50, 256, 320,
+            *[t.data_ptr() for t in ws], dt, 4, 64, qp.ACTS[act], None, *grads, work.data_ptr(), work.numel(), None))
+        torch.cuda.synchronize()
+        assert all(oh.same_bits(a, b) for a, b in zip(pair, want[1 + i])), i
+        mf = 50 * 320 * x.element_size()          # a multiple of 16: dg, then du
+        if i == 2:
+            assert (work[:2 * mf] == 1).all()

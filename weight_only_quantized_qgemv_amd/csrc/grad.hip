@@ -7,8 +7,10 @@
 // and of each dW only the sums that belong to the scales and biases.
 #include <algorithm>
 
+#include "act.hpp"
 #include "common.hpp"
 #include "model_ops.hpp"
+#include "xgrad.hpp"
 
 namespace qp {
 
@@ -95,6 +97,28 @@ hipError_t pieces_of_rows(const void*& p, int64_t m, int64_t n, char* to, int64_
     return hipGetLastError();
 }
 size_t piece_bytes(int64_t m, int64_t n) { return up16((size_t)m * (size_t)up8(n) * 2); }
+
+// h[i] = act(g[i]) u[i] as the close of dh forms it, for a call that asks for the
+// down projection's gradients alone: dh is not needed there.
+template <int DT>
+__global__ __launch_bounds__(256) void ffn_hidden_kernel(const void* g, const void* u, int act, int64_t n, void* h)
+{
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        float a, da;
+        act_grad_f32(act, load_elem<DT>(g, i), a, da);
+        store_elem<DT>(h, i, a * load_elem<DT>(u, i));
+    }
+}
+hipError_t hidden(int dt, const void* g, const void* u, int act, int64_t n, void* h, hipStream_t st)
+{
+    const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 16384);
+    switch (dt) {
+    case DT_F32: hipLaunchKernelGGL(ffn_hidden_kernel<DT_F32>, dim3(blocks), dim3(256), 0, st, g, u, act, n, h); break;
+    case DT_F16: hipLaunchKernelGGL(ffn_hidden_kernel<DT_F16>, dim3(blocks), dim3(256), 0, st, g, u, act, n, h); break;
+    default: hipLaunchKernelGGL(ffn_hidden_kernel<DT_BF16>, dim3(blocks), dim3(256), 0, st, g, u, act, n, h);
+    }
+    return hipGetLastError();
+}
 
 // Zeros for a weight's gradients (no rows to sum over).
 hipError_t zero_grads(void* ds, void* db, int dt, int64_t count, hipStream_t st)
@@ -230,7 +254,9 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t st)
     x.u = static_cast<const char*>(a.saved) + mf;
     x.dg = dg; x.du = du;
     x.h = a.ddown[0] != nullptr ? h : nullptr;
-    if (hipError_t e = xgrad(x, xgrad_plan(M, D, F, 1, tiles && averages(D)), st); e != hipSuccess)
+    const bool down_only = a.dx == nullptr && a.dgate[0] == nullptr && a.dup[0] == nullptr;
+    if (hipError_t e = down_only ? hidden(a.dt, x.g, x.u, a.act, M * F, h, st)
+                                 : xgrad(x, xgrad_plan(M, D, F, 1, tiles && averages(D)), st); e != hipSuccess)
         return e;
     if (a.dx != nullptr) {
         x.g = x.u = nullptr;
