@@ -339,7 +339,7 @@ namespace {
 // copies where they are not aligned, and one product's partial sums and
 // filled-up operands. The 16-bit kernels reach 2 GB of an operand: x, h and y
 // of more rows go in passes (70000 rows of d_ff 16384: two).
-struct FfnRoom {
+struct FfnRoom {   // (of sizes above zero)
     int64_t rows;
     size_t h, u, copies, partial;
 };
@@ -349,9 +349,9 @@ FfnRoom ffn_room(int64_t m, int64_t d, int64_t f, int dt)
     FfnRoom r{m, 0, 0, 0, 0};
     // Filled-up contractions always go in pieces: 4 bytes for each of g and u.
     const int64_t bytes = d % 64 != 0 || f % 64 != 0 ? 8 : 2;
-    if (dt != DT_F32 && m > 0) {
-        const int64_t most = (k2GB - 1) / (bytes * std::max<int64_t>(std::max(d, f), 1)) / 256 * 256;
-        r.rows = std::min(m, std::max<int64_t>(most, 256));
+    if (dt != DT_F32) {
+        const int64_t most = (k2GB - 1) / (bytes * std::max(d, f));
+        r.rows = std::min(m, most >= 256 ? most / 256 * 256 : std::max<int64_t>(most, 1));
         r.copies = up16((size_t)r.rows * (size_t)d * 2);
         if (m > 16 && !huge_weight(d, f))
             r.copies += 4 * up16((size_t)f * (size_t)(d / 32) * 2 + 2);   // groups of 32 have most
@@ -359,7 +359,7 @@ FfnRoom ffn_room(int64_t m, int64_t d, int64_t f, int dt)
     r.h = up16((size_t)r.rows * (size_t)f * es);
     r.u = dt == DT_F32 ? r.h : 0;
     // The last pass may be shorter, and its plans others.
-    for (const int64_t rows : {r.rows, m > 0 ? m - (m - 1) / r.rows * r.rows : 0}) {
+    for (const int64_t rows : {r.rows, m - (m - 1) / r.rows * r.rows}) {
         auto split = [](const FfnSplit& p) { return up16(p.partial_bytes) + p.pad_bytes; };
         size_t part = std::max(split(ffn_split(rows, d, f, 2, dt)), split(ffn_split(rows, f, d, 1, dt)));
         // ffn_any's products: every one of fp32; of 16 bits those that contract
@@ -436,6 +436,8 @@ hipError_t ffn_pass(FfnArgs a, const FfnRoom& room, hipStream_t st)
 
 size_t ffn_workspace_bytes(int64_t m, int64_t d, int64_t f, int dt)
 {
+    if (m == 0 || d == 0 || f == 0)
+        return 0;
     const FfnRoom r = ffn_room(m, d, f, dt);
     return r.h + r.u + r.copies + r.partial;
 }
