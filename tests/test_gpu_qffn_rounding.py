@@ -126,3 +126,18 @@ def test_more_rows_than_one_pass():
     # 257 and 129 in eight bits.
     assert (saved[0, :, f - 1] == 256.0).all() and (saved[1, :, f - 1] == 129.0 * sign).all()
     assert not saved[:, :, :f - 1].any()
+
+
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("bits,gs", [(4, 64), (3, 32), (8, 32)])
+@pytest.mark.parametrize("m", [1, 2, 5, 16, 40, 150])
+def test_alignment_changes_nothing(m, bits, gs, dt):
+    g = oh.rng(oh.seed_of(m, bits, gs, dt, "address"))
+    d, f = 384, 640
+    x = oh.normal((m, d), 1.0, dt, g)
+    ws = [oh.weight(n, k, bits, gs, dt, g) for n, k in ((f, d), (f, d), (d, f))]
+    log(f"block at other addresses m={m} bits={bits} gs={gs} dt={dt}")
+    y = qp.qffn(x.to(dev()), *(oh.cuda(w) for w in ws), bits, gs)
+    off = qp.qffn(shifted(x), *(tuple(shifted(t) for t in w) for w in ws), bits, gs)
+    torch.cuda.synchronize()
+    assert oh.same_bits(y, off)

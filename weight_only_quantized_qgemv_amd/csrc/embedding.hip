@@ -126,7 +126,6 @@ struct GradTables {
     int32_t* id;          // [T] their ids (-1: outside the table; these come last)
     float* partial;       // [2 windows][2 G]: of the run a window begins with, and of the one it ends with
 };
-size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 int64_t window_count(int64_t t) { return (t + kWindow - 1) / kWindow; }
 size_t tables(int64_t t, int64_t groups, char* p, GradTables* out)
 {
@@ -569,8 +568,6 @@ __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(EmbedGradArgs 
         }
     }
 }
-
-inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 template <int BITS, int DT> hipError_t lookup(const EmbedArgs& a, hipStream_t st)
 {

@@ -13,10 +13,6 @@ namespace qp {
 
 namespace {
 
-inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-size_t elem_size(int dt) { return dt == DT_F32 ? 4 : 2; }
-size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
-
 // fp32: h[i] = act(g[i]) u[i]; h may be g's own memory. (16-bit projections are
 // closed from their sums, before any rounding.)
 __global__ __launch_bounds__(256) void ffn_gate_kernel(const float* g, const float* u, int act, int64_t n, float* h)

@@ -17,7 +17,6 @@ namespace qp {
 
 namespace {
 
-inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 constexpr int64_t k2GB = int64_t(1) << 31;
 
 template <int BITS, int DT, int MT, int UPL, int KL>

@@ -16,9 +16,6 @@ namespace qp {
 
 namespace {
 
-size_t elem_size(int dt) { return dt == DT_F32 ? 4 : 2; }
-size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
-
 hipError_t xgrad(const XgradArgs& a, const GradPlan& p, hipStream_t st)
 {
     switch (a.bits) {
@@ -43,7 +40,6 @@ hipError_t wgrad(const WgradArgs& a, const GradPlan& p, hipStream_t st)
     return hipErrorInvalidValue;
 }
 
-inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 int64_t up8(int64_t n) { return (n + 7) & ~(int64_t)7; }
 
 // Whether the tile kernels' 32-bit offsets reach a tile's rows: rows of at

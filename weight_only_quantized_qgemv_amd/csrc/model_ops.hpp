@@ -10,6 +10,9 @@
 
 namespace qp {
 
+inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+inline size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
+
 // One packed weight [N, K] with its scales and biases.
 struct QWeight {
     const uint32_t* wq;     // [N, K*bits/32]

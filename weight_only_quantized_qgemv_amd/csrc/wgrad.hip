@@ -90,9 +90,11 @@ hipError_t QP_CAT(launch_wgrad_b, QP_BITS)(const WgradArgs& a, const GradPlan& p
 
 #if QP_BITS == 4
 // The wide kernel where its 256 x 256 tiles reach every CU: 2048 rows of a 14336
-// x 4096 weight 232 us, tiles of 128 304; 1024 rows of 4096 x 2048 (128 tiles)
-// 27.2 and 25.4. The others in pieces of the rows, at least four steps each, until
-// there are two blocks a CU.
+// x 4096 weight 227 us, tiles of 128 304; 1024 rows of 4096 x 2048 (128 tiles)
+// 27.2 and 25.4. So too where a second round is all but empty (4352 x 4096, 272
+// tiles: 2048 rows 107.5 and 107.3, 256 rows 28.8 and 25.9; 320 tiles 107.5 and
+// 113.1, 27.9 and 25.6). The others in pieces of the rows, at least four steps
+// each, until there are two blocks a CU.
 GradPlan wgrad_plan(int64_t m, int64_t n, int64_t k, int nmat, int gs, bool tile_kernels)
 {
     GradPlan p{};

@@ -14,6 +14,8 @@
 
 namespace qp {
 
+inline size_t elem_size(int dt) { return dt == DT_F32 ? 4 : 2; }
+
 template <int DT>
 __device__ __forceinline__ float load_elem(const void* p, int64_t i)
 {
