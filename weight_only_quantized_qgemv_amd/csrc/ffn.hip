@@ -1,7 +1,11 @@
 // ffn.hip — the dense gated feed-forward block over packed weights:
 //   h = act(x Wg^T) * (x Wu^T),   y = h Wd^T
 // (the block of qgemv_moe_ffn, ferrum-kernels src/stacked_expert.rs, with one
-// set of weights for every row).
+// set of weights for every row). h comes from the fp32 projections and is rounded
+// once to the activations' type, because it is the down projection's operand on
+// 16-bit instructions: with y's own rounding an error of 0.0023 of y's size in
+// bf16 against 64 bits (one row), where one rounding gives 0.0016; the tile
+// kernels' rounding of the weights makes it 0.0036.
 #include <algorithm>
 
 #include "act.hpp"
@@ -84,8 +88,8 @@ bool huge_weight(int64_t n, int64_t k) { return k + 32 >= k2GB / (n + 32); }
 
 // Whether ffn_any's kernel takes a product: the decode kernels, which qmatmul
 // runs such shapes on, stream the weights once for every few rows (fp32, 4096 x
-// 14336, 4-bit, the three products: 1 row 133 us against 165, 2 rows 227 against
-// 165, 32 rows 3890 against 174).
+// 14336, 4-bit, the three products: 1 row 131 us against 152, 2 rows 227 against
+// 152, 32 rows 3890 against 155).
 bool any_product(const FfnArgs& a, int64_t k, const QWeight& w, int64_t n)
 {
     if (a.dt == DT_F32)
@@ -269,8 +273,8 @@ hipError_t gate_up(const GateUpArgs& a, hipStream_t st, bool* done)
 
 // Tiles of 64 x 256 up to 128 rows, 256 x 128 beyond, and as many pieces as fill
 // the 256 CUs once, at least four steps each. 4096 x 14336, 4-bit, the whole
-// block, without pieces and with: 64 rows 254 and 74 us, 256 rows 277 and 126, 512
-// rows 354 and 210. Filling the CUs twice: 64 rows 83 us.
+// block, without pieces and with: 64 rows 254 and 70 us, 256 rows 277 and 124, 512
+// rows 354 and 205. Filling the CUs twice: 64 rows 83 us.
 // A contraction of whole 32-wide groups but not whole 64-wide steps (groups of 32
 // then) is filled up with zeros: x, the scales and the biases in a copy, the codes
 // where they lie, the next row's times zero, or (2 and 6 bits) in a copy too

@@ -24,8 +24,8 @@ constexpr int AN_N = 128, AN_K = 32;   // weight rows a block, k a step
 // 36 floats (16 lanes' 16-byte reads fall on all banks). Loads run D steps
 // ahead: four in the kernel for up to 32 rows, where the weights' latency shows,
 // one in that for 128, bound by the matrix instructions (16 FM of 64 cycles a
-// step). A 4096 x 14336 block in fp32, 4-bit: 2 to 32 rows 165 to 174 us, 128
-// rows 458, 2048 rows 5790 (125 TFLOP/s; a large fp32 library product reaches 150).
+// step). A 4096 x 14336 block in fp32, 4-bit: 2 to 32 rows 149 to 157 us, 128
+// rows 456, 2048 rows 5881 (123 TFLOP/s; a large fp32 library product reaches 154).
 template <int BITS, int DT, int FM, int D>
 __global__ __launch_bounds__(256) void ffn_any_kernel(FfnAnyArgs a)
 {

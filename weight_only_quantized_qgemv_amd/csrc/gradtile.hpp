@@ -22,8 +22,10 @@
 // Both are bound by the work beside the matrix instructions, which are busy 60
 // to 62% of the time: a step of 256 x 256 outputs has 2048 cycles of them on
 // each SIMD (and, with eight waves, as many of LDS reads and writes). 14336 x
-// 4096, 4-bit, bf16, 2048 / 4096 / 8192 rows: dx 231 / 403 / 822 us, dW 237 / 427
-// / 825 us (998 to 1194 TFLOP/s).
+// 4096, 4-bit, bf16, 2048 / 4096 / 8192 rows: dx 227 / 405 / 808 us, dW 225 / 425
+// / 831 us (1058 to 1190 TFLOP/s; a library's product of dense operands 205 / 336
+// / 685 us). The roundings of the weights here make dx 0.0023 of its size
+// off 64 bits in bf16, where its own rounding alone makes it 0.0017.
 #pragma once
 
 #include "codes8.hpp"
