@@ -64,3 +64,88 @@ def test_logits_of_more_than_2_23_rows():
     out = qp.qlogits_adjust(z, mask=mask)
     assert torch.equal(out[:, 1:31], z[:, 1:31])
     assert (out[:, 0] == float("-inf")).all() and (out[:, 31] == float("-inf")).all()
+
+
+def big_weight(n, k, gs, dt, entries):
+    """8-bit weights [n, k] of 2 GiB and more on the device: scale 1, bias 0, entries
+    (row, column, code)."""
+    q = torch.zeros((n, k), dtype=torch.uint8, device=dev())
+    for r, c, code in entries:
+        q[r, c] = code
+    one = torch.ones((n, k // gs), dtype=dt, device=dev())
+    return q.view(torch.int32), one, torch.zeros_like(one)
+
+
+@pytest.mark.parametrize("m", [1, 3, 20])
+def test_block_of_weights_of_2_gib(m):
+    """Weights past the 32-bit offsets of the tile and skinny kernels: exact numbers in the last
+    rows and columns (bf16: g = 257, u = 129, h = 33153, which rounds to 33152)."""
+    need(20)
+    d, f, gs, dt = 32768, 65600, 32, torch.bfloat16
+    log(f"block of 2 GiB weights, {m} rows")
+    x = torch.zeros((m, d), dtype=dt, device=dev())
+    x[:, d - 1] = x[:, d - 2] = 1
+    gate = big_weight(f, d, gs, dt, [(f - 1, d - 1, 255), (f - 1, d - 2, 2)])
+    up = big_weight(f, d, gs, dt, [(f - 1, d - 1, 127), (f - 1, d - 2, 2)])
+    down = big_weight(d, f, gs, dt, [(d - 1, f - 1, 1)])
+    saved = torch.empty((2, m, f), dtype=dt, device=dev())
+    for kept in (None, saved):
+        y = qp.qffn(x, gate, up, down, 8, gs, saved=kept)
+        torch.cuda.synchronize()
+        assert (y[:, d - 1] == 33152).all() and not y[:, :d - 1].any()
+    assert (saved[0, :, f - 1] == 256).all() and (saved[1, :, f - 1] == 129).all()
+    assert not saved[:, :, :f - 1].any()
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_gradients_and_lookup_of_a_weight_of_2_gib(dt):
+    need(20)
+    m, n, k, gs = 3, 65600, 32768, 32
+    log(f"gradients of a 2 GiB weight, {dt}")
+    w = big_weight(n, k, gs, dt, [(n - 1, k - 1, 255), (n - 1, 0, 3), (n - 2, 5, 7)])
+    x, dy = (torch.zeros((m, c), dtype=dt, device=dev()) for c in (k, n))
+    x[2, k - 1], x[2, 0], dy[2, n - 1] = 2, 1, 4
+    dx, ds, db = qp.qmatmul_backward(x, dy, *w, 8, gs)
+    torch.cuda.synchronize()
+    want = torch.zeros_like(dx)
+    want[2, k - 1], want[2, 0] = 1020, 12         # 4 times the last weight row
+    assert torch.equal(dx, want)
+    # dW's last row is 4 x[2]: 8 in the last column, 4 in the first.
+    for got, first, last in ((ds, 4 * 3, 8 * 255), (db, 4, 8)):
+        assert float(got[n - 1, 0]) == first and float(got[n - 1, -1]) == last
+        assert not got[:n - 1].any() and not got[n - 1, 1:-1].any()
+    ids = torch.tensor([n - 1, 0, n - 2], dtype=torch.int32, device=dev())
+    rows = qp.qembedding(ids, *w, 8, gs)
+    assert float(rows[0, k - 1]) == 255 and float(rows[0, 0]) == 3 and float(rows[2, 5]) == 7
+    assert int((rows != 0).sum()) == 3
+    ds, db = qp.qembedding_backward(ids, x, w[0], 8, gs)
+    torch.cuda.synchronize()
+    assert float(ds[n - 2, 0]) == 0 and float(db[n - 2, 0]) == 1 and float(db[n - 2, -1]) == 2
+    assert float(ds[n - 1, 0]) == 0 and not db[n - 1].any() and not db[:n - 2].any()
+
+
+def test_block_backward_past_2_gib():
+    """dg, du and h of more than 2 GiB each, every row the same: exact numbers everywhere."""
+    need(30)
+    m, d, f, gs, dt = 70000, 64, 16384, 64, torch.bfloat16
+    log(f"block backward, {m} rows of {f}")
+    gate = big_weight(f, d, gs, dt, [(f - 1, d - 1, 1)])
+    up = big_weight(f, d, gs, dt, [(f - 1, 0, 1)])
+    down = big_weight(d, f, gs, dt, [(5, f - 1, 1)])
+    x, dy = (torch.zeros((m, d), dtype=dt, device=dev()) for _ in range(2))
+    x[:, 3], dy[:, 5] = 1, 1
+    saved = torch.zeros((2, m, f), dtype=dt, device=dev())
+    saved[0, :, f - 1], saved[1, :, f - 1] = 256, 129     # act(256) = 256, act' = 1
+    dx, dgate, dup, ddown = qp.qffn_backward(x, dy, saved, gate, up, down, 8, gs)
+    torch.cuda.synchronize()
+    want = torch.zeros((d,), dtype=dt, device=dev())
+    want[d - 1], want[0] = 129, 256               # dg Wg + du Wu
+    assert torch.equal(dx, want.expand(m, d))
+    # Sums over the rows of dg, du and h, exact in fp32, at code 0 (and, down, code 1).
+    total = lambda v: float(torch.tensor(float(v * m)).to(dt))  # noqa: E731
+    for (ds, db), value in ((dgate, 129), (dup, 256)):
+        assert not ds.any() and float(db[f - 1, 0]) == total(value) and not db[:f - 1].any()
+    ds, db = ddown
+    h = 256 * 129                                 # 33024, exact in eight bits
+    assert float(ds[5, -1]) == total(h) and float(db[5, -1]) == total(h)
+    assert int((ds != 0).sum()) == 1 and int((db != 0).sum()) == 1
