@@ -503,6 +503,98 @@ qp_status qlogits_adjust(const void* logits, qp_dtype dtype, int64_t rows, int64
                          const int32_t* bias_offsets, const uint32_t* mask, int64_t mask_stride,
                          void* out, int64_t out_stride, hipStream_t stream);
 
+/*
+ * Softmax cross entropy over a packed head, without the logits:
+ *   z[i, v] = x[i] . W[v],  lse[i] = log sum_v exp(z[i, v]),
+ *   loss[i] = lse[i] - z[i, targets[i]]
+ *   x        device, x_dtype [m, k]; m up to 2^20, k up to 2^24
+ *   targets  device, int32 [m]; a target outside [0, vocab) is none: the row's
+ *            loss is 0, and it has no gradient
+ *   wq, scales, biases  device, the head [vocab, k] as in qmatmul
+ *   loss, lse  device, fp32 [m] (outputs)
+ *   workspace device, >= qcross_entropy_workspace_bytes(...), 16-byte aligned
+ * The logits are formed and reduced in fp32, in pieces of the vocabulary;
+ * nothing of them is rounded to 16 bits. vocab == 0: lse is -infinity. A row of x
+ * with an infinity or a NaN gives NaN in its own row. Deterministic.
+ */
+size_t qcross_entropy_workspace_bytes(int64_t m, int64_t k, int64_t vocab, int32_t bits, int32_t group_size,
+                                      qp_dtype dtype);
+qp_status qcross_entropy(const void* x, qp_dtype x_dtype, int64_t m, int64_t k, const int32_t* targets,
+                         const uint32_t* wq, const void* scales, const void* biases, qp_dtype sb_dtype,
+                         int64_t vocab, int32_t bits, int32_t group_size, float* loss, float* lse,
+                         void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of qcross_entropy, from the rows' upstream gradients dloss (1 / rows
+ * for a mean), with dW as in qffn_backward:
+ *   dz[i, v] = dloss[i] (exp(z[i, v] - lse[i]) - [v = targets[i]]),
+ *   dx = dz W,  dW = dz^T x
+ *   lse      device, fp32 [m], as qcross_entropy wrote it
+ *   dloss    device, fp32 [m]; not used for rows without a target
+ *   dx       device, x_dtype [m, k] (output), or null
+ *   dscales, dbiases  device, x_dtype [vocab, k/group_size] (outputs), or both null
+ *   workspace device, >= qcross_entropy_backward_workspace_bytes(...), 16-byte aligned
+ * The logits are formed again, a piece of the vocabulary at a time. dz is rounded
+ * to x_dtype as the products' operand (16-bit types: times a factor that makes the
+ * largest |dloss| 2^14, taken out of the sums again); everything else is fp32. Rows of x must be finite where there is no target too.
+ * Deterministic. m == 0 or vocab == 0 writes zeros.
+ */
+size_t qcross_entropy_backward_workspace_bytes(int64_t m, int64_t k, int64_t vocab, int32_t bits,
+                                               int32_t group_size, qp_dtype dtype);
+qp_status qcross_entropy_backward(const void* x, qp_dtype x_dtype, int64_t m, int64_t k, const int32_t* targets,
+                                  const float* lse, const float* dloss, const uint32_t* wq, const void* scales,
+                                  const void* biases, qp_dtype sb_dtype, int64_t vocab, int32_t bits,
+                                  int32_t group_size, void* dx, void* dscales, void* dbiases, void* workspace,
+                                  size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * What stands between two blocks of a model, in one pass over a row: the norm
+ * after a block, its gate, the residual sum and the norm before the next block,
+ *   t = y r(y) (post_weight + offset),   r(v) = 1 / sqrt(mean(v^2) + eps)
+ *   s = x + scale * gate * t,            a = s r(s) (weight + offset)
+ *   x        device, x_dtype [m, d]: the residual stream; m up to 2^22, d up to 16384
+ *   y        device, dtype [m, d]: the block's output; or null: s = x, not written
+ *   weight, post_weight  device, dtype [d]; a null one leaves its norm out (t = y;
+ *            no a). y or weight must be there
+ *   gate     device, dtype [gate_rows, d], or null (1); row i uses gate row
+ *            i / (m / gate_rows): 1 row for all, m one each, or a divisor of m, one
+ *            for each run of rows (a sequence)
+ *   offset   added to both weights (1 for weights stored around 0)
+ *   stream_out device, x_dtype [m, d] (output, with y); it may be x
+ *   out      device, dtype [m, d] (output, with weight); it may be y
+ * x_dtype is dtype, or QP_F32 (a stream kept in fp32). Everything is fp32 and
+ * rounded once at each output; a is formed from s before its rounding.
+ */
+qp_status qblock_norm(const void* x, qp_dtype x_dtype, int64_t m, int64_t d, const void* y, qp_dtype dtype,
+                      const void* weight, const void* post_weight, const void* gate, int64_t gate_rows,
+                      float scale, float offset, float eps, void* stream_out, void* out, hipStream_t stream);
+
+/*
+ * Gradients of qblock_norm, from ds (of s: what reaches it past the next block)
+ * and da (of a):
+ *   G = ds + the gradient of s through a,  dx = G,  dt = scale * gate * G,
+ *   dy and dpost_weight from dt through the post-norm,
+ *   dgate = sum of scale * t * G over a gate row's rows, dweight from da
+ *   s        device, s_dtype [m, d], as qblock_norm wrote it (x where there was no
+ *            y); read with weight only
+ *   ds       device, s_dtype [m, d], or null (zeros)
+ *   da       device, dtype [m, d] (with weight)
+ *   dx       device, s_dtype [m, d] (output); it may be ds
+ *   dy       device, dtype [m, d] (output, with y); it may be da or y
+ *   dweight, dpost_weight  device, dtype [d]; dgate [gate_rows, d] (outputs, with
+ *            what they are the gradients of)
+ *   workspace device, >= qblock_norm_backward_workspace_bytes(m, d, gate_rows; 0
+ *            without a gate), 16-byte aligned
+ * Sums over rows are fp32 in a fixed order: deterministic. m == 0 writes zeros to
+ * the sums.
+ */
+size_t qblock_norm_backward_workspace_bytes(int64_t m, int64_t d, int64_t gate_rows);
+qp_status qblock_norm_backward(const void* s, const void* ds, qp_dtype s_dtype, int64_t m, int64_t d,
+                               const void* da, const void* y, qp_dtype dtype, const void* weight,
+                               const void* post_weight, const void* gate, int64_t gate_rows, float scale,
+                               float offset, float eps, void* dx, void* dy, void* dweight, void* dpost_weight,
+                               void* dgate, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

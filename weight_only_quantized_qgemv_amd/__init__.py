@@ -16,6 +16,9 @@ Calls (same names as the C ABI):
     qmatmul_backward(x, dy, wq, scales, biases, ...) -> dx, dscales, dbiases
     qembedding(ids, wq, scales, biases, ...)       -> rows of a packed table, qembedding_backward
     qlogits_adjust(logits, ...)                    -> penalties, biases and masks on logits
+    qcross_entropy(x, targets, wq, scales, ...)    -> loss, lse over a packed head; qcross_entropy_backward
+    qblock_norm(x, y, weight, ...)                 -> norms, gate and residual sum around a block;
+                                                      qblock_norm_backward
 """
 from __future__ import annotations
 
@@ -39,6 +42,9 @@ EXPORTS = ("qpack_quantize", "qpack_dequantize", "qpack_dequantize_mx", "qmatmul
            "qmatmul_t", "qffn_workspace_bytes", "qffn", "qffn_backward_workspace_bytes",
            "qffn_backward", "qmatmul_backward_workspace_bytes", "qmatmul_backward", "qembedding",
            "qembedding_backward_workspace_bytes", "qembedding_backward", "qlogits_adjust",
+           "qcross_entropy_workspace_bytes", "qcross_entropy",
+           "qcross_entropy_backward_workspace_bytes", "qcross_entropy_backward", "qblock_norm",
+           "qblock_norm_backward_workspace_bytes", "qblock_norm_backward",
            "qpack_last_error",
            "qpack_version")
 
@@ -126,6 +132,23 @@ def lib() -> ctypes.CDLL:
         L.qlogits_adjust.argtypes = [P, CI, I64, I64, I64, P, I64, P, P, P, P, P, P, P, I64, P, P,
                                      I64, P, I64, P]
         L.qlogits_adjust.restype = CI
+        L.qcross_entropy_workspace_bytes.argtypes = [I64, I64, I64, I32, I32, CI]
+        L.qcross_entropy_workspace_bytes.restype = SZ
+        L.qcross_entropy.argtypes = [P, CI, I64, I64, P, P, P, P, CI, I64, I32, I32, P, P, P, SZ, P]
+        L.qcross_entropy.restype = CI
+        L.qcross_entropy_backward_workspace_bytes.argtypes = [I64, I64, I64, I32, I32, CI]
+        L.qcross_entropy_backward_workspace_bytes.restype = SZ
+        L.qcross_entropy_backward.argtypes = ([P, CI, I64, I64] + [P] * 6 + [CI, I64, I32, I32] +
+                                              [P] * 4 + [SZ, P])
+        L.qcross_entropy_backward.restype = CI
+        FL = ctypes.c_float
+        L.qblock_norm.argtypes = [P, CI, I64, I64, P, CI, P, P, P, I64, FL, FL, FL, P, P, P]
+        L.qblock_norm.restype = CI
+        L.qblock_norm_backward_workspace_bytes.argtypes = [I64, I64, I64]
+        L.qblock_norm_backward_workspace_bytes.restype = SZ
+        L.qblock_norm_backward.argtypes = ([P, P, CI, I64, I64, P, P, CI, P, P, P, I64, FL, FL, FL] +
+                                           [P] * 6 + [SZ, P])
+        L.qblock_norm_backward.restype = CI
         L.qpack_last_error.restype = ctypes.c_char_p
         L.qpack_version.restype = ctypes.c_char_p
         _lib = L
@@ -695,3 +718,156 @@ def qlogits_adjust(logits, history=None, offsets=None, prompt_lens=None, repetit
         ptr(frequency), ptr(presence), ptr(bids), ptr(bvals), 0 if bids is None else bids.numel(),
         ptr(boff), ptr(mask), mask_stride, ptr(out), out.stride(0), _stream(logits)))
     return out
+
+
+# ------------------------------------------------------------------ training and scoring
+
+def _check_head(x, targets, w, bits, group_size):
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be a contiguous [m, k] tensor")
+    _like(x, x, "x")
+    m, k = x.shape
+    v = w[0].shape[0]
+    dt = _check_packed(w, x, "head", v, k, bits, group_size)
+    _like(targets, x, "targets", (m,), torch.int32)
+    return m, k, v, dt
+
+
+def qcross_entropy_workspace_bytes(m: int, k: int, vocab: int, bits: int, group_size: int, dtype) -> int:
+    return int(lib().qcross_entropy_workspace_bytes(m, k, vocab, bits, group_size, dtype_code(dtype)))
+
+
+def qcross_entropy(x, targets, wq, scales, biases, bits: int, group_size: int, loss=None, lse=None,
+                   workspace=None):
+    """Softmax cross entropy of x [m, k] over a packed head [vocab, k], without the logits: (loss,
+    lse), fp32 [m] each; loss = lse - the logit of targets (int32 [m]), 0 where the target is
+    outside the vocabulary. lse is what qcross_entropy_backward takes."""
+    import torch
+    _dev(x, "x")
+    m, k, v, dt = _check_head(x, targets, (wq, scales, biases), bits, group_size)
+    out = [torch.empty(m, dtype=torch.float32, device=x.device) if t is None
+           else _like(t, x, name, (m,), torch.float32) for t, name in ((loss, "loss"), (lse, "lse"))]
+    workspace = _workspace(qcross_entropy_workspace_bytes(m, k, v, bits, group_size, x.dtype), x, workspace)
+    check(lib().qcross_entropy(_ptr(x), dtype_code(x.dtype), m, k, _ptr(targets), _ptr(wq), _ptr(scales),
+                               _ptr(biases), dtype_code(dt), v, bits, group_size, _ptr(out[0]), _ptr(out[1]),
+                               _ptr(workspace), _ws_bytes(workspace), _stream(x)))
+    return out[0], out[1]
+
+
+def qcross_entropy_backward_workspace_bytes(m: int, k: int, vocab: int, bits: int, group_size: int,
+                                            dtype) -> int:
+    return int(lib().qcross_entropy_backward_workspace_bytes(m, k, vocab, bits, group_size,
+                                                             dtype_code(dtype)))
+
+
+def qcross_entropy_backward(x, targets, lse, dloss, wq, scales, biases, bits: int, group_size: int,
+                            input_grad: bool = True, weight_grads: bool = True, workspace=None):
+    """Gradients of qcross_entropy at dloss (fp32 [m], the rows' own upstream gradients: 1 / m for a
+    mean over all rows): (dx, dscales, dbiases) in x's dtype, each None where it is not asked for."""
+    import torch
+    _dev(x, "x")
+    m, k, v, dt = _check_head(x, targets, (wq, scales, biases), bits, group_size)
+    _like(lse, x, "lse", (m,), torch.float32)
+    _like(dloss, x, "dloss", (m,), torch.float32)
+    dx = torch.empty((m, k), dtype=x.dtype, device=x.device) if input_grad else None
+    ds = db = None
+    if weight_grads:
+        ds, db = (torch.empty(scales.shape, dtype=x.dtype, device=x.device) for _ in range(2))
+    workspace = _workspace(qcross_entropy_backward_workspace_bytes(m, k, v, bits, group_size, x.dtype), x,
+                           workspace)
+    check(lib().qcross_entropy_backward(
+        _ptr(x), dtype_code(x.dtype), m, k, _ptr(targets), _ptr(lse), _ptr(dloss), _ptr(wq), _ptr(scales),
+        _ptr(biases), dtype_code(dt), v, bits, group_size, *[None if t is None else _ptr(t) for t in (dx, ds, db)],
+        _ptr(workspace), _ws_bytes(workspace), _stream(x)))
+    return dx, ds, db
+
+
+def _check_norm(x, y, weight, post_weight, gate):
+    """(m, d, the block's dtype, gate rows) of the norms' calls; x is the stream."""
+    if x.dim() != 2:
+        raise ValueError("the stream must be a contiguous [m, d] tensor")
+    _like(x, x, "the stream")
+    m, d = x.shape
+    if y is None and weight is None:
+        raise ValueError("neither a block's output nor a weight: nothing to do")
+    if y is None and (post_weight is not None or gate is not None):
+        raise ValueError("a post-norm or gate needs the block's output y")
+    dt = (y if y is not None else weight).dtype
+    if y is not None:
+        _like(y, x, "y", (m, d))
+    for t, name in ((weight, "weight"), (post_weight, "post_weight")):
+        if t is not None:
+            _like(t, x, name, (d,), dt)
+    rows = 0
+    if gate is not None:
+        if gate.dim() != 2:
+            raise ValueError("gate must be [rows, d]")
+        rows = gate.shape[0]
+        _like(gate, x, "gate", (rows, d), dt)
+    return m, d, dt, rows
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def qblock_norm(x, y=None, weight=None, post_weight=None, gate=None, scale: float = 1.0, offset: float = 0.0,
+                eps: float = 1e-6, stream=None, out=None):
+    """The norm after a block, its gate, the residual sum and the norm before the next block: with
+    rms(v) = sqrt(mean(v^2) + eps), t = y / rms(y) * (post_weight + offset) (t = y without
+    post_weight), s = x + scale * gate * t (s = x without y), a = s / rms(s) * (weight + offset).
+
+    x [m, d] is the residual stream, in y's dtype or fp32; weight and post_weight are [d]; gate is
+    [rows, d], each row for m / rows consecutive rows of x. Returns (s, a): s is x itself without y,
+    a is None without weight. stream=x and out=y work in place."""
+    import torch
+    _dev(x, "x")
+    m, d, dt, rows = _check_norm(x, y, weight, post_weight, gate)
+    if y is None:
+        if stream is not None:
+            raise ValueError("stream: without y the stream is x itself")
+        stream = x
+    elif stream is None:
+        stream = torch.empty_like(x)
+    else:
+        _like(stream, x, "stream", (m, d), x.dtype)
+    if weight is None:
+        if out is not None:
+            raise ValueError("out: without weight there is none")
+    elif out is None:
+        out = torch.empty((m, d), dtype=dt, device=x.device)
+    else:
+        _like(out, x, "out", (m, d), dt)
+    check(lib().qblock_norm(_ptr(x), dtype_code(x.dtype), m, d, _opt(y), dtype_code(dt), _opt(weight),
+                            _opt(post_weight), _opt(gate), rows, scale, offset, eps,
+                            _ptr(stream) if y is not None else None, _opt(out), _stream(x)))
+    return stream, out
+
+
+def qblock_norm_backward_workspace_bytes(m: int, d: int, gate_rows: int) -> int:
+    return int(lib().qblock_norm_backward_workspace_bytes(m, d, gate_rows))
+
+
+def qblock_norm_backward(s, da=None, ds=None, y=None, weight=None, post_weight=None, gate=None,
+                         scale: float = 1.0, offset: float = 0.0, eps: float = 1e-6, workspace=None):
+    """Gradients of qblock_norm: (dx, dy, dweight, dpost_weight, dgate), None for what was not there.
+    s is the stream that it returned, da the gradient of a (with weight), ds that of s (None:
+    zeros); the other arguments as in the forward call."""
+    import torch
+    _dev(s, "s")
+    m, d, dt, rows = _check_norm(s, y, weight, post_weight, gate)
+    if (da is None) != (weight is None):
+        raise ValueError("da, the gradient of a, goes with weight")
+    if da is not None:
+        _like(da, s, "da", (m, d), dt)
+    if ds is not None:
+        _like(ds, s, "ds", (m, d), s.dtype)
+    dx = torch.empty_like(s)
+    dy, dw, dp, dg = (None if t is None else torch.empty_like(t) for t in (y, weight, post_weight, gate))
+    workspace = _workspace(qblock_norm_backward_workspace_bytes(m, d, rows), s, workspace)
+    check(lib().qblock_norm_backward(
+        _ptr(s), _opt(ds), dtype_code(s.dtype), m, d, _opt(da), _opt(y), dtype_code(dt), _opt(weight),
+        _opt(post_weight), _opt(gate), rows, scale, offset, eps, _ptr(dx), _opt(dy), _opt(dw), _opt(dp),
+        _opt(dg), _ptr(workspace), _ws_bytes(workspace), _stream(s)))
+    return dx, dy, dw, dp, dg

@@ -11,53 +11,7 @@ using namespace qp::api;
 
 namespace {
 
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;   // sizes are below 2^31
-
 bool act_ok(int a) { return a == QP_SILU || a == QP_GELU_TANH; }
-
-// A packed weight of `count` codes: present and aligned.
-qp_status check_weight(const char* what, const char* name, const void* wq, const void* scales, const void* biases,
-                       size_t es)
-{
-    if (!wq || !scales || !biases)
-        return fail(QP_ERR_INVALID_ARG, "%s: null %s weight pointer", what, name);
-    if (!aligned(wq, 4) || !aligned(scales, es) || !aligned(biases, es))
-        return fail(QP_ERR_ALIGN, "%s: %s weight pointer not aligned", what, name);
-    return QP_OK;
-}
-
-// A tensor of the activations' type: present and aligned.
-qp_status check_tensor(const char* what, const char* name, const void* p, size_t es)
-{
-    if (!p)
-        return fail(QP_ERR_INVALID_ARG, "%s: null %s", what, name);
-    if (!aligned(p, es))
-        return fail(QP_ERR_ALIGN, "%s: %s not aligned to its element size", what, name);
-    return QP_OK;
-}
-
-// A pair of gradients: both or neither, aligned.
-qp_status check_grads(const char* what, const char* name, const void* ds, const void* db, size_t es)
-{
-    if ((ds == nullptr) != (db == nullptr))
-        return fail(QP_ERR_INVALID_ARG, "%s: %s gradients need both scales and biases", what, name);
-    if (!aligned(ds, es) || !aligned(db, es))
-        return fail(QP_ERR_ALIGN, "%s: %s gradients not aligned to their element size", what, name);
-    return QP_OK;
-}
-
-qp_status check_workspace(const char* what, const void* ws, size_t bytes, size_t need)
-{
-    if (need == 0)
-        return QP_OK;
-    if (!ws)
-        return fail(QP_ERR_INVALID_ARG, "%s: null workspace", what);
-    if (bytes < need)
-        return fail(QP_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", what, bytes, need);
-    if (!aligned(ws, 16))
-        return fail(QP_ERR_ALIGN, "%s: workspace not aligned to 16 bytes", what);
-    return QP_OK;
-}
 
 // Types, sizes and layout of the gated block's calls.
 qp_status check_ffn(const char* what, int dt, int sdt, int64_t m, int64_t d, int64_t f, int32_t bits, int32_t gs,

@@ -18,9 +18,7 @@
 
 namespace qp {
 
-namespace {
-
-hipError_t xgrad(const XgradArgs& a, const GradPlan& p, hipStream_t st)
+hipError_t launch_xgrad(const XgradArgs& a, const GradPlan& p, hipStream_t st)
 {
     switch (a.bits) {
     case 2: return launch_xgrad_b2(a, p, st);
@@ -32,7 +30,7 @@ hipError_t xgrad(const XgradArgs& a, const GradPlan& p, hipStream_t st)
     return hipErrorInvalidValue;
 }
 
-hipError_t wgrad(const WgradArgs& a, const GradPlan& p, hipStream_t st)
+hipError_t launch_wgrad(const WgradArgs& a, const GradPlan& p, hipStream_t st)
 {
     switch (a.bits) {
     case 2: return launch_wgrad_b2(a, p, st);
@@ -44,17 +42,9 @@ hipError_t wgrad(const WgradArgs& a, const GradPlan& p, hipStream_t st)
     return hipErrorInvalidValue;
 }
 
+namespace {
+
 int64_t up8(int64_t n) { return (n + 7) & ~(int64_t)7; }
-
-// Whether the tile kernels' 32-bit offsets reach a tile's rows: rows of at
-// most 2^20 elements.
-bool tile_sizes(int64_t n, int64_t k, int dt) { return dt != DT_F32 && n <= (1 << 20) && k <= (1 << 20); }
-
-// The tile kernel rounds each weight to the activations' type. Over fewer than
-// 64 rows (one step, the shortest contraction of the forward tiles too) those
-// roundings, up to 2^-8 of a bfloat16 weight, do not average out: the fp32
-// kernel takes such a product.
-bool averages(int64_t n) { return n >= 64; }
 
 // The larger of the two kernels' partial sums: which one runs depends on the
 // pointers too.
@@ -81,22 +71,6 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restric
         reinterpret_cast<u32x4_t*>(out)[i] = u32x4_t{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
     }
 }
-
-// The tile kernels read 16-bit rows in 16-byte pieces: rows p [m, n] as they lie
-// where they are such, else in a copy at `to`, zeros between; *stride their distance.
-hipError_t pieces_of_rows(const void*& p, int64_t m, int64_t n, char* to, int64_t* stride, hipStream_t st)
-{
-    *stride = n;
-    if (n % 8 == 0 && aligned16(p))
-        return hipSuccess;
-    *stride = up8(n);
-    const unsigned blocks = (unsigned)std::min<int64_t>((m * (*stride / 8) + 255) / 256, 16384);
-    hipLaunchKernelGGL(pad_rows_kernel, dim3(blocks), dim3(256), 0, st, static_cast<const uint16_t*>(p), m, n, *stride,
-                       reinterpret_cast<uint16_t*>(to));
-    p = to;
-    return hipGetLastError();
-}
-size_t piece_bytes(int64_t m, int64_t n) { return up16((size_t)m * (size_t)up8(n) * 2); }
 
 // h[i] = act(g[i]) u[i] as the close of dh forms it, for a call that asks for the
 // down projection's gradients alone: dh is not needed there.
@@ -132,12 +106,25 @@ hipError_t zero_grads(void* ds, void* db, int dt, int64_t count, hipStream_t st)
 
 } // namespace
 
+hipError_t pieces_of_rows(const void*& p, int64_t m, int64_t n, char* to, int64_t* stride, hipStream_t st)
+{
+    *stride = n;
+    if (n % 8 == 0 && aligned16(p))
+        return hipSuccess;
+    *stride = up8(n);
+    const unsigned blocks = (unsigned)std::min<int64_t>((m * (*stride / 8) + 255) / 256, 16384);
+    hipLaunchKernelGGL(pad_rows_kernel, dim3(blocks), dim3(256), 0, st, static_cast<const uint16_t*>(p), m, n, *stride,
+                       reinterpret_cast<uint16_t*>(to));
+    p = to;
+    return hipGetLastError();
+}
+
 // Room for copies of dy and x, then the partial sums of one product at a time.
 size_t linear_grad_workspace_bytes(int64_t m, int64_t k, int64_t n, int gs, int dt)
 {
     if (m == 0 || k == 0 || n == 0)
         return 0;
-    return (tile_sizes(n, k, dt) ? piece_bytes(m, n) + piece_bytes(m, k) : 0) +
+    return (grad_tile_sizes(n, k, dt) ? piece_bytes(m, n) + piece_bytes(m, k) : 0) +
            std::max(xgrad_bytes(m, n, k, 1), wgrad_bytes(m, n, k, 1, gs));
 }
 
@@ -152,7 +139,7 @@ hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t st)
     }
     const void *dy = a.dy, *xs = a.x;
     int64_t stride = N, xstride = K;
-    const bool tiles = tile_sizes(N, K, a.dt);
+    const bool tiles = grad_tile_sizes(N, K, a.dt);
     char* room = static_cast<char*>(a.workspace);
     if (tiles) {
         if (hipError_t e = pieces_of_rows(dy, M, N, room, &stride, st); e != hipSuccess)
@@ -175,7 +162,7 @@ hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t st)
         x.bits = a.bits; x.gs = a.gs;
         x.out = a.dx;
         x.partial = partial;
-        if (hipError_t e = xgrad(x, xgrad_plan(M, N, K, 1, tiles && averages(N)), st); e != hipSuccess)
+        if (hipError_t e = launch_xgrad(x, xgrad_plan(M, N, K, 1, tiles && grad_averages(N)), st); e != hipSuccess)
             return e;
     }
     if (a.dscales == nullptr)
@@ -192,7 +179,7 @@ hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t st)
     w.dscales[0] = a.dscales;
     w.dbiases[0] = a.dbiases;
     w.partial = partial;
-    return wgrad(w, wgrad_plan(M, N, K, 1, a.gs, tiles), st);
+    return launch_wgrad(w, wgrad_plan(M, N, K, 1, a.gs, tiles), st);
 }
 
 // dg, du and h, room for copies of dy and x, then the partial sums of one product
@@ -205,7 +192,7 @@ size_t ffn_grad_workspace_bytes(int64_t m, int64_t d, int64_t f, int gs, int dt)
     part = std::max(part, std::max(wgrad_bytes(m, f, d, 2, gs), wgrad_bytes(m, f, d, 1, gs)));
     part = std::max(part, wgrad_bytes(m, d, f, 1, gs));
     return 3 * up16((size_t)m * (size_t)f * elem_size(dt)) +
-           (tile_sizes(d, f, dt) ? 2 * piece_bytes(m, d) : 0) + part;
+           (grad_tile_sizes(d, f, dt) ? 2 * piece_bytes(m, d) : 0) + part;
 }
 
 hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t st)
@@ -228,7 +215,7 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t st)
     char* const h = du + step;
     char* room = h + step;
 
-    const bool tiles = tile_sizes(D, F, a.dt);
+    const bool tiles = grad_tile_sizes(D, F, a.dt);
     const void *dy = a.dy, *xs = a.x;
     if (tiles) {
         int64_t stride = D;   // whole pieces: it stays
@@ -256,7 +243,7 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t st)
     x.h = a.ddown[0] != nullptr ? h : nullptr;
     const bool down_only = a.dx == nullptr && a.dgate[0] == nullptr && a.dup[0] == nullptr;
     if (hipError_t e = down_only ? hidden(a.dt, x.g, x.u, a.act, M * F, h, st)
-                                 : xgrad(x, xgrad_plan(M, D, F, 1, tiles && averages(D)), st); e != hipSuccess)
+                                 : launch_xgrad(x, xgrad_plan(M, D, F, 1, tiles && grad_averages(D)), st); e != hipSuccess)
         return e;
     if (a.dx != nullptr) {
         x.g = x.u = nullptr;
@@ -266,7 +253,7 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t st)
         x.nmat = 2;
         x.N = F; x.K = D;
         x.out = a.dx;
-        if (hipError_t e = xgrad(x, xgrad_plan(M, F, D, 2, tiles && averages(F)), st); e != hipSuccess)
+        if (hipError_t e = launch_xgrad(x, xgrad_plan(M, F, D, 2, tiles && grad_averages(F)), st); e != hipSuccess)
             return e;
     }
     WgradArgs w{};
@@ -288,7 +275,7 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t st)
     add(dg, a.gate, a.dgate);
     add(du, a.up, a.dup);
     if (w.nmat > 0)
-        if (hipError_t e = wgrad(w, wgrad_plan(M, F, D, w.nmat, a.gs, tiles), st); e != hipSuccess)
+        if (hipError_t e = launch_wgrad(w, wgrad_plan(M, F, D, w.nmat, a.gs, tiles), st); e != hipSuccess)
             return e;
     if (a.ddown[0] == nullptr)
         return hipSuccess;
@@ -297,7 +284,7 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t st)
     w.dy_stride = D;
     w.nmat = 0;
     add(static_cast<const char*>(dy), a.down, a.ddown);
-    return wgrad(w, wgrad_plan(M, D, F, 1, a.gs, tiles), st);
+    return launch_wgrad(w, wgrad_plan(M, D, F, 1, a.gs, tiles), st);
 }
 
 } // namespace qp

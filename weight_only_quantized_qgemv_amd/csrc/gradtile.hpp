@@ -351,6 +351,26 @@ __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPla
                                                       at == OOB ? OOB : 4 * (at + reg_off(R)), 0, 0);
             });
         });
+    } else if (a.sums != nullptr) {
+        // A call of several over pieces of the contraction (16 loads at a time).
+        const __amdgpu_buffer_rsrc_t rs = rows_of(a.sums, m0, 4), ro = rows_of(a.out, m0, 2);
+        const float scale = a.last && a.scale != nullptr ? *a.scale : 1.0f;
+        each_tile([&](const f32x16_t& v, uint32_t at) {
+            float t[16];
+            static_for<16>([&](auto R) {
+                t[R] = a.first ? 0.0f : __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                    rs, at == OOB ? OOB : 4 * (at + reg_off(R)), 0, 0));
+            });
+            static_for<16>([&](auto R) {
+                const float w = v[(int)R] + t[R];
+                if (a.last)
+                    __builtin_amdgcn_raw_buffer_store_b16(Elem<DT>::from_f32(w * scale), ro,
+                                                          at == OOB ? OOB : 2 * (at + reg_off(R)), 0, 0);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, w), rs,
+                                                          at == OOB ? OOB : 4 * (at + reg_off(R)), 0, 0);
+            });
+        });
     } else if (a.g == nullptr) {
         const __amdgpu_buffer_rsrc_t ro = rows_of(a.out, m0, 2);
         each_tile([&](const f32x16_t& v, uint32_t at) {
@@ -466,6 +486,7 @@ __device__ __forceinline__ void wgrad_close(const WgradArgs& a, int splits, int 
     using St = typename Elem<DT>::storage;
     const int64_t groups = a.K / a.gs, count = a.N * groups, at = (nw + (lane & 31)) * groups + kw / a.gs;
     const bool parts = splits > 1;
+    const float scale = !parts && a.scale != nullptr ? *a.scale : 1.0f;
     float* const pd = parts ? a.partial + (((int64_t)split * a.nmat + mat) * 2 + half) * count + at : nullptr;
     St* const sd = parts ? nullptr : static_cast<St*>(half ? a.dbiases[mat] : a.dscales[mat]) + at;
     const int per = a.gs / 32;                                      // units of a group
@@ -476,7 +497,7 @@ __device__ __forceinline__ void wgrad_close(const WgradArgs& a, int splits, int 
             if (parts)
                 pd[o] = v;
             else
-                sd[o] = Elem<DT>::from_f32(v);
+                sd[o] = Elem<DT>::from_f32(v * scale);
         }
     };
     if (per == 1) {

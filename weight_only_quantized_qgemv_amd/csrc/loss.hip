@@ -1,0 +1,378 @@
+// loss.hip — softmax cross entropy over a packed head, without the logits:
+//   z = x W^T (W [V, K] packed),  lse = log sum_v exp(z_v),  loss = lse - z_target
+// and its gradients, with the rows' upstream gradients g:
+//   dz = g (exp(z - lse) - [v = target]),  dx = dz W,  dW = dz^T x,
+// of dW the sums that belong to the scales and biases (wgrad.hpp).
+//
+// The vocabulary goes in pieces: of each, the logits are formed in fp32 and
+// reduced at once, to a maximum and a sum of exponentials for each row and part
+// of the piece (forward), or to dz, the operand of the two gradient products
+// (backward, where they are formed a second time: the price of not keeping them,
+// 2 M K V of 8 M K V operations). The parts' pairs are joined in a fixed order.
+#include <algorithm>
+
+#include "common.hpp"
+#include "train_ops.hpp"
+#include "xgrad.hpp"
+
+namespace qp {
+
+namespace {
+
+constexpr int kPart = 4096;   // logits of a part, in the kernels that read them
+
+struct Stat {
+    float top, sum;   // the largest logit, the sum of exp(z - top)
+};
+
+// Two parts' statistics as one (an empty part: -infinity, 0).
+__device__ __forceinline__ Stat join_stats(Stat a, Stat b)
+{
+    const float top = fmaxf(a.top, b.top);
+    if (top == -__builtin_inff())
+        return Stat{top, a.sum + b.sum};   // nothing, or NaN
+    return Stat{top, a.sum * expf(a.top - top) + b.sum * expf(b.top - top)};
+}
+
+// The statistics of each row's part of z [M, N], and the target's logit where it
+// is in it.
+__global__ __launch_bounds__(256) void loss_parts_kernel(const float* __restrict__ z, int64_t m, int64_t n, int parts,
+                                                         int64_t v0, const int32_t* __restrict__ targets,
+                                                         Stat* __restrict__ stats, float* __restrict__ picked)
+{
+    __shared__ Stat room[4];
+    const int64_t block = blockIdx.x + (int64_t)blockIdx.y * gridDim.x;
+    const int64_t row = block / parts, c0 = block % parts * kPart;
+    if (row >= m)
+        return;
+    const float* const p = z + row * n;
+    const int tid = (int)threadIdx.x;
+    float v[kPart / 256];
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < kPart / 256; ++i) {
+        const int64_t c = c0 + tid + 256 * i;
+        v[i] = c < n ? p[c] : -__builtin_inff();
+        top = fmaxf(top, v[i]);
+    }
+    Stat s{top, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kPart / 256; ++i)
+        s.sum += c0 + tid + 256 * i < n ? (v[i] == top ? 1.0f : expf(v[i] - top)) : 0.0f;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1)
+        s = join_stats(s, Stat{__shfl_xor(s.top, off, 64), __shfl_xor(s.sum, off, 64)});
+    if ((tid & 63) == 0)
+        room[tid >> 6] = s;
+    __syncthreads();
+    if (tid != 0)
+        return;
+    for (int w = 1; w < 4; ++w)
+        s = join_stats(s, room[w]);
+    stats[(v0 + c0) / kPart * m + row] = s;
+    const int64_t t = targets[row];
+    if (t >= v0 + c0 && t < v0 + c0 + kPart && t < v0 + n)
+        picked[row] = p[t - v0];
+}
+
+// The rows' losses from their parts: 64 rows a block, 16 waves a share of the parts
+// each.
+__global__ __launch_bounds__(1024) void loss_finish_kernel(const Stat* __restrict__ stats, int64_t parts, int64_t m,
+                                                           int64_t vocab, const int32_t* __restrict__ targets,
+                                                           const float* __restrict__ picked, float* __restrict__ loss,
+                                                           float* __restrict__ lse)
+{
+    __shared__ Stat room[16][64];
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    const int64_t row = (int64_t)blockIdx.x * 64 + lane;
+    Stat s{-__builtin_inff(), 0.0f};
+    if (row < m)
+        for (int64_t i = wave; i < parts; i += 16)
+            s = join_stats(s, stats[i * m + row]);
+    room[wave][lane] = s;
+    __syncthreads();
+    if (wave != 0 || row >= m)
+        return;
+    for (int w = 1; w < 16; ++w)
+        s = join_stats(s, room[w][lane]);
+    const float l = s.top + logf(s.sum);
+    const int32_t t = targets[row];
+    lse[row] = l;
+    loss[row] = t >= 0 && t < vocab ? l - picked[row] : 0.0f;
+}
+
+// No features: every logit is 0. No vocabulary: lse is log 0.
+__global__ __launch_bounds__(256) void loss_even_kernel(int64_t m, int64_t vocab, const int32_t* __restrict__ targets,
+                                                        float* __restrict__ loss, float* __restrict__ lse)
+{
+    const float l = logf((float)vocab);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < m; i += (int64_t)gridDim.x * 256) {
+        lse[i] = l;
+        loss[i] = targets[i] >= 0 && targets[i] < vocab ? l : 0.0f;
+    }
+}
+
+// dz of a piece from its logits; columns up to the next multiple of 8 are zeros
+// (the gradient products read 16-bit rows in 16-byte pieces). dz may be z (fp32).
+template <int DT>
+__global__ __launch_bounds__(256) void loss_dz_kernel(const float* z, int64_t m, int64_t n, int64_t v0, int64_t vocab,
+                                                      const int32_t* __restrict__ targets, const float* __restrict__ lse,
+                                                      const float* __restrict__ dloss, const float* __restrict__ scale,
+                                                      void* dz, int64_t stride)
+{
+    const int64_t cols = DT == DT_F32 ? n : (n + 7) & ~(int64_t)7, total = m * cols;
+    const float by = scale != nullptr ? *scale : 1.0f;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / cols, c = i - r * cols, t = targets[r];
+        const float g = t >= 0 && t < vocab ? dloss[r] * by : 0.0f;
+        float v = 0.0f;
+        if (c < n && g != 0.0f)
+            v = g * (expf(z[r * n + c] - lse[r]) - (t == v0 + c ? 1.0f : 0.0f));
+        store_elem<DT>(dz, r * stride + c, v);
+    }
+}
+
+// The factor that makes the rows' largest |dloss| 2^14, and what takes it out of the
+// sums again. dz is the products' 16-bit operand: most of it is p - 1 or a small p times
+// one and the same dloss, whose own rounding would not average out (2048 rows, a mean
+// over 1843 of them, in bf16: the gradients 0.0040 of their size off 64 bits, with
+// the factor 0.0024); and in fp16 a mean over many rows would leave the normal range
+// (2^-14) for a token of probability 1e-2 already.
+__global__ __launch_bounds__(1024) void loss_scale_kernel(const float* __restrict__ dloss, int64_t m,
+                                                          const int32_t* __restrict__ targets, int64_t vocab,
+                                                          float* __restrict__ scale)
+{
+    __shared__ float room[16];
+    float top = 0.0f;
+    for (int64_t i = threadIdx.x; i < m; i += 1024) {
+        const float g = fabsf(dloss[i]);
+        if (targets[i] >= 0 && targets[i] < vocab && g < __builtin_inff())
+            top = fmaxf(top, g);
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1)
+        top = fmaxf(top, __shfl_xor(top, off, 64));
+    if ((threadIdx.x & 63) == 0)
+        room[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x != 0)
+        return;
+    for (int w = 1; w < 16; ++w)
+        top = fmaxf(top, room[w]);
+    top = top > 0.0f ? fmaxf(top, 0x1p-100f) : 16384.0f;   // (both factors stay finite)
+    scale[0] = 16384.0f / top;
+    scale[1] = top / 16384.0f;
+}
+
+// Vocabulary of a piece: logits of about 256 MB in fp32, whole parts, or all of it.
+int64_t piece_of(int64_t m, int64_t v)
+{
+    const int64_t most = std::max<int64_t>((int64_t(1) << 26) / m / kPart * kPart, kPart);
+    return std::min(most, v);
+}
+
+QWeight rows_from(const QWeight& w, int64_t v0, int64_t k, int bits, int gs, int dt)
+{
+    const int64_t es = (int64_t)elem_size(dt), groups = k / gs;
+    return {w.wq + v0 * (k * bits / 32), static_cast<const char*>(w.scales) + v0 * groups * es,
+            static_cast<const char*>(w.biases) + v0 * groups * es};
+}
+
+hipError_t any_product(int bits, const FfnAnyArgs& a, hipStream_t st)
+{
+    switch (bits) {
+    case 2: return launch_ffn_any_b2(a, st);
+    case 3: return launch_ffn_any_b3(a, st);
+    case 4: return launch_ffn_any_b4(a, st);
+    case 6: return launch_ffn_any_b6(a, st);
+    case 8: return launch_ffn_any_b8(a, st);
+    }
+    return hipErrorInvalidValue;
+}
+
+// One piece's logits, from weight row v0 on, as fp32 [M, n].
+hipError_t logits(const void* x, int dt, int64_t m, int64_t k, QWeight w, int bits, int gs, int64_t v0, int64_t n,
+                  float* z, hipStream_t st)
+{
+    FfnSplit plan = ffn_any_plan(m, k, n);
+    plan.splits = 1;   // the vocabulary fills the GPU
+    plan.per_split = (int)(k / 32);
+    return any_product(bits, FfnAnyArgs{x, dt, m, k, n, rows_from(w, v0, k, bits, gs, dt), gs, plan, z, m * n, nullptr}, st);
+}
+
+unsigned grid_of(int64_t n) { return (unsigned)std::min<int64_t>((n + 255) / 256, 16384); }
+
+// The workspace front to back: the parts' statistics, the targets' logits, and the
+// logits of a piece.
+struct LossRoom {
+    int64_t piece, parts;
+    size_t stats, picked, z;
+    size_t all() const { return stats + picked + z; }
+};
+LossRoom loss_room(int64_t m, int64_t v)
+{
+    LossRoom r{};
+    r.piece = piece_of(m, v);
+    r.parts = (v + kPart - 1) / kPart;
+    r.stats = up16((size_t)r.parts * (size_t)m * sizeof(Stat));
+    r.picked = up16((size_t)m * 4);
+    r.z = up16((size_t)m * (size_t)r.piece * 4);
+    return r;
+}
+
+// The backward pass: the factor of dz (16 bits), the sums of dx over the pieces, a piece's
+// logits and dz, a copy of x where it is not aligned, the products' partial sums.
+struct LossGradRoom {
+    int64_t piece, stride;
+    size_t scale, sums, z, dz, x, partial;
+    size_t all() const { return scale + sums + z + dz + x + partial; }
+};
+LossGradRoom loss_grad_room(int64_t m, int64_t k, int64_t v, int gs, int dt)
+{
+    LossGradRoom r{};
+    r.piece = piece_of(m, v);
+    r.stride = dt == DT_F32 ? r.piece : (r.piece + 7) & ~(int64_t)7;
+    r.scale = 16;
+    r.sums = r.piece < v ? up16((size_t)m * (size_t)k * 4) : 0;
+    r.z = up16((size_t)m * (size_t)r.piece * 4);
+    r.dz = dt == DT_F32 ? 0 : up16((size_t)m * (size_t)r.stride * 2);
+    r.x = grad_tile_sizes(r.piece, k, dt) ? piece_bytes(m, k) : 0;
+    // The last piece may be shorter, and its plans others.
+    for (const int64_t n : {r.piece, v - (v - 1) / r.piece * r.piece})
+        for (const bool tiles : {false, true})
+            r.partial = std::max(r.partial, up16(std::max(xgrad_plan(m, n, k, 1, tiles).partial_bytes,
+                                                          wgrad_plan(m, n, k, 1, gs, tiles).partial_bytes)));
+    return r;
+}
+
+} // namespace
+
+size_t loss_workspace_bytes(int64_t m, int64_t k, int64_t v, int, int, int)
+{
+    return m == 0 || v == 0 || k == 0 ? 0 : loss_room(m, v).all();
+}
+
+hipError_t launch_loss(const LossArgs& a, hipStream_t st)
+{
+    if (a.V == 0 || a.K == 0) {
+        hipLaunchKernelGGL(loss_even_kernel, dim3(grid_of(a.M)), dim3(256), 0, st, a.M, a.V, a.targets, a.loss, a.lse);
+        return hipGetLastError();
+    }
+    const LossRoom r = loss_room(a.M, a.V);
+    Stat* const stats = static_cast<Stat*>(a.workspace);
+    float* const picked = reinterpret_cast<float*>(reinterpret_cast<char*>(stats) + r.stats);
+    float* const z = reinterpret_cast<float*>(reinterpret_cast<char*>(picked) + r.picked);
+    for (int64_t v0 = 0; v0 < a.V; v0 += r.piece) {
+        const int64_t n = std::min(r.piece, a.V - v0), parts = (n + kPart - 1) / kPart;
+        if (hipError_t e = logits(a.x, a.dt, a.M, a.K, a.w, a.bits, a.gs, v0, n, z, st); e != hipSuccess)
+            return e;
+        hipLaunchKernelGGL(loss_parts_kernel, wide_grid(a.M * parts, 256), dim3(256), 0, st, z, a.M, n, (int)parts, v0,
+                           a.targets, stats, picked);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess)
+            return e;
+    }
+    hipLaunchKernelGGL(loss_finish_kernel, dim3((unsigned)((a.M + 63) / 64)), dim3(1024), 0, st, stats, r.parts, a.M,
+                       a.V, a.targets, picked, a.loss, a.lse);
+    return hipGetLastError();
+}
+
+size_t loss_grad_workspace_bytes(int64_t m, int64_t k, int64_t v, int, int gs, int dt)
+{
+    return m == 0 || v == 0 || k == 0 ? 0 : loss_grad_room(m, k, v, gs, dt).all();
+}
+
+hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t st)
+{
+    if (a.M == 0 || a.V == 0 || a.K == 0) {   // nothing to sum over
+        if (a.dx != nullptr && a.M * a.K > 0)
+            if (hipError_t e = launch_fill_zero(a.dx, a.dt, a.M * a.K, st); e != hipSuccess)
+                return e;
+        if (a.dscales == nullptr || a.V * a.K == 0)
+            return hipSuccess;
+        if (hipError_t e = launch_fill_zero(a.dscales, a.dt, a.V * (a.K / a.gs), st); e != hipSuccess)
+            return e;
+        return launch_fill_zero(a.dbiases, a.dt, a.V * (a.K / a.gs), st);
+    }
+    const LossGradRoom r = loss_grad_room(a.M, a.K, a.V, a.gs, a.dt);
+    char* at = static_cast<char*>(a.workspace);
+    auto take = [&](size_t n) { return std::exchange(at, at + n); };
+    float* const scale = reinterpret_cast<float*>(take(r.scale));
+    float* const sums = reinterpret_cast<float*>(take(r.sums));
+    float* const z = reinterpret_cast<float*>(take(r.z));
+    void* const dz = a.dt == DT_F32 ? static_cast<void*>(z) : take(r.dz);
+    char* const xcopy = take(r.x);
+    float* const partial = reinterpret_cast<float*>(at);
+    const bool half = a.dt != DT_F32, tiles = grad_tile_sizes(r.piece, a.K, a.dt);
+    if (half) {
+        hipLaunchKernelGGL(loss_scale_kernel, dim3(1), dim3(1024), 0, st, a.dloss, a.M, a.targets, a.V, scale);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess)
+            return e;
+    }
+    const void* xs = a.x;
+    if (tiles && a.dscales != nullptr) {
+        int64_t stride = a.K;   // whole pieces: it stays
+        if (hipError_t e = pieces_of_rows(xs, a.M, a.K, xcopy, &stride, st); e != hipSuccess)
+            return e;
+    }
+    for (int64_t v0 = 0; v0 < a.V; v0 += r.piece) {
+        const int64_t n = std::min(r.piece, a.V - v0), es = (int64_t)elem_size(a.dt);
+        const QWeight w = rows_from(a.w, v0, a.K, a.bits, a.gs, a.dt);
+        if (hipError_t e = logits(a.x, a.dt, a.M, a.K, a.w, a.bits, a.gs, v0, n, z, st); e != hipSuccess)
+            return e;
+        const int64_t stride = a.dt == DT_F32 ? n : r.stride;
+        const dim3 grid(grid_of(a.M * n));
+        switch (a.dt) {
+        case DT_F32:
+            hipLaunchKernelGGL(loss_dz_kernel<DT_F32>, grid, dim3(256), 0, st, z, a.M, n, v0, a.V, a.targets, a.lse,
+                               a.dloss, nullptr, dz, stride);
+            break;
+        case DT_F16:
+            hipLaunchKernelGGL(loss_dz_kernel<DT_F16>, grid, dim3(256), 0, st, z, a.M, n, v0, a.V, a.targets, a.lse,
+                               a.dloss, scale, dz, stride);
+            break;
+        default:
+            hipLaunchKernelGGL(loss_dz_kernel<DT_BF16>, grid, dim3(256), 0, st, z, a.M, n, v0, a.V, a.targets, a.lse,
+                               a.dloss, scale, dz, stride);
+        }
+        if (hipError_t e = hipGetLastError(); e != hipSuccess)
+            return e;
+        if (a.dscales != nullptr) {
+            WgradArgs g{};
+            g.x = xs;
+            g.dy[0] = g.dy[1] = dz;
+            g.dy_stride = stride;
+            g.wq[0] = g.wq[1] = w.wq;
+            g.nmat = 1;
+            g.dt = a.dt;
+            g.M = a.M; g.N = n; g.K = a.K;
+            g.bits = a.bits; g.gs = a.gs;
+            g.dscales[0] = static_cast<char*>(a.dscales) + v0 * (a.K / a.gs) * es;
+            g.dbiases[0] = static_cast<char*>(a.dbiases) + v0 * (a.K / a.gs) * es;
+            g.partial = partial;
+            g.scale = half ? scale + 1 : nullptr;
+            if (hipError_t e = launch_wgrad(g, wgrad_plan(a.M, n, a.K, 1, a.gs, tiles), st); e != hipSuccess)
+                return e;
+        }
+        if (a.dx != nullptr) {
+            XgradArgs g{};
+            g.dy[0] = g.dy[1] = dz;
+            g.dy_stride = stride;
+            g.w[0] = g.w[1] = w;
+            g.nmat = 1;
+            g.dt = a.dt;
+            g.M = a.M; g.N = n; g.K = a.K;
+            g.bits = a.bits; g.gs = a.gs;
+            g.out = a.dx;
+            g.partial = partial;
+            g.first = v0 == 0;
+            g.last = v0 + n == a.V;
+            g.sums = g.first && g.last && !half ? nullptr : g.first && g.last ? partial : sums;
+            g.scale = half ? scale + 1 : nullptr;
+            if (hipError_t e = launch_xgrad(g, xgrad_plan(a.M, n, a.K, 1, tiles && grad_averages(n)), st); e != hipSuccess)
+                return e;
+        }
+    }
+    return hipSuccess;
+}
+
+} // namespace qp

@@ -6,6 +6,7 @@
 // returns the hipError_t of its launches.
 #pragma once
 
+#include "common.hpp"
 #include "launch.hpp"
 
 namespace qp {
@@ -112,6 +113,12 @@ struct XgradArgs {
     const void *g, *u;      // [M, K] of dt, or null
     void *dg, *du, *h;      // [M, K] of dt
     float* partial;         // fp32 partial sums of the splits (xgrad_plan)
+    // A result in pieces of the contraction, a call each: sums [M, K] kept from
+    // call to call (the first writes them, the last adds them and writes out),
+    // or null; out is multiplied by *scale (on the device) where that is given.
+    float* sums;
+    bool first, last;
+    const float* scale;
 };
 
 // dscales[n, G] = sum_{k in G} q[n, k] dW[n, k], dbiases[n, G] = sum_{k in G} dW[n, k],
@@ -127,6 +134,7 @@ struct WgradArgs {
     void* dscales[2];       // [N, K/gs] of dt
     void* dbiases[2];
     float* partial;         // fp32 partial sums of the splits (wgrad_plan)
+    const float* scale;     // the results are multiplied by *scale (on the device), or null
 };
 
 // How a gradient product is cut: `tile` chooses the kernel and its tile,
@@ -151,6 +159,22 @@ QP_GRAD_DECL(4)
 QP_GRAD_DECL(6)
 QP_GRAD_DECL(8)
 #undef QP_GRAD_DECL
+// By a.bits (grad.hip), and what the callers of the products share.
+hipError_t launch_xgrad(const XgradArgs& a, const GradPlan& p, hipStream_t stream);
+hipError_t launch_wgrad(const WgradArgs& a, const GradPlan& p, hipStream_t stream);
+// Whether the tile kernels' 32-bit offsets reach a tile's rows: rows of at
+// most 2^20 elements.
+inline bool grad_tile_sizes(int64_t n, int64_t k, int dt) { return dt != DT_F32 && n <= (1 << 20) && k <= (1 << 20); }
+// The tile kernel rounds each weight to the activations' type. Over fewer than
+// 64 rows (one step, the shortest contraction of the forward tiles too) those
+// roundings, up to 2^-8 of a bfloat16 weight, do not average out: the fp32
+// kernel takes such a product.
+inline bool grad_averages(int64_t n) { return n >= 64; }
+// The tile kernels read 16-bit rows in 16-byte pieces: rows p [m, n] as they lie
+// where they are such, else in a copy at `to` (piece_bytes), zeros between;
+// *stride their distance.
+hipError_t pieces_of_rows(const void*& p, int64_t m, int64_t n, char* to, int64_t* stride, hipStream_t stream);
+inline size_t piece_bytes(int64_t m, int64_t n) { return up16((size_t)m * (size_t)((n + 7) & ~(int64_t)7) * 2); }
 
 struct LinearGradArgs {
     const void *x, *dy;     // [M, K], [M, N] of dt

@@ -1,0 +1,76 @@
+// train_ops.hpp — host-side launchers of the operators that train and score a
+// model around the packed layers: the norms around a block and the cross entropy
+// over a packed head, with their gradients. Implemented by the kernel files,
+// called by the C ABI layer (api_train.cpp), which validates the arguments; every
+// launcher returns the hipError_t of its launches.
+#pragma once
+
+#include "model_ops.hpp"
+
+namespace qp {
+
+// ---- norms around a block (norm.hip)
+constexpr int64_t kNormMaxWidth = 16384;
+
+struct NormArgs {
+    const void* x;           // [M, D] of sdt: the stream
+    int sdt, dt;             // its type; the block's (sdt, or sdt is fp32)
+    int64_t M, D;
+    const void* y;           // [M, D] of dt: the block's output, or null
+    const void *post, *weight;   // [D] of dt each: the norm after the block, before the next; or null
+    const void* gate;        // [gates, D] of dt, or null
+    int64_t gates;           // a divisor of M; gate row r / (M / gates) for row r
+    float factor, offset, eps;
+    void* s;                 // [M, D] of sdt: the new stream (with y)
+    void* a;                 // [M, D] of dt (with weight)
+};
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
+
+struct NormGradArgs {
+    const void* s;           // [M, D] of sdt (with weight)
+    const void* da;          // [M, D] of dt (with weight)
+    const void* ds;          // [M, D] of sdt, or null (zeros)
+    const void* y;           // [M, D] of dt, or null
+    int sdt, dt;
+    int64_t M, D;
+    const void *post, *weight, *gate;
+    int64_t gates;
+    float factor, offset, eps;
+    void* dx;                // [M, D] of sdt
+    void* dy;                // [M, D] of dt (with y)
+    void *dweight, *dpost, *dgate;   // of dt, with what they are the gradients of
+    void* workspace;         // >= norm_grad_workspace_bytes, 16-byte aligned
+};
+size_t norm_grad_workspace_bytes(int64_t m, int64_t d, int64_t gates);
+hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t stream);
+
+// ---- cross entropy over a packed head (loss.hip)
+struct LossArgs {
+    const void* x;           // [M, K] of dt
+    int dt;
+    int64_t M, K, V;
+    const int32_t* targets;  // [M]; outside [0, V): no target
+    QWeight w;               // [V, K]
+    int bits, gs;
+    float *loss, *lse;       // [M]
+    void* workspace;         // >= loss_workspace_bytes, 16-byte aligned
+};
+size_t loss_workspace_bytes(int64_t m, int64_t k, int64_t v, int bits, int gs, int dt);
+hipError_t launch_loss(const LossArgs& a, hipStream_t stream);
+
+struct LossGradArgs {
+    const void* x;
+    int dt;
+    int64_t M, K, V;
+    const int32_t* targets;
+    QWeight w;
+    int bits, gs;
+    const float *lse, *dloss;    // [M]
+    void* dx;                // [M, K] of dt, or null
+    void *dscales, *dbiases; // [V, K/gs] of dt, or both null
+    void* workspace;         // >= loss_grad_workspace_bytes, 16-byte aligned
+};
+size_t loss_grad_workspace_bytes(int64_t m, int64_t k, int64_t v, int bits, int gs, int dt);
+hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t stream);
+
+} // namespace qp

@@ -68,7 +68,7 @@ hipError_t run(const WgradArgs& a, const GradPlan& p, hipStream_t st)
         for (int mat = 0; mat < a.nmat; ++mat) {
             hipLaunchKernelGGL((wgrad_finish_kernel<DT>), dim3((unsigned)blocks), dim3(256), 0, st,
                                a.partial + (int64_t)mat * 2 * count, p.splits, 2 * count * a.nmat, count,
-                               a.dscales[mat], a.dbiases[mat]);
+                               a.dscales[mat], a.dbiases[mat], a.scale);
             if (hipError_t e = hipGetLastError(); e != hipSuccess)
                 return e;
         }

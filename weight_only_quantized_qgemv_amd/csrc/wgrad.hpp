@@ -20,10 +20,10 @@ namespace qp {
 template <int DT>
 __global__ __launch_bounds__(256) void wgrad_finish_kernel(const float* __restrict__ partial, int splits,
                                                            int64_t per_split, int64_t count, void* dscales,
-                                                           void* dbiases)
+                                                           void* dbiases, const float* scale)
 {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < 2 * count; i += (int64_t)gridDim.x * 256) {
-        const float v = sum_splits(partial, splits, per_split, i);
+        const float v = scaled(sum_splits(partial, splits, per_split, i), scale);
         if (i < count)
             store_elem<DT>(dscales, i, v);
         else
@@ -41,7 +41,7 @@ __device__ __forceinline__ void wgrad_store(const WgradArgs& a, const GradPlan& 
     if (plan.splits > 1)
         a.partial[(((int64_t)split * a.nmat + mat) * 2 + (bias ? 1 : 0)) * count + i] = v;
     else
-        store_elem<DT>(bias ? a.dbiases[mat] : a.dscales[mat], i, v);
+        store_elem<DT>(bias ? a.dbiases[mat] : a.dscales[mat], i, scaled(v, a.scale));
 }
 
 // Any type, size and alignment: fp32 products on the 32x32x2 matrix

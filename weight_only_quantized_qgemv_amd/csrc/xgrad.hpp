@@ -27,10 +27,32 @@ __device__ __forceinline__ void store_elem(void* p, int64_t i, float v)
     static_cast<typename Elem<DT>::storage*>(p)[i] = Elem<DT>::from_f32(v);
 }
 
+// v times a factor that is on the device, where there is one.
+__device__ __forceinline__ float scaled(float v, const float* scale)
+{
+    return scale != nullptr ? v * *scale : v;
+}
+
+// The result v of element i = m K + k of a call with sums: added to them, or stored.
+template <int DT>
+__device__ __forceinline__ void xgrad_add(const XgradArgs& a, int64_t i, float v)
+{
+    if (!a.first)
+        v += a.sums[i];
+    if (a.last)
+        store_elem<DT>(a.out, i, scaled(v, a.scale));
+    else
+        a.sums[i] = v;
+}
+
 // The result v of element i = m K + k: stored, or closed as above.
 template <int DT>
 __device__ __forceinline__ void xgrad_store(const XgradArgs& a, int64_t i, float v)
 {
+    if (a.sums != nullptr) {
+        xgrad_add<DT>(a, i, v);
+        return;
+    }
     if (a.g == nullptr) {
         store_elem<DT>(a.out, i, v);
         return;
@@ -196,6 +218,8 @@ __global__ __launch_bounds__(256) void xgrad_f32_kernel(XgradArgs a, GradPlan pl
     if (plan.splits > 1) {
         float* const part = a.partial + (int64_t)blockIdx.y * a.M * a.K;
         each([&](int64_t i, float v) { part[i] = v; });
+    } else if (a.sums != nullptr) {
+        each([&](int64_t i, float v) { xgrad_add<DT>(a, i, v); });
     } else if (a.g == nullptr) {
         each([&](int64_t i, float v) { store_elem<DT>(a.out, i, v); });
     } else {
