@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "common.hpp"
+#include "loss_stat.hpp"
 #include "train_ops.hpp"
 #include "xgrad.hpp"
 
@@ -20,19 +21,6 @@ namespace qp {
 namespace {
 
 constexpr int kPart = 4096;   // logits of a part, in the kernels that read them
-
-struct Stat {
-    float top, sum;   // the largest logit, the sum of exp(z - top)
-};
-
-// Two parts' statistics as one (an empty part: -infinity, 0).
-__device__ __forceinline__ Stat join_stats(Stat a, Stat b)
-{
-    const float top = fmaxf(a.top, b.top);
-    if (top == -__builtin_inff())
-        return Stat{top, a.sum + b.sum};   // nothing, or NaN
-    return Stat{top, a.sum * expf(a.top - top) + b.sum * expf(b.top - top)};
-}
 
 // The statistics of each row's part of z [M, N], and the target's logit where it
 // is in it.
@@ -164,6 +152,34 @@ __global__ __launch_bounds__(1024) void loss_scale_kernel(const float* __restric
     scale[1] = top / 16384.0f;
 }
 
+// The scales [n, groups] transposed to [groups, np], zeros behind n, and the biases in
+// rows of gp (null: they lie so already). Tiles of 64 x 64.
+__global__ __launch_bounds__(256) void loss_prep_w_kernel(const uint16_t* __restrict__ scales,
+                                                          const uint16_t* __restrict__ biases, int64_t n, int groups,
+                                                          int64_t np, int gp, uint16_t* __restrict__ st,
+                                                          uint16_t* __restrict__ bp)
+{
+    __shared__ uint16_t room[64][66];
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    const int tiles_g = (gp + 63) / 64;
+    const int g0 = (int)(blockIdx.x % tiles_g) * 64;
+    const int64_t v0 = (int64_t)(blockIdx.x / tiles_g) * 64;
+    const int g = g0 + lane;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int64_t v = v0 + 4 * i + wave;
+        const bool in = v < n && g < groups;
+        room[4 * i + wave][lane] = in ? scales[v * groups + g] : (uint16_t)0;
+        if (bp != nullptr && v < n && g < gp)
+            bp[v * gp + g] = in ? biases[v * groups + g] : (uint16_t)0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (g0 + 4 * i + wave < groups)
+            st[(int64_t)(g0 + 4 * i + wave) * np + v0 + lane] = room[lane][4 * i + wave];
+}
+
 // Vocabulary of a piece: logits of about 256 MB in fp32, whole parts, or all of it.
 int64_t piece_of(int64_t m, int64_t v)
 {
@@ -202,39 +218,151 @@ hipError_t logits(const void* x, int dt, int64_t m, int64_t k, QWeight w, int bi
 
 unsigned grid_of(int64_t n) { return (unsigned)std::min<int64_t>((n + 255) / 256, 16384); }
 
+// Whether the tile kernel takes a product (its last step holds a row's last 64 features;
+// up to 16 rows the decode kernels stream the weights once).
+bool tile_product(int64_t m, int64_t k, int dt) { return dt != DT_F32 && m > 16 && k >= 64 && k <= (1 << 20); }
+
+hipError_t tile_kernel(int bits, int dt, const LossTileArgs& a, hipStream_t st)
+{
+    switch (bits) {
+    case 2: return launch_loss_tile_b2(dt, a, st);
+    case 3: return launch_loss_tile_b3(dt, a, st);
+    case 4: return launch_loss_tile_b4(dt, a, st);
+    case 6: return launch_loss_tile_b6(dt, a, st);
+    case 8: return launch_loss_tile_b8(dt, a, st);
+    }
+    return hipErrorInvalidValue;
+}
+hipError_t prep_x(int bits, int dt, const LossTileArgs& a, const void* x, hipStream_t st)
+{
+    switch (bits) {
+    case 2: return launch_loss_prep_x_b2(dt, a, x, st);
+    case 3: return launch_loss_prep_x_b3(dt, a, x, st);
+    case 4: return launch_loss_prep_x_b4(dt, a, x, st);
+    case 6: return launch_loss_prep_x_b6(dt, a, x, st);
+    case 8: return launch_loss_prep_x_b8(dt, a, x, st);
+    }
+    return hipErrorInvalidValue;
+}
+
+// Fills a.st and, where bp is given, bp.
+hipError_t prep_w(const LossTileArgs& a, const void* scales, const void* biases, void* bp, hipStream_t st)
+{
+    const int64_t blocks = (int64_t)(a.np / 64) * ((a.gp + 63) / 64);
+    if (!grid_fits(blocks, 256))
+        return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(loss_prep_w_kernel, dim3((unsigned)blocks), dim3(256), 0, st,
+                       static_cast<const uint16_t*>(scales), static_cast<const uint16_t*>(biases), (int64_t)a.N,
+                       a.K / a.gs, (int64_t)a.np, a.gp, static_cast<uint16_t*>(const_cast<void*>(a.st)),
+                       static_cast<uint16_t*>(bp));
+    return hipGetLastError();
+}
+
+// What the tile kernel reads beside the codes, laid out once a call (x) or a piece (the
+// weight's): sizes in bytes.
+struct TileRoom {
+    int64_t kp, gp, np;
+    size_t xp, xs, st, bp;
+    size_t all() const { return xp + xs + st + bp; }
+};
+TileRoom tile_room(int64_t m, int64_t k, int64_t piece, int gs)
+{
+    TileRoom t{};
+    t.kp = (k + 63) / 64 * 64;
+    t.gp = (k / gs + 15) / 16 * 16;
+    t.np = (piece + LOSS_BN - 1) / LOSS_BN * LOSS_BN;
+    t.xp = (size_t)m * (size_t)t.kp * 2;
+    t.xs = (size_t)m * (size_t)t.gp * 4;
+    t.st = (size_t)(k / gs) * (size_t)t.np * 2;
+    t.bp = (size_t)piece * (size_t)t.gp * 2;
+    return {t.kp, t.gp, t.np, up16(t.xp), up16(t.xs), up16(t.st), up16(t.bp)};
+}
+// The kernel's arguments for x, which is laid out at `room`; the weight's follow it.
+hipError_t tile_begin(LossTileArgs& t, const TileRoom& r, char* room, const void* x, int dt, int64_t m, int64_t k,
+                      int bits, int gs, int64_t vocab, const int32_t* targets, hipStream_t st)
+{
+    t.xp = room;
+    t.xs = room + r.xp;
+    t.st = room + r.xp + r.xs;
+    t.M = (int)m; t.K = (int)k; t.gs = gs;
+    t.kp = (int)r.kp; t.gp = (int)r.gp;
+    t.vocab = vocab;
+    t.targets = targets;
+    t.stat_rows = m;
+    return prep_x(bits, dt, t, x, st);
+}
+hipError_t tile_piece(LossTileArgs& t, const TileRoom& r, char* room, const QWeight& w, int bits, int dt, int64_t v0,
+                      int64_t n, hipStream_t st)
+{
+    t.wq = w.wq;
+    t.N = (int)n;
+    t.np = (int)((n + LOSS_BN - 1) / LOSS_BN * LOSS_BN);
+    t.v0 = v0;
+    t.part0 = (int)(v0 / LOSS_BN);
+    // The biases as they lie, where their rows are whole 16-byte pieces.
+    const bool as_is = t.gp == t.K / t.gs && aligned16(w.biases);
+    char* const bp = room + r.xp + r.xs + r.st;
+    t.bp = as_is ? w.biases : bp;
+    if (hipError_t e = prep_w(t, w.scales, w.biases, as_is ? nullptr : bp, st); e != hipSuccess)
+        return e;
+    return tile_kernel(bits, dt, t, st);
+}
+// Vocabulary of a piece: scales of up to 2^29 bytes, whole tiles, and (backward) dz of
+// about 128 MB, but not less than 2048 tokens.
+int64_t tile_piece_of(int64_t m, int64_t k, int64_t v, int gs, bool grad)
+{
+    int64_t most = std::max<int64_t>((int64_t(1) << 28) / (k / gs) / LOSS_BN * LOSS_BN, LOSS_BN);
+    if (grad)
+        most = std::min(most, std::max<int64_t>((int64_t(1) << 26) / m / LOSS_BN * LOSS_BN, 2048));
+    return std::min(most, v);
+}
+
 // The workspace front to back: the parts' statistics, the targets' logits, and the
-// logits of a piece.
+// logits of a piece or what the tile kernel reads.
 struct LossRoom {
+    bool tiles;
     int64_t piece, parts;
     size_t stats, picked, z;
-    size_t all() const { return stats + picked + z; }
+    TileRoom t;
+    size_t all() const { return stats + picked + z + t.all(); }
 };
-LossRoom loss_room(int64_t m, int64_t v)
+LossRoom loss_room(int64_t m, int64_t k, int64_t v, int gs, int dt)
 {
     LossRoom r{};
-    r.piece = piece_of(m, v);
-    r.parts = (v + kPart - 1) / kPart;
+    r.tiles = tile_product(m, k, dt);
+    r.piece = r.tiles ? tile_piece_of(m, k, v, gs, false) : piece_of(m, v);
+    r.parts = r.tiles ? (v + LOSS_BN - 1) / LOSS_BN : (v + kPart - 1) / kPart;
     r.stats = up16((size_t)r.parts * (size_t)m * sizeof(Stat));
     r.picked = up16((size_t)m * 4);
-    r.z = up16((size_t)m * (size_t)r.piece * 4);
+    if (r.tiles)
+        r.t = tile_room(m, k, r.piece, gs);
+    else
+        r.z = up16((size_t)m * (size_t)r.piece * 4);
     return r;
 }
 
 // The backward pass: the factor of dz (16 bits), the sums of dx over the pieces, a piece's
-// logits and dz, a copy of x where it is not aligned, the products' partial sums.
+// logits (or what the tile kernel reads) and dz, a copy of x where it is not aligned, the
+// products' partial sums.
 struct LossGradRoom {
+    bool tiles;
     int64_t piece, stride;
     size_t scale, sums, z, dz, x, partial;
-    size_t all() const { return scale + sums + z + dz + x + partial; }
+    TileRoom t;
+    size_t all() const { return scale + sums + z + t.all() + dz + x + partial; }
 };
 LossGradRoom loss_grad_room(int64_t m, int64_t k, int64_t v, int gs, int dt)
 {
     LossGradRoom r{};
-    r.piece = piece_of(m, v);
+    r.tiles = tile_product(m, k, dt);
+    r.piece = r.tiles ? tile_piece_of(m, k, v, gs, true) : piece_of(m, v);
     r.stride = dt == DT_F32 ? r.piece : (r.piece + 7) & ~(int64_t)7;
     r.scale = 16;
     r.sums = r.piece < v ? up16((size_t)m * (size_t)k * 4) : 0;
-    r.z = up16((size_t)m * (size_t)r.piece * 4);
+    if (r.tiles)
+        r.t = tile_room(m, k, r.piece, gs);
+    else
+        r.z = up16((size_t)m * (size_t)r.piece * 4);
     r.dz = dt == DT_F32 ? 0 : up16((size_t)m * (size_t)r.stride * 2);
     r.x = grad_tile_sizes(r.piece, k, dt) ? piece_bytes(m, k) : 0;
     // The last piece may be shorter, and its plans others.
@@ -245,11 +373,32 @@ LossGradRoom loss_grad_room(int64_t m, int64_t k, int64_t v, int gs, int dt)
     return r;
 }
 
+// dz of a piece from its logits.
+hipError_t dz_of(const LossGradArgs& a, const float* z, int64_t v0, int64_t n, const float* scale, void* dz,
+                 int64_t stride, hipStream_t st)
+{
+    const dim3 grid(grid_of(a.M * n));
+    switch (a.dt) {
+    case DT_F32:
+        hipLaunchKernelGGL(loss_dz_kernel<DT_F32>, grid, dim3(256), 0, st, z, a.M, n, v0, a.V, a.targets, a.lse,
+                           a.dloss, scale, dz, stride);
+        break;
+    case DT_F16:
+        hipLaunchKernelGGL(loss_dz_kernel<DT_F16>, grid, dim3(256), 0, st, z, a.M, n, v0, a.V, a.targets, a.lse,
+                           a.dloss, scale, dz, stride);
+        break;
+    default:
+        hipLaunchKernelGGL(loss_dz_kernel<DT_BF16>, grid, dim3(256), 0, st, z, a.M, n, v0, a.V, a.targets, a.lse,
+                           a.dloss, scale, dz, stride);
+    }
+    return hipGetLastError();
+}
+
 } // namespace
 
-size_t loss_workspace_bytes(int64_t m, int64_t k, int64_t v, int, int, int)
+size_t loss_workspace_bytes(int64_t m, int64_t k, int64_t v, int, int gs, int dt)
 {
-    return m == 0 || v == 0 || k == 0 ? 0 : loss_room(m, v).all();
+    return m == 0 || v == 0 || k == 0 ? 0 : loss_room(m, k, v, gs, dt).all();
 }
 
 hipError_t launch_loss(const LossArgs& a, hipStream_t st)
@@ -258,12 +407,26 @@ hipError_t launch_loss(const LossArgs& a, hipStream_t st)
         hipLaunchKernelGGL(loss_even_kernel, dim3(grid_of(a.M)), dim3(256), 0, st, a.M, a.V, a.targets, a.loss, a.lse);
         return hipGetLastError();
     }
-    const LossRoom r = loss_room(a.M, a.V);
+    const LossRoom r = loss_room(a.M, a.K, a.V, a.gs, a.dt);
     Stat* const stats = static_cast<Stat*>(a.workspace);
     float* const picked = reinterpret_cast<float*>(reinterpret_cast<char*>(stats) + r.stats);
-    float* const z = reinterpret_cast<float*>(reinterpret_cast<char*>(picked) + r.picked);
+    char* const room = reinterpret_cast<char*>(picked) + r.picked;
+    float* const z = reinterpret_cast<float*>(room);
+    LossTileArgs t{};
+    if (r.tiles) {
+        t.stats = stats;
+        t.picked = picked;
+        if (hipError_t e = tile_begin(t, r.t, room, a.x, a.dt, a.M, a.K, a.bits, a.gs, a.V, a.targets, st); e != hipSuccess)
+            return e;
+    }
     for (int64_t v0 = 0; v0 < a.V; v0 += r.piece) {
         const int64_t n = std::min(r.piece, a.V - v0), parts = (n + kPart - 1) / kPart;
+        if (r.tiles) {
+            if (hipError_t e = tile_piece(t, r.t, room, rows_from(a.w, v0, a.K, a.bits, a.gs, a.dt), a.bits, a.dt, v0, n, st);
+                e != hipSuccess)
+                return e;
+            continue;
+        }
         if (hipError_t e = logits(a.x, a.dt, a.M, a.K, a.w, a.bits, a.gs, v0, n, z, st); e != hipSuccess)
             return e;
         hipLaunchKernelGGL(loss_parts_kernel, wide_grid(a.M * parts, 256), dim3(256), 0, st, z, a.M, n, (int)parts, v0,
@@ -299,6 +462,7 @@ hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t st)
     float* const scale = reinterpret_cast<float*>(take(r.scale));
     float* const sums = reinterpret_cast<float*>(take(r.sums));
     float* const z = reinterpret_cast<float*>(take(r.z));
+    char* const room = take(r.t.all());
     void* const dz = a.dt == DT_F32 ? static_cast<void*>(z) : take(r.dz);
     char* const xcopy = take(r.x);
     float* const partial = reinterpret_cast<float*>(at);
@@ -314,28 +478,27 @@ hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t st)
         if (hipError_t e = pieces_of_rows(xs, a.M, a.K, xcopy, &stride, st); e != hipSuccess)
             return e;
     }
+    LossTileArgs t{};
+    if (r.tiles) {
+        t.dz = dz;
+        t.dz_stride = r.stride;
+        t.lse = a.lse; t.dloss = a.dloss; t.scale = scale;
+        if (hipError_t e = tile_begin(t, r.t, room, a.x, a.dt, a.M, a.K, a.bits, a.gs, a.V, a.targets, st); e != hipSuccess)
+            return e;
+    }
     for (int64_t v0 = 0; v0 < a.V; v0 += r.piece) {
         const int64_t n = std::min(r.piece, a.V - v0), es = (int64_t)elem_size(a.dt);
         const QWeight w = rows_from(a.w, v0, a.K, a.bits, a.gs, a.dt);
-        if (hipError_t e = logits(a.x, a.dt, a.M, a.K, a.w, a.bits, a.gs, v0, n, z, st); e != hipSuccess)
-            return e;
         const int64_t stride = a.dt == DT_F32 ? n : r.stride;
-        const dim3 grid(grid_of(a.M * n));
-        switch (a.dt) {
-        case DT_F32:
-            hipLaunchKernelGGL(loss_dz_kernel<DT_F32>, grid, dim3(256), 0, st, z, a.M, n, v0, a.V, a.targets, a.lse,
-                               a.dloss, nullptr, dz, stride);
-            break;
-        case DT_F16:
-            hipLaunchKernelGGL(loss_dz_kernel<DT_F16>, grid, dim3(256), 0, st, z, a.M, n, v0, a.V, a.targets, a.lse,
-                               a.dloss, scale, dz, stride);
-            break;
-        default:
-            hipLaunchKernelGGL(loss_dz_kernel<DT_BF16>, grid, dim3(256), 0, st, z, a.M, n, v0, a.V, a.targets, a.lse,
-                               a.dloss, scale, dz, stride);
+        if (r.tiles) {
+            if (hipError_t e = tile_piece(t, r.t, room, w, a.bits, a.dt, v0, n, st); e != hipSuccess)
+                return e;
+        } else {
+            if (hipError_t e = logits(a.x, a.dt, a.M, a.K, a.w, a.bits, a.gs, v0, n, z, st); e != hipSuccess)
+                return e;
+            if (hipError_t e = dz_of(a, z, v0, n, half ? scale : nullptr, dz, stride, st); e != hipSuccess)
+                return e;
         }
-        if (hipError_t e = hipGetLastError(); e != hipSuccess)
-            return e;
         if (a.dscales != nullptr) {
             WgradArgs g{};
             g.x = xs;

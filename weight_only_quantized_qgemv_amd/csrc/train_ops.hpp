@@ -73,4 +73,37 @@ struct LossGradArgs {
 size_t loss_grad_workspace_bytes(int64_t m, int64_t k, int64_t v, int bits, int gs, int dt);
 hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t stream);
 
+// The tile kernel of the loss (loss_tile.hpp): rows of 16-bit x times a piece of the
+// vocabulary, closed to statistics or (dz) to the logits' gradient.
+constexpr int LOSS_BN = 256;   // columns of a tile, and of a part of the statistics
+struct Stat;
+struct LossTileArgs {
+    const void* xp;          // [M, kp]: x in the order of the code pairs (loss_prep_x)
+    const void* xs;          // [M, 2, gp]: the groups' sums, high and low part
+    const uint32_t* wq;      // [N, K*bits/32]
+    const void* st;          // [K/gs, np]: the scales, transposed (loss_prep_w)
+    const void* bp;          // [N, gp]: the biases
+    int M, N, K, gs;
+    int kp, gp, np;          // K, the groups and N filled up to 64, 16 and LOSS_BN
+    int tiles_m, tiles, per_xcd;
+    const int32_t* targets;  // [M]
+    int64_t vocab, v0;       // the whole vocabulary; the piece's first token
+    Stat* stats;             // [parts][stat_rows], from part part0 on
+    float* picked;           // [M]: the targets' logits
+    int64_t stat_rows;
+    int part0;
+    void* dz;                // [M, dz_stride], or null: statistics
+    int64_t dz_stride;
+    const float *lse, *dloss, *scale;   // [M], [M], and scale[0] a factor of dloss
+};
+#define QP_LOSS_DECL(B)                                                                                          \
+    hipError_t launch_loss_prep_x_b##B(int dt, const LossTileArgs& a, const void* x, hipStream_t stream);       \
+    hipError_t launch_loss_tile_b##B(int dt, LossTileArgs a, hipStream_t stream);
+QP_LOSS_DECL(2)
+QP_LOSS_DECL(3)
+QP_LOSS_DECL(4)
+QP_LOSS_DECL(6)
+QP_LOSS_DECL(8)
+#undef QP_LOSS_DECL
+
 } // namespace qp
