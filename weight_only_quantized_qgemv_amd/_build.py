@@ -29,7 +29,7 @@ UNITS = ([("api.cpp", "api", {}), ("quantize.hip", "quantize", {}), ("moe.hip", 
           ("logits.hip", "logits", {}), ("api_train.cpp", "api_train", {}), ("norm.hip", "norm", {}),
           ("loss.hip", "loss", {})]
          + [("qgemv.hip", f"qgemv_b{b}", {"QP_BITS": b}) for b in BITS]
-         + [(f"{f}.hip", f"{f}_b{b}", {"QP_BITS": b}) for f in ("xgrad", "wgrad", "gate_up", "ffn_any", "loss_tile") for b in BITS]
+         + [(f"{f}.hip", f"{f}_b{b}", {"QP_BITS": b}) for f in ("xgrad", "wgrad", "gate_up", "ffn_any", "loss_tile", "loss_rows") for b in BITS]
          + [("moe_compute.hip", f"moe_b{b}_n{n}", {"QP_BITS": b, "QP_NMAT": n})
             for b in BITS for n in (1, 2)])
 

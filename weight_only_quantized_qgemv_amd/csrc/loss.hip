@@ -44,9 +44,10 @@ __global__ __launch_bounds__(256) void loss_parts_kernel(const float* __restrict
         top = fmaxf(top, v[i]);
     }
     Stat s{top, 0.0f};
+    const float at = top == -__builtin_inff() ? 0.0f : top;   // nothing here: sums of 0
 #pragma unroll
     for (int i = 0; i < kPart / 256; ++i)
-        s.sum += c0 + tid + 256 * i < n ? (v[i] == top ? 1.0f : expf(v[i] - top)) : 0.0f;
+        s.sum += expf(v[i] - at);
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1)
         s = join_stats(s, Stat{__shfl_xor(s.top, off, 64), __shfl_xor(s.sum, off, 64)});
@@ -87,6 +88,76 @@ __global__ __launch_bounds__(1024) void loss_finish_kernel(const Stat* __restric
     const int32_t t = targets[row];
     lse[row] = l;
     loss[row] = t >= 0 && t < vocab ? l - picked[row] : 0.0f;
+}
+
+// The losses of few rows, a block each, from all their logits at once: 32 a thread at a
+// time, the next 32 on their way.
+__global__ __launch_bounds__(1024) void loss_rows_kernel(const float* __restrict__ z, int64_t vocab,
+                                                         const int32_t* __restrict__ targets, float* __restrict__ loss,
+                                                         float* __restrict__ lse)
+{
+    typedef f32x4_t Wide __attribute__((aligned(4)));
+    constexpr int V = 8, STEP = 1024 * 4 * V;
+    __shared__ Stat room[16];
+    const int tid = (int)threadIdx.x;
+    const int64_t row = blockIdx.x;
+    const float* const p = z + row * vocab;
+    const int32_t target = targets[row];
+    const bool live = target >= 0 && target < vocab;
+    const float picked = live ? p[target] : 0.0f;
+    f32x4_t v[2][V];
+    auto fetch = [&](int64_t c0, f32x4_t (&to)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int64_t c = c0 + 4 * (tid + 1024 * i);
+            if (c + 4 <= vocab)
+                to[i] = *reinterpret_cast<const Wide*>(p + c);
+            else
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    to[i][j] = c + j < vocab ? p[c + j] : -__builtin_inff();
+        }
+    };
+    Stat s{-__builtin_inff(), 0.0f};
+    auto take = [&](const f32x4_t (&t)[V]) {
+        float top = s.top;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                top = fmaxf(top, t[i][j]);
+        if (top == -__builtin_inff())
+            top = 0.0f;   // nothing yet: sums of 0
+        float sum = s.sum * expf(s.top - top);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                sum += expf(t[i][j] - top);
+        s = Stat{top, sum};
+    };
+    fetch(0, v[0]);
+    for (int64_t c = 0; c < vocab; c += 2 * STEP) {
+        fetch(c + STEP, v[1]);
+        take(v[0]);
+        if (c + STEP >= vocab)
+            break;
+        fetch(c + 2 * STEP, v[0]);
+        take(v[1]);
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1)
+        s = join_stats(s, Stat{__shfl_xor(s.top, off, 64), __shfl_xor(s.sum, off, 64)});
+    if ((tid & 63) == 0)
+        room[tid >> 6] = s;
+    __syncthreads();
+    if (tid != 0)
+        return;
+    for (int w = 1; w < 16; ++w)
+        s = join_stats(s, room[w]);
+    const float l = s.top + logf(s.sum);
+    lse[row] = l;
+    loss[row] = live ? l - picked : 0.0f;
 }
 
 // No features: every logit is 0. No vocabulary: lse is log 0.
@@ -206,14 +277,29 @@ hipError_t any_product(int bits, const FfnAnyArgs& a, hipStream_t st)
     return hipErrorInvalidValue;
 }
 
+// Whether the decode kernels take a product: up to 16 rows of 16 bits, the weights
+// streamed once (1 row of 4096 x 32000, 4-bit: 120 us on ffn_any's kernel, now 19).
+bool rows_product(int64_t m, int dt) { return dt != DT_F32 && m <= 16; }
+
 // One piece's logits, from weight row v0 on, as fp32 [M, n].
 hipError_t logits(const void* x, int dt, int64_t m, int64_t k, QWeight w, int bits, int gs, int64_t v0, int64_t n,
                   float* z, hipStream_t st)
 {
+    w = rows_from(w, v0, k, bits, gs, dt);
+    if (rows_product(m, dt) && aligned16(x)) {
+        const GemvArgs a{x, dt, m, k, n, w.wq, w.scales, w.biases, bits, gs, z};
+        switch (bits) {
+        case 2: return launch_loss_rows_b2(a, st);
+        case 3: return launch_loss_rows_b3(a, st);
+        case 4: return launch_loss_rows_b4(a, st);
+        case 6: return launch_loss_rows_b6(a, st);
+        case 8: return launch_loss_rows_b8(a, st);
+        }
+    }
     FfnSplit plan = ffn_any_plan(m, k, n);
     plan.splits = 1;   // the vocabulary fills the GPU
     plan.per_split = (int)(k / 32);
-    return any_product(bits, FfnAnyArgs{x, dt, m, k, n, rows_from(w, v0, k, bits, gs, dt), gs, plan, z, m * n, nullptr}, st);
+    return any_product(bits, FfnAnyArgs{x, dt, m, k, n, w, gs, plan, z, m * n, nullptr}, st);
 }
 
 unsigned grid_of(int64_t n) { return (unsigned)std::min<int64_t>((n + 255) / 256, 16384); }
@@ -318,13 +404,14 @@ int64_t tile_piece_of(int64_t m, int64_t k, int64_t v, int gs, bool grad)
 }
 
 // The workspace front to back: the parts' statistics, the targets' logits, and the
-// logits of a piece or what the tile kernel reads.
+// logits of a piece (few rows: and a copy of x where it is not aligned) or what the tile
+// kernel reads.
 struct LossRoom {
     bool tiles;
     int64_t piece, parts;
-    size_t stats, picked, z;
+    size_t stats, picked, z, x;
     TileRoom t;
-    size_t all() const { return stats + picked + z + t.all(); }
+    size_t all() const { return stats + picked + z + x + t.all(); }
 };
 LossRoom loss_room(int64_t m, int64_t k, int64_t v, int gs, int dt)
 {
@@ -338,6 +425,8 @@ LossRoom loss_room(int64_t m, int64_t k, int64_t v, int gs, int dt)
         r.t = tile_room(m, k, r.piece, gs);
     else
         r.z = up16((size_t)m * (size_t)r.piece * 4);
+    if (rows_product(m, dt))
+        r.x = piece_bytes(m, k);
     return r;
 }
 
@@ -364,7 +453,7 @@ LossGradRoom loss_grad_room(int64_t m, int64_t k, int64_t v, int gs, int dt)
     else
         r.z = up16((size_t)m * (size_t)r.piece * 4);
     r.dz = dt == DT_F32 ? 0 : up16((size_t)m * (size_t)r.stride * 2);
-    r.x = grad_tile_sizes(r.piece, k, dt) ? piece_bytes(m, k) : 0;
+    r.x = rows_product(m, dt) || grad_tile_sizes(r.piece, k, dt) ? piece_bytes(m, k) : 0;
     // The last piece may be shorter, and its plans others.
     for (const int64_t n : {r.piece, v - (v - 1) / r.piece * r.piece})
         for (const bool tiles : {false, true})
@@ -419,6 +508,15 @@ hipError_t launch_loss(const LossArgs& a, hipStream_t st)
         if (hipError_t e = tile_begin(t, r.t, room, a.x, a.dt, a.M, a.K, a.bits, a.gs, a.V, a.targets, st); e != hipSuccess)
             return e;
     }
+    // Few rows whose logits are one piece, of a vocabulary that a block reads in some
+    // microseconds, need no parts.
+    const bool few = !r.tiles && a.M <= 16 && r.piece == a.V && a.V <= (1 << 18);
+    const void* x = a.x;
+    if (rows_product(a.M, a.dt)) {
+        int64_t stride = a.K;   // whole pieces: it stays
+        if (hipError_t e = pieces_of_rows(x, a.M, a.K, room + r.z, &stride, st); e != hipSuccess)
+            return e;
+    }
     for (int64_t v0 = 0; v0 < a.V; v0 += r.piece) {
         const int64_t n = std::min(r.piece, a.V - v0), parts = (n + kPart - 1) / kPart;
         if (r.tiles) {
@@ -427,8 +525,12 @@ hipError_t launch_loss(const LossArgs& a, hipStream_t st)
                 return e;
             continue;
         }
-        if (hipError_t e = logits(a.x, a.dt, a.M, a.K, a.w, a.bits, a.gs, v0, n, z, st); e != hipSuccess)
+        if (hipError_t e = logits(x, a.dt, a.M, a.K, a.w, a.bits, a.gs, v0, n, z, st); e != hipSuccess)
             return e;
+        if (few) {
+            hipLaunchKernelGGL(loss_rows_kernel, dim3((unsigned)a.M), dim3(1024), 0, st, z, a.V, a.targets, a.loss, a.lse);
+            return hipGetLastError();
+        }
         hipLaunchKernelGGL(loss_parts_kernel, wide_grid(a.M * parts, 256), dim3(256), 0, st, z, a.M, n, (int)parts, v0,
                            a.targets, stats, picked);
         if (hipError_t e = hipGetLastError(); e != hipSuccess)
@@ -473,7 +575,7 @@ hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t st)
             return e;
     }
     const void* xs = a.x;
-    if (tiles && a.dscales != nullptr) {
+    if (rows_product(a.M, a.dt) || (tiles && a.dscales != nullptr)) {
         int64_t stride = a.K;   // whole pieces: it stays
         if (hipError_t e = pieces_of_rows(xs, a.M, a.K, xcopy, &stride, st); e != hipSuccess)
             return e;
@@ -494,7 +596,7 @@ hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t st)
             if (hipError_t e = tile_piece(t, r.t, room, w, a.bits, a.dt, v0, n, st); e != hipSuccess)
                 return e;
         } else {
-            if (hipError_t e = logits(a.x, a.dt, a.M, a.K, a.w, a.bits, a.gs, v0, n, z, st); e != hipSuccess)
+            if (hipError_t e = logits(xs, a.dt, a.M, a.K, a.w, a.bits, a.gs, v0, n, z, st); e != hipSuccess)
                 return e;
             if (hipError_t e = dz_of(a, z, v0, n, half ? scale : nullptr, dz, stride, st); e != hipSuccess)
                 return e;

@@ -94,7 +94,8 @@ template <int BITS, int UPL, int MT = 1> constexpr int rowstream_depth()
         return d;
 }
 
-template <int BITS, int DT, int MT, int UPL, int WPB, bool WIDE, int KL, int NMAT = 1>
+// ODT: the output's type, where it is not the activations' (fp32; one matrix).
+template <int BITS, int DT, int MT, int UPL, int WPB, bool WIDE, int KL, int NMAT = 1, int ODT = DT>
 __global__ __launch_bounds__(64 * WPB) void qgemv_rowstream_kernel(RowStreamArgs a)
 {
     using PX = RowStreamPair<DT>;
@@ -130,7 +131,7 @@ __global__ __launch_bounds__(64 * WPB) void qgemv_rowstream_kernel(RowStreamArgs
         rb[t] = make_rsrc(t ? a.up_biases : a.biases, (uint32_t)a.N * groups_row * 2);
     }
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, (uint32_t)a.M * (uint32_t)a.K * 2);
-    St* y = static_cast<St*>(a.y);
+    auto* const y = static_cast<typename Elem<ODT>::storage*>(a.y);
     uint32_t gofs[UPL];
 #pragma unroll
     for (int j = 0; j < UPL; ++j)
@@ -319,7 +320,7 @@ __global__ __launch_bounds__(64 * WPB) void qgemv_rowstream_kernel(RowStreamArgs
                             }
                             v = act_f32(a.act, v) * u;
                         }
-                        y[at] = E::from_f32(v);
+                        y[at] = Elem<ODT>::from_f32(v);
                     }
         }
     }

@@ -334,7 +334,8 @@ __host__ __device__ constexpr uint32_t skinny_lds_bytes(int waves, int nmat)
     return (uint32_t)waves * skinny_wave_lds(nmat);
 }
 
-template <int BITS, int DT, int NMAT, int GU>
+// ODT: the output's type, where it is not the activations' (fp32).
+template <int BITS, int DT, int NMAT, int GU, int ODT = DT>
 __global__ __launch_bounds__(64 * kSkinnyMaxWaves) void qgemv_skinny_kernel(GemvKernelArgs a, SkinnyShape sh)
 {
     using M16 = SkMfma<DT>;
@@ -674,7 +675,7 @@ __global__ __launch_bounds__(64 * kSkinnyMaxWaves) void qgemv_skinny_kernel(Gemv
                 uint32_t off = OOB;
                 if (m < rows && n < r_hi) {
                     const uint32_t pr = a.perm != nullptr ? (uint32_t)a.perm[start + m] : (uint32_t)(start + m);
-                    off = (pr * (uint32_t)R + (uint32_t)n) * (uint32_t)SB;
+                    off = (pr * (uint32_t)R + (uint32_t)n) * (uint32_t)sizeof(typename Elem<ODT>::storage);
                 }
                 float v = tot[0][r];
                 if constexpr (NMAT == 2) {
@@ -684,7 +685,7 @@ __global__ __launch_bounds__(64 * kSkinnyMaxWaves) void qgemv_skinny_kernel(Gemv
                     }
                     v = act_f32(a.act, tot[0][r]) * tot[1][r];
                 }
-                buffer_store_elem<DT>(E::from_f32(v), ro, off);
+                buffer_store_elem<ODT>(Elem<ODT>::from_f32(v), ro, off);
             }
         }
         // Every wave is done with the partial sums before the next tile.
@@ -697,26 +698,26 @@ __global__ __launch_bounds__(64 * kSkinnyMaxWaves) void qgemv_skinny_kernel(Gemv
 namespace qp {
 
 // Launch one instance (its LDS size is allowed once per instance and device).
-template <int BITS, int DT, int NMAT, int GU>
+template <int BITS, int DT, int NMAT, int GU, int ODT>
 hipError_t skinny_launch_one(const GemvKernelArgs& k, const SkinnyShape& sh, dim3 grid, hipStream_t st)
 {
     static std::atomic<uint64_t> lds{0};   // per instantiation
-    if (hipError_t e = allow_lds(lds, reinterpret_cast<const void*>(&qgemv_skinny_kernel<BITS, DT, NMAT, GU>),
+    if (hipError_t e = allow_lds(lds, reinterpret_cast<const void*>(&qgemv_skinny_kernel<BITS, DT, NMAT, GU, ODT>),
                                  (int)skinny_lds_bytes(kSkinnyMaxWaves, NMAT)); e != hipSuccess)
         return e;
     const int waves = sh.ks * sh.wr;
-    hipLaunchKernelGGL((qgemv_skinny_kernel<BITS, DT, NMAT, GU>), grid, dim3(64 * waves),
+    hipLaunchKernelGGL((qgemv_skinny_kernel<BITS, DT, NMAT, GU, ODT>), grid, dim3(64 * waves),
                        skinny_lds_bytes(waves, NMAT), st, k, sh);
     return hipGetLastError();
 }
 
-template <int BITS, int DT, int NMAT>
+template <int BITS, int DT, int NMAT, int ODT = DT>
 hipError_t skinny_launch(const GemvKernelArgs& k, const SkinnyShape& sh, dim3 grid, hipStream_t st)
 {
     switch (k.gs) {
-    case 32: return skinny_launch_one<BITS, DT, NMAT, 1>(k, sh, grid, st);
-    case 64: return skinny_launch_one<BITS, DT, NMAT, 2>(k, sh, grid, st);
-    case 128: return skinny_launch_one<BITS, DT, NMAT, 4>(k, sh, grid, st);
+    case 32: return skinny_launch_one<BITS, DT, NMAT, 1, ODT>(k, sh, grid, st);
+    case 64: return skinny_launch_one<BITS, DT, NMAT, 2, ODT>(k, sh, grid, st);
+    case 128: return skinny_launch_one<BITS, DT, NMAT, 4, ODT>(k, sh, grid, st);
     }
     return hipErrorInvalidValue;
 }

@@ -43,7 +43,7 @@ __host__ __device__ constexpr uint32_t skinny4_wave_lds()
 static_assert(2 * sk4_code_buf<6>() <= 16 * kSkinnyXRow && (uint32_t)kSkinnyRG * 1024u <= 16 * kSkinnyXRow,
               "code buffers and partial sums within the staging region");
 
-template <int BITS, int DT, int GU>
+template <int BITS, int DT, int GU, int ODT = DT>   // ODT: the output's type
 __global__ __launch_bounds__(64 * kSkinnyMaxWaves) void qgemv_skinny4_kernel(GemvKernelArgs a, SkinnyShape sh)
 {
     static_assert(BITS == 2 || BITS == 3 || BITS == 4 || BITS == 6, "2-, 3-, 4- and 6-bit codes");
@@ -340,31 +340,31 @@ __global__ __launch_bounds__(64 * kSkinnyMaxWaves) void qgemv_skinny4_kernel(Gem
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int m = 4 * g + r;
-            const uint32_t off = (m < rows && n < r_hi) ? ((uint32_t)m * (uint32_t)R + (uint32_t)n) * (uint32_t)SB : OOB;
-            buffer_store_elem<DT>(E::from_f32(tot[r]), ro, off);
+            const uint32_t off = (m < rows && n < r_hi) ? ((uint32_t)m * (uint32_t)R + (uint32_t)n) * (uint32_t)sizeof(typename Elem<ODT>::storage) : OOB;
+            buffer_store_elem<ODT>(Elem<ODT>::from_f32(tot[r]), ro, off);
         }
     }
 }
 
-template <int BITS, int DT, int GU>
+template <int BITS, int DT, int GU, int ODT>
 hipError_t skinny4_launch_one(const GemvKernelArgs& k, const SkinnyShape& sh, dim3 grid, hipStream_t st)
 {
     static std::atomic<uint64_t> lds{0};   // per instantiation
-    if (hipError_t e = allow_lds(lds, reinterpret_cast<const void*>(&qgemv_skinny4_kernel<BITS, DT, GU>),
+    if (hipError_t e = allow_lds(lds, reinterpret_cast<const void*>(&qgemv_skinny4_kernel<BITS, DT, GU, ODT>),
                                  (int)(kSkinnyMaxWaves * skinny4_wave_lds())); e != hipSuccess)
         return e;
     const int waves = sh.ks * sh.wr;
-    hipLaunchKernelGGL((qgemv_skinny4_kernel<BITS, DT, GU>), grid, dim3(64 * waves), waves * skinny4_wave_lds(), st, k, sh);
+    hipLaunchKernelGGL((qgemv_skinny4_kernel<BITS, DT, GU, ODT>), grid, dim3(64 * waves), waves * skinny4_wave_lds(), st, k, sh);
     return hipGetLastError();
 }
 
-template <int BITS, int DT>
+template <int BITS, int DT, int ODT = DT>
 hipError_t skinny4_launch(const GemvKernelArgs& k, const SkinnyShape& sh, dim3 grid, hipStream_t st)
 {
     switch (k.gs) {
-    case 32: return skinny4_launch_one<BITS, DT, 1>(k, sh, grid, st);
-    case 64: return skinny4_launch_one<BITS, DT, 2>(k, sh, grid, st);
-    case 128: return skinny4_launch_one<BITS, DT, 4>(k, sh, grid, st);
+    case 32: return skinny4_launch_one<BITS, DT, 1, ODT>(k, sh, grid, st);
+    case 64: return skinny4_launch_one<BITS, DT, 2, ODT>(k, sh, grid, st);
+    case 128: return skinny4_launch_one<BITS, DT, 4, ODT>(k, sh, grid, st);
     }
     return hipErrorInvalidValue;
 }

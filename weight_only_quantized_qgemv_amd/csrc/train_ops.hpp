@@ -96,9 +96,11 @@ struct LossTileArgs {
     int64_t dz_stride;
     const float *lse, *dloss, *scale;   // [M], [M], and scale[0] a factor of dloss
 };
+// Logits of up to 16 rows of 16-bit x (16-byte aligned) as fp32 y (loss_rows.hip).
 #define QP_LOSS_DECL(B)                                                                                          \
     hipError_t launch_loss_prep_x_b##B(int dt, const LossTileArgs& a, const void* x, hipStream_t stream);       \
-    hipError_t launch_loss_tile_b##B(int dt, LossTileArgs a, hipStream_t stream);
+    hipError_t launch_loss_tile_b##B(int dt, LossTileArgs a, hipStream_t stream);                               \
+    hipError_t launch_loss_rows_b##B(const GemvArgs& a, hipStream_t stream);
 QP_LOSS_DECL(2)
 QP_LOSS_DECL(3)
 QP_LOSS_DECL(4)
