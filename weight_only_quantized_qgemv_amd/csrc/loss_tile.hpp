@@ -35,8 +35,6 @@ using gemm::CodeLayout;
 using gemm::CodeStage;
 using gemm::MfmaTraits;
 using gemm::code_swz;
-using gemm::dma12;
-using gemm::dma16;
 using gemm::lds_off;
 using gemm::rsrc;
 using gemm::swz;
@@ -74,6 +72,20 @@ template <int BITS, int FM, int WMW> constexpr int lds_bytes()
     return NA * 32 * FM * WMW * 128 + NC<BITS> * (CodeStage<BITS, LOSS_BN, 4 * WMW>::STAGE + 4 * WMW * 256);
 }
 
+// DMA of 16, 12 or 4 bytes a lane, from a lane's offset and a uniform one.
+__device__ __forceinline__ void dma16_at(__amdgpu_buffer_rsrc_t r, char* dst, uint32_t voff, int soff)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, voff, soff, 0, 0);
+}
+__device__ __forceinline__ void dma12_at(__amdgpu_buffer_rsrc_t r, char* dst, uint32_t voff, int soff)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 12, voff, soff, 0, 0);
+}
+__device__ __forceinline__ void dma4_at(__amdgpu_buffer_rsrc_t r, char* dst, uint32_t voff, int soff)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 4, voff, soff, 0, 0);
+}
+
 template <int BITS, int DT, int FM, int WMW, bool G32>
 __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
 {
@@ -88,10 +100,8 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
     constexpr int NCS = NC<BITS>;
     // As in gemm_core.hpp: step kt + 1 reads the activations and codes of kt + 2 at
     // its end; what was issued after them may be in flight when step kt ends.
-    constexpr int STEP_OPS = A_INSTR + C_INSTR + 1;
     constexpr int IN_FLIGHT = NCS > NA ? C_INSTR + 1 : 0;
     static_assert(NA == 3 && (NCS == 3 || NCS == 4), "prefetch depth");
-    (void)STEP_OPS;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     char* const a_st = lds;
     char* const c_st = a_st + NA * A_STAGE;
@@ -138,28 +148,27 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
     const uint32_t s_goff = wave < SB_WAVES ? (uint32_t)(wave & 1) * 256 + (uint32_t)lane * 4 : OOB;
     const int gs_steps = a.gs == 128 ? 1 : 0;   // log2 of the steps of a group (of 64 and more)
 
-    auto dma_a = [&](int kt, int stage) {
-#pragma unroll
-        for (int i = 0; i < A_INSTR; ++i)
-            dma16(rx, a_st + stage * A_STAGE + (wave * A_INSTR + i) * 1024, a_goff[i] + (uint32_t)kt * BK * 2);
+    // DMA operation o of step kt's: A_INSTR of the activations, C_INSTR of the codes, the
+    // scales. A row's place in the step goes into the scalar offset, which is not range
+    // checked: rows past the tile are past the range by their own, and the activations'
+    // last steps read on into the workspace behind them.
+    auto dma_a = [&](int kt, int stage, int i) {
+        dma16_at(rx, a_st + stage * A_STAGE + (wave * A_INSTR + i) * 1024, a_goff[i], kt * BK * 2);
     };
-    auto dma_c = [&](int kt, int stage) {
+    auto dma_c = [&](int kt, int stage, int i) {
         // The last step of 64 n + 32 features holds the row's last two units.
-        const uint32_t k = (uint32_t)kt * CL::RB, last = wrow - CL::RB, off = k < last ? k : last;
-#pragma unroll
-        for (int i = 0; i < C_INSTR; ++i) {
-            char* const dst = c_st + stage * C_STAGE + (wave * C_INSTR + i) * 1024;
-            if constexpr (CL::CS == 12)
-                dma12(rw, dst, c_goff[i] + off);
-            else
-                dma16(rw, dst, c_goff[i] + off);
-        }
+        const int k = kt * CL::RB, last = (int)wrow - CL::RB, off = k < last ? k : last;
+        char* const dst = c_st + stage * C_STAGE + (wave * C_INSTR + i) * 1024;
+        if constexpr (CL::CS == 12)
+            dma12_at(rw, dst, c_goff[i], off);
+        else
+            dma16_at(rw, dst, c_goff[i], off);
+    };
+    auto dma_s = [&](int kt, int stage) {
         int g = G32 ? 2 * kt : kt >> gs_steps;
         const int most = groups - (G32 ? 2 : 1);
         g = (g < most ? g : most) + (G32 ? wave >> 1 : 0);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rs, (__attribute__((address_space(3))) void*)(sb_st + stage * SB_STAGE + wave * 256), 4,
-            s_goff + (uint32_t)g * (uint32_t)a.np * 2, 0, 0, 0);
+        dma4_at(rs, sb_st + stage * SB_STAGE + wave * 256, s_goff, g * a.np * 2);
     };
     auto step_barrier = [&](auto VM) {
         __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(decltype(VM)::value));
@@ -171,8 +180,11 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
 #pragma unroll
     for (int s = 1 - NCS; s < 0; ++s) {
         if (s + NA - 1 >= 0)
-            dma_a(s + NA - 1, s + NA - 1);
-        dma_c(s + NCS - 1, s + NCS - 1);
+            for (int i = 0; i < A_INSTR; ++i)
+                dma_a(s + NA - 1, s + NA - 1, i);
+        for (int i = 0; i < C_INSTR; ++i)
+            dma_c(s + NCS - 1, s + NCS - 1, i);
+        dma_s(s + NCS - 1, s + NCS - 1);
     }
 
     // The biases: X (hi, lo) times b, 16 groups an instruction; they start the totals.
@@ -223,15 +235,17 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
 
     // B fragments of column block j for a step: the unit `half` of its row as 16 code
     // pairs, four a matrix instruction; with groups of 32 the halves of the wave swap so
-    // that an instruction's two halves are of one unit.
-    uint32_t bq[FN][16];
+    // that an instruction's two halves are of one unit. Loaded, and converted in four
+    // parts (groups of 32: two).
+    uint32_t bq[FN][16], raw[FN][BITS];
     float sc[FN][G32 ? 2 : 1];
-    auto convert = [&](auto J, int stage) {
+    uint16_t raws[FN][G32 ? 2 : 1];
+    auto load_codes = [&](auto J, int stage) {
         constexpr int j = decltype(J)::value;
         const int r = wn * WN + 32 * j + c32;
         const char* const row = c_st + stage * C_STAGE + r * CL::SLOT_ROW;
         const int sw = code_swz<BITS>(r);
-        uint32_t w[BITS];
+        uint32_t(&w)[BITS] = raw[j];
         if constexpr (BITS == 4 || BITS == 3) {
             const u32x4_t v = *reinterpret_cast<const u32x4_t*>(row + ((half ^ sw) << 4));
 #pragma unroll
@@ -249,19 +263,34 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
                 w[2 * i + 1] = v[1];
             }
         }
-        code_pairs<BITS, DT>(w, 0u, bq[j]);
-        if constexpr (G32) {
-#pragma unroll
-            for (int p = 0; p < 8; ++p) {
-                const auto x = __builtin_amdgcn_permlane32_swap(bq[j][p], bq[j][8 + p], false, false);
-                bq[j][p] = x[0];
-                bq[j][8 + p] = x[1];
-            }
-        }
         const char* const sb = sb_st + stage * SB_STAGE + 2 * r;
 #pragma unroll
         for (int u = 0; u < (G32 ? 2 : 1); ++u)
-            sc[j][u] = Elem<DT>::to_f32(*reinterpret_cast<const uint16_t*>(sb + 512 * u));
+            raws[j][u] = *reinterpret_cast<const uint16_t*>(sb + 512 * u);
+    };
+    auto convert = [&](auto J, auto P) {
+        constexpr int j = decltype(J)::value, p = decltype(P)::value;
+        uint32_t q[16];
+        code_pairs<BITS, DT>(raw[j], 0u, q);   // (of which the rest is dropped)
+        if constexpr (G32) {
+            if constexpr (p < 2) {
+#pragma unroll
+                for (int i = 4 * p; i < 4 * p + 4; ++i) {
+                    const auto x = __builtin_amdgcn_permlane32_swap(q[i], q[8 + i], false, false);
+                    bq[j][i] = x[0];
+                    bq[j][8 + i] = x[1];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 4 * p; i < 4 * p + 4; ++i)
+                bq[j][i] = q[i];
+        }
+    };
+    auto take_scales = [&](auto J) {
+#pragma unroll
+        for (int u = 0; u < (G32 ? 2 : 1); ++u)
+            sc[J][u] = Elem<DT>::to_f32(raws[J][u]);
     };
     // Fragment kk of the rows of tile i.
     auto a_frag = [&](int stage, int i, int kk) {
@@ -271,57 +300,75 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
     auto b_frag = [&](int j, int kk) {
         return __builtin_bit_cast(frag_t, u32x4_t{bq[j][4 * kk], bq[j][4 * kk + 1], bq[j][4 * kk + 2], bq[j][4 * kk + 3]});
     };
-    static_for<FN>([&](auto J) { convert(J, 0); });
-
-    // A step is 2 FM chains of 4 matrix instructions (groups of 32: 4 FM of 2), each into
-    // one of two accumulators; while a chain runs, the one before it is scaled and added.
-    // The last chains of a row block take the next one's fragments into the registers that
-    // they have read; at the step's end the next step's codes are converted, column block
-    // 0's under the last chain, block 1's after it.
-    constexpr int U = G32 ? 2 : 1, L = 4 / U, CHAINS = FM * FN * U;
+    // A step is 2 FM chains of L = 4 matrix instructions (groups of 32: 4 FM of 2), each
+    // into one of two accumulators, and every instruction has its share of the other work
+    // beside it: the chain before is scaled and added once its result is there; the last
+    // chains of a row block take the next one's fragments into the registers that they
+    // have read; column block 0's codes of the next step are converted under the last
+    // chain, block 1's under the next step's first; the DMA is spread over the first.
+    constexpr int U = G32 ? 2 : 1, L = 4 / U, CHAINS = FM * FN * U, DMAS = A_INSTR + C_INSTR + 1;
     frag_t af[4];
     f32x16_t acc[2];
-    auto scale_chain = [&](auto C) {
+    auto scale_part = [&](auto C, auto R0, auto R1) {   // registers R0 .. R1 - 1 of chain C's sums
         constexpr int c = decltype(C)::value, i = c / (FN * U), j = c / U % FN, u = c % U;
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
+        for (int r = decltype(R0)::value; r < decltype(R1)::value; ++r)
             total[i][j][r] = __builtin_fmaf(sc[j][u], acc[c & 1][r], total[i][j][r]);
     };
+    static_for<FN>([&](auto J) {
+        load_codes(J, 0);
+        take_scales(J);
+    });
+    static_for<4>([&](auto P) { convert(std::integral_constant<int, 0>{}, P); });
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
         af[kk] = a_frag(0, 0, kk);
+    acc[(CHAINS - 1) & 1] = f32x16_t{};   // before the first step: nothing to add
     int a_cur = 0, c_cur = 0;
     for (int kt = 0; kt < KT; ++kt) {
         const int a_new = a_cur == 0 ? NA - 1 : a_cur - 1;
         const int c_new = c_cur == 0 ? NCS - 1 : c_cur - 1;
         const int a_nxt = a_cur + 1 == NA ? 0 : a_cur + 1;
         const int c_nxt = c_cur + 1 == NCS ? 0 : c_cur + 1;
-        dma_a(kt + NA - 1, a_new);
-        dma_c(kt + NCS - 1, c_new);
-        static_for<CHAINS>([&](auto C) {
-            constexpr int c = decltype(C)::value, i = c / (FN * U), j = c / U % FN, u = c % U;
-            static_for<L>([&](auto KL) {
-                constexpr int kk = L * u + (int)decltype(KL)::value;
-                if constexpr ((int)decltype(KL)::value == 0)
-                    acc[c & 1] = T::mfma(af[kk], b_frag(j, kk), f32x16_t{});
+        static_for<CHAINS * L>([&](auto Q) {
+            constexpr int q = decltype(Q)::value, c = q / L, l = q % L, i = c / (FN * U), j = c / U % FN, u = c % U;
+            constexpr int kk = L * u + l, prev = (c + CHAINS - 1) % CHAINS;
+            if constexpr (l == 0)
+                acc[c & 1] = T::mfma(af[kk], b_frag(j, kk), f32x16_t{});
+            else
+                acc[c & 1] = T::mfma(af[kk], b_frag(j, kk), acc[c & 1]);
+            if constexpr (j == FN - 1)
+                af[kk] = i + 1 < FM ? a_frag(a_cur, i + 1, kk) : a_frag(a_nxt, 0, kk);
+            if constexpr (q < DMAS) {
+                if constexpr (q < A_INSTR)
+                    dma_a(kt + NA - 1, a_new, q);
+                else if constexpr (q < A_INSTR + C_INSTR)
+                    dma_c(kt + NCS - 1, c_new, q - A_INSTR);
                 else
-                    acc[c & 1] = T::mfma(af[kk], b_frag(j, kk), acc[c & 1]);
-                if constexpr (j == FN - 1)
-                    af[kk] = i + 1 < FM ? a_frag(a_cur, i + 1, kk) : a_frag(a_nxt, 0, kk);
-            });
-            if constexpr (c > 0)
-                scale_chain(std::integral_constant<int, c - 1>{});
-            if constexpr (c < CHAINS - 1)
-                __builtin_amdgcn_sched_barrier(0);
+                    dma_s(kt + NCS - 1, c_new);
+            }
+            constexpr int R0 = L == 4 ? (l == 0 ? 0 : l == 1 ? 0 : l == 2 ? 6 : 11) : (l == 0 ? 0 : 4);
+            constexpr int R1 = L == 4 ? (l == 0 ? 0 : l == 1 ? 6 : l == 2 ? 11 : 16) : (l == 0 ? 4 : 16);
+            scale_part(std::integral_constant<int, prev>{}, std::integral_constant<int, R0>{}, std::integral_constant<int, R1>{});
+            // Four slots each for the two conversions.
+            if constexpr (q < 4)
+                convert(std::integral_constant<int, 1>{}, std::integral_constant<int, q>{});
+            if constexpr (q == CHAINS * L - 6)
+                load_codes(std::integral_constant<int, 0>{}, c_nxt);
+            if constexpr (q >= CHAINS * L - (G32 ? 2 : 4))
+                convert(std::integral_constant<int, 0>{}, std::integral_constant<int, q - (CHAINS * L - (G32 ? 2 : 4))>{});
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (q == CHAINS * L - 1)
+                take_scales(std::integral_constant<int, 0>{});
+            if constexpr (c == 0 && l == L - 1)
+                take_scales(std::integral_constant<int, 1>{});
         });
-        convert(std::integral_constant<int, 0>{}, c_nxt);
-        __builtin_amdgcn_sched_barrier(0);
-        scale_chain(std::integral_constant<int, CHAINS - 1>{});
-        convert(std::integral_constant<int, 1>{}, c_nxt);
+        load_codes(std::integral_constant<int, 1>{}, c_nxt);
         step_barrier(std::integral_constant<int, IN_FLIGHT>{});
         a_cur = a_nxt;
         c_cur = c_nxt;
     }
+    scale_part(std::integral_constant<int, CHAINS - 1>{}, std::integral_constant<int, 0>{}, std::integral_constant<int, 16>{});
     __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
     __builtin_amdgcn_s_barrier();   // the LDS is free
     // Opaque here, so that the close's addresses are formed now and not kept in
