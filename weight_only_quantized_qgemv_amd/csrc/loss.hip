@@ -347,31 +347,25 @@ hipError_t prep_w(const LossTileArgs& a, const void* scales, const void* biases,
 // What the tile kernel reads beside the codes, laid out once a call (x) or a piece (the
 // weight's): sizes in bytes.
 struct TileRoom {
-    int64_t kp, gp, np;
-    size_t xp, xs, st, bp;
-    size_t all() const { return xp + xs + st + bp; }
+    int64_t xn, gp;
+    size_t xp, st, bp;
+    size_t all() const { return xp + st + bp; }
 };
 TileRoom tile_room(int64_t m, int64_t k, int64_t piece, int gs)
 {
-    TileRoom t{};
-    t.kp = (k + 63) / 64 * 64;
-    t.gp = (k / gs + 15) / 16 * 16;
-    t.np = (piece + LOSS_BN - 1) / LOSS_BN * LOSS_BN;
-    t.xp = (size_t)m * (size_t)t.kp * 2;
-    t.xs = (size_t)m * (size_t)t.gp * 4;
-    t.st = (size_t)(k / gs) * (size_t)t.np * 2;
-    t.bp = (size_t)piece * (size_t)t.gp * 2;
-    return {t.kp, t.gp, t.np, up16(t.xp), up16(t.xs), up16(t.st), up16(t.bp)};
+    const int64_t gp = (k / gs + 31) / 32 * 32, xn = 2 * gp + (k + 63) / 64 * 64;
+    const int64_t np = (piece + LOSS_BN - 1) / LOSS_BN * LOSS_BN;
+    return {xn, gp, up16((size_t)m * (size_t)xn * 2), up16((size_t)(k / gs) * (size_t)np * 2),
+            up16((size_t)piece * (size_t)gp * 2)};
 }
 // The kernel's arguments for x, which is laid out at `room`; the weight's follow it.
 hipError_t tile_begin(LossTileArgs& t, const TileRoom& r, char* room, const void* x, int dt, int64_t m, int64_t k,
                       int bits, int gs, int64_t vocab, const int32_t* targets, hipStream_t st)
 {
     t.xp = room;
-    t.xs = room + r.xp;
-    t.st = room + r.xp + r.xs;
+    t.st = room + r.xp;
     t.M = (int)m; t.K = (int)k; t.gs = gs;
-    t.kp = (int)r.kp; t.gp = (int)r.gp;
+    t.xn = (int)r.xn; t.gp = (int)r.gp;
     t.vocab = vocab;
     t.targets = targets;
     t.stat_rows = m;
@@ -387,7 +381,7 @@ hipError_t tile_piece(LossTileArgs& t, const TileRoom& r, char* room, const QWei
     t.part0 = (int)(v0 / LOSS_BN);
     // The biases as they lie, where their rows are whole 16-byte pieces.
     const bool as_is = t.gp == t.K / t.gs && aligned16(w.biases);
-    char* const bp = room + r.xp + r.xs + r.st;
+    char* const bp = room + r.xp + r.st;
     t.bp = as_is ? w.biases : bp;
     if (hipError_t e = prep_w(t, w.scales, w.biases, as_is ? nullptr : bp, st); e != hipSuccess)
         return e;

@@ -40,12 +40,13 @@ hipError_t by_rows(const LossTileArgs& a, hipStream_t st)
 
 template <int DT> hipError_t prep_x(const LossTileArgs& a, const void* x, hipStream_t st)
 {
-    const int64_t waves = (int64_t)a.M * ((a.kp / 32 + 63) / 64), blocks = (waves + 3) / 4;
+    const int units = (a.xn - 2 * a.gp) / 32;
+    const int64_t waves = (int64_t)a.M * ((units + 63) / 64), blocks = (waves + 3) / 4;
     if (!grid_fits(blocks, 256))
         return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((losstile::loss_prep_x_kernel<QP_BITS, DT>), dim3((unsigned)blocks), dim3(256), 0, st,
-                       static_cast<const uint16_t*>(x), (int64_t)a.M, a.K, a.gs, a.kp, a.gp,
-                       static_cast<u32x4_t*>(const_cast<void*>(a.xp)), static_cast<uint16_t*>(const_cast<void*>(a.xs)));
+                       static_cast<const uint16_t*>(x), (int64_t)a.M, a.K, a.gs, a.xn, a.gp,
+                       static_cast<uint16_t*>(const_cast<void*>(a.xp)));
     return hipGetLastError();
 }
 

@@ -47,29 +47,26 @@ template <int BITS> constexpr int NC = BITS >= 6 ? 3 : 4;
 // e^x for the closes: 2^-24 (1 + |x|) of itself, half the instructions of expf.
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
 
-// The maximum and the sum over each half of a wave, in all its lanes.
-__device__ __forceinline__ float max32(float v)
+// The maximum and the sum over eight lanes in a row, in all of them.
+__device__ __forceinline__ float max8(float v)
 {
     v = fmaxf(v, dpp_f32<0xB1>(v));
     v = fmaxf(v, dpp_f32<0x4E>(v));
-    v = fmaxf(v, dpp_f32<0x141>(v));
-    v = fmaxf(v, dpp_f32<0x140>(v));
-    const auto x = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
-    return fmaxf(__builtin_bit_cast(float, (uint32_t)x[0]), __builtin_bit_cast(float, (uint32_t)x[1]));
+    return fmaxf(v, dpp_f32<0x141>(v));
 }
-__device__ __forceinline__ float sum32(float v)
+__device__ __forceinline__ float sum8(float v)
 {
     v += dpp_f32<0xB1>(v);
     v += dpp_f32<0x4E>(v);
-    v += dpp_f32<0x141>(v);
-    v += dpp_f32<0x140>(v);
-    const auto x = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
-    return __builtin_bit_cast(float, (uint32_t)x[0]) + __builtin_bit_cast(float, (uint32_t)x[1]);
+    return v + dpp_f32<0x141>(v);
 }
 
+// Stages of the products, and then of the close.
 template <int BITS, int FM, int WMW> constexpr int lds_bytes()
 {
-    return NA * 32 * FM * WMW * 128 + NC<BITS> * (CodeStage<BITS, LOSS_BN, 4 * WMW>::STAGE + 4 * WMW * 256);
+    constexpr int steps = NA * 32 * FM * WMW * 128 + NC<BITS> * (CodeStage<BITS, LOSS_BN, 4 * WMW>::STAGE + 4 * WMW * 256);
+    constexpr int close = 4 * WMW * 32 * 68 * 4 + 4 * 32 * FM * WMW * (int)sizeof(Stat);
+    return steps > close ? steps : close;
 }
 
 // DMA of 16, 12 or 4 bytes a lane, from a lane's offset and a uniform one.
@@ -117,8 +114,8 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, c32 = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WGN, wn = wave % WGN;
-    const uint32_t xrow = (uint32_t)a.kp * 2, wrow = (uint32_t)a.K * BITS / 8;
-    const int KT = a.kp / BK, groups = a.K / a.gs, rows_left = a.M - m0;
+    const uint32_t xrow = (uint32_t)a.xn * 2, wrow = (uint32_t)a.K * BITS / 8;
+    const int KT = (a.K + BK - 1) / BK, BT = a.gp / 32, groups = a.K / a.gs, rows_left = a.M - m0;
 
     // A tile's own rows as resources: their offsets are below 2^31 whatever M and N are.
     const __amdgpu_buffer_rsrc_t rx = rsrc(static_cast<const char*>(a.xp) + (size_t)m0 * xrow,
@@ -133,7 +130,7 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
 #pragma unroll
     for (int i = 0; i < A_INSTR; ++i) {
         const int r = 8 * (wave * A_INSTR + i) + (lane >> 3);
-        a_goff[i] = r < rows_left ? (uint32_t)r * xrow + (uint32_t)(((lane & 7) ^ swz(r)) * 16) : OOB;
+        a_goff[i] = (uint32_t)r * xrow + (uint32_t)(((lane & 7) ^ swz(r)) * 16);   // (past the rows: past the range)
     }
     uint32_t c_goff[C_INSTR];
 #pragma unroll
@@ -156,8 +153,9 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
         dma16_at(rx, a_st + stage * A_STAGE + (wave * A_INSTR + i) * 1024, a_goff[i], kt * BK * 2);
     };
     auto dma_c = [&](int kt, int stage, int i) {
-        // The last step of 64 n + 32 features holds the row's last two units.
-        const int k = kt * CL::RB, last = (int)wrow - CL::RB, off = k < last ? k : last;
+        // The last step of 64 n + 32 features holds the row's last two units; the biases'
+        // steps, before step 0, have none of their own.
+        const int k = (kt > 0 ? kt : 0) * CL::RB, last = (int)wrow - CL::RB, off = k < last ? k : last;
         char* const dst = c_st + stage * C_STAGE + (wave * C_INSTR + i) * 1024;
         if constexpr (CL::CS == 12)
             dma12_at(rw, dst, c_goff[i], off);
@@ -165,7 +163,7 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
             dma16_at(rw, dst, c_goff[i], off);
     };
     auto dma_s = [&](int kt, int stage) {
-        int g = G32 ? 2 * kt : kt >> gs_steps;
+        int g = kt < 0 ? 0 : G32 ? 2 * kt : kt >> gs_steps;
         const int most = groups - (G32 ? 2 : 1);
         g = (g < most ? g : most) + (G32 ? wave >> 1 : 0);
         dma4_at(rs, sb_st + stage * SB_STAGE + wave * 256, s_goff, g * a.np * 2);
@@ -177,51 +175,77 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
         asm volatile("" ::: "memory");
     };
 
+    // Steps of the pipeline: BT of the biases, then KT of the codes.
 #pragma unroll
     for (int s = 1 - NCS; s < 0; ++s) {
         if (s + NA - 1 >= 0)
             for (int i = 0; i < A_INSTR; ++i)
                 dma_a(s + NA - 1, s + NA - 1, i);
         for (int i = 0; i < C_INSTR; ++i)
-            dma_c(s + NCS - 1, s + NCS - 1, i);
-        dma_s(s + NCS - 1, s + NCS - 1);
+            dma_c(s + NCS - 1 - BT, s + NCS - 1, i);
+        dma_s(s + NCS - 1 - BT, s + NCS - 1);
     }
-
-    // The biases: X (hi, lo) times b, 16 groups an instruction; they start the totals.
     f32x16_t total[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j)
             total[i][j] = f32x16_t{};
+
+    // Fragment kk of the rows of tile i. Groups of 32 (and X): an instruction's two halves
+    // are 16 positions of one half of the step.
+    auto a_frag = [&](int stage, int i, int kk) {
+        const int chunk = G32 ? 4 * (kk >> 1) + (kk & 1) + 2 * half : kk + 4 * half;
+        return *reinterpret_cast<const frag_t*>(a_st + stage * A_STAGE + lds_off(wm * WM + 32 * i + c32, chunk));
+    };
+    int a_cur = 0, c_cur = 0;
+    // The biases: 32 groups a step, instructions 0 and 1 the high and the low part of X
+    // times b of the first 16 groups, 2 and 3 of the others. b's fragments come from memory,
+    // a step ahead.
     {
         const uint32_t grow = (uint32_t)a.gp * 2;
-        const __amdgpu_buffer_rsrc_t rh = rsrc(static_cast<const char*>(a.xs) + (size_t)m0 * 2 * grow,
-                                               (uint32_t)(rows_left < BM ? rows_left : BM) * 2 * grow);
         const __amdgpu_buffer_rsrc_t rb = rsrc(static_cast<const char*>(a.bp) + (size_t)n0 * grow,
                                                (uint32_t)(cols_left < BN ? cols_left : BN) * grow);
-        for (uint32_t c = 0; c < grow; c += 32) {
-            frag_t bf[FN], xh[FM], xl[FM];
+        frag_t bf[FN][2];
+        auto load_b = [&](int bt) {
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                const int col = wn * WN + 32 * j + c32;
-                bf[j] = __builtin_bit_cast(frag_t, __builtin_amdgcn_raw_buffer_load_b128(
-                    rb, col < cols_left ? (uint32_t)col * grow + c + 16 * half : OOB, 0, 0));
-            }
+            for (int j = 0; j < FN; ++j)
 #pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                const int row = wm * WM + 32 * i + c32;
-                const uint32_t at = row < rows_left ? (uint32_t)row * 2 * grow + c + 16 * half : OOB;
-                xh[i] = __builtin_bit_cast(frag_t, __builtin_amdgcn_raw_buffer_load_b128(rh, at, 0, 0));
-                xl[i] = __builtin_bit_cast(frag_t, __builtin_amdgcn_raw_buffer_load_b128(rh, at == OOB ? OOB : at + grow, 0, 0));
-            }
+                for (int h = 0; h < 2; ++h)
+                    bf[j][h] = __builtin_bit_cast(frag_t, __builtin_amdgcn_raw_buffer_load_b128(
+                        rb, (uint32_t)(wn * WN + 32 * j + c32) * grow + (uint32_t)bt * 64 + 32 * h + 16 * half, 0, 0));
+        };
+        load_b(0);
+        step_barrier(std::integral_constant<int, 0>{});
+        for (int bt = 0; bt < BT; ++bt) {
+            const int a_new = a_cur == 0 ? NA - 1 : a_cur - 1, c_new = c_cur == 0 ? NCS - 1 : c_cur - 1;
+            frag_t b0[FN][2];
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    b0[j][h] = bf[j][h];
+            if (bt + 1 < BT)
+                load_b(bt + 1);
+#pragma unroll
+            for (int i = 0; i < A_INSTR; ++i)
+                dma_a(bt + NA - 1, a_new, i);
+#pragma unroll
+            for (int i = 0; i < C_INSTR; ++i)
+                dma_c(bt + NCS - 1 - BT, c_new, i);
+            dma_s(bt + NCS - 1 - BT, c_new);
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    total[i][j] = T::mfma(xl[i], bf[j], total[i][j]);
-                    total[i][j] = T::mfma(xh[i], bf[j], total[i][j]);
+                for (int kk = 3; kk >= 0; --kk) {   // (the low parts first)
+                    const frag_t x = a_frag(a_cur, i, kk);
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+                        total[i][j] = T::mfma(x, b0[j][kk >> 1], total[i][j]);
                 }
+            step_barrier(std::integral_constant<int, IN_FLIGHT>{});
+            a_cur = a_cur + 1 == NA ? 0 : a_cur + 1;
+            c_cur = c_cur + 1 == NCS ? 0 : c_cur + 1;
         }
         if constexpr (DT == DT_F16) {   // X was divided by 128, which keeps it inside fp16's range
 #pragma unroll
@@ -231,7 +255,6 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
                     total[i][j] *= 128.0f;
         }
     }
-    step_barrier(std::integral_constant<int, IN_FLIGHT>{});
 
     // B fragments of column block j for a step: the unit `half` of its row as 16 code
     // pairs, four a matrix instruction; with groups of 32 the halves of the wave swap so
@@ -292,11 +315,6 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
         for (int u = 0; u < (G32 ? 2 : 1); ++u)
             sc[J][u] = Elem<DT>::to_f32(raws[J][u]);
     };
-    // Fragment kk of the rows of tile i.
-    auto a_frag = [&](int stage, int i, int kk) {
-        const int chunk = G32 ? 4 * (kk >> 1) + (kk & 1) + 2 * half : kk + 4 * half;
-        return *reinterpret_cast<const frag_t*>(a_st + stage * A_STAGE + lds_off(wm * WM + 32 * i + c32, chunk));
-    };
     auto b_frag = [&](int j, int kk) {
         return __builtin_bit_cast(frag_t, u32x4_t{bq[j][4 * kk], bq[j][4 * kk + 1], bq[j][4 * kk + 2], bq[j][4 * kk + 3]});
     };
@@ -316,15 +334,14 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
             total[i][j][r] = __builtin_fmaf(sc[j][u], acc[c & 1][r], total[i][j][r]);
     };
     static_for<FN>([&](auto J) {
-        load_codes(J, 0);
+        load_codes(J, c_cur);
         take_scales(J);
     });
     static_for<4>([&](auto P) { convert(std::integral_constant<int, 0>{}, P); });
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
-        af[kk] = a_frag(0, 0, kk);
+        af[kk] = a_frag(a_cur, 0, kk);
     acc[(CHAINS - 1) & 1] = f32x16_t{};   // before the first step: nothing to add
-    int a_cur = 0, c_cur = 0;
     for (int kt = 0; kt < KT; ++kt) {
         const int a_new = a_cur == 0 ? NA - 1 : a_cur - 1;
         const int c_new = c_cur == 0 ? NCS - 1 : c_cur - 1;
@@ -341,7 +358,7 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
                 af[kk] = i + 1 < FM ? a_frag(a_cur, i + 1, kk) : a_frag(a_nxt, 0, kk);
             if constexpr (q < DMAS) {
                 if constexpr (q < A_INSTR)
-                    dma_a(kt + NA - 1, a_new, q);
+                    dma_a(BT + kt + NA - 1, a_new, q);
                 else if constexpr (q < A_INSTR + C_INSTR)
                     dma_c(kt + NCS - 1, c_new, q - A_INSTR);
                 else
@@ -377,67 +394,82 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
     asm volatile("" : "+v"(l));
     const int half2 = l >> 5, c = l & 31;
 
-    // Register r of a 32 x 32 tile: row 8 (r / 4) + 4 half + r % 4, column c.
-    struct Row {
-        float lse, g;
-        int32_t target;   // its column in the tile, or -1
-    };
-    Row* const rows = reinterpret_cast<Row*>(lds);
-    for (int r = wave * 64 + l; r < BM; r += 64 * WAVES) {
-        const bool in = r < rows_left;
-        const int64_t t = in ? (int64_t)a.targets[m0 + r] : -1;
-        const bool live = t >= 0 && t < a.vocab;
-        const int64_t at = t - a.v0 - n0;
-        Row p;
-        p.target = live && at >= 0 && at < BN ? (int32_t)at : -1;
-        p.lse = a.dz != nullptr && in ? a.lse[m0 + r] : 0.0f;
-        p.g = a.dz != nullptr && live ? a.dloss[m0 + r] * a.scale[0] : 0.0f;
-        rows[r] = p;
-    }
-    __syncthreads();
-    const int col0 = wn * WN + c, row0 = wm * WM + 4 * half2;
-    if (a.dz != nullptr) {
-        // dz, and zeros up to the next multiple of 8 columns. (A row without a target, or
-        // of g = 0, is zeros whatever its logits are.)
-        const uint32_t drow = (uint32_t)a.dz_stride * 2;
-        const __amdgpu_buffer_rsrc_t rd = rsrc(static_cast<char*>(a.dz) + (size_t)m0 * drow + (size_t)n0 * 2,
-                                               (uint32_t)(rows_left < BM ? rows_left : BM) * drow - (uint32_t)n0 * 2);
-        const int cols8 = (cols_left + 7) & ~7;
-        static_for<FM>([&](auto I) {
-            static_for<16>([&](auto R) {
-                constexpr int i = decltype(I)::value, r = decltype(R)::value;
-                const int row = row0 + 32 * i + 8 * (r >> 2) + (r & 3);
-                const Row p = rows[row];
-#pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    const int col = col0 + 32 * j;
-                    const float v = p.g * (exp_fast(total[i][j][r] - p.lse) - (p.target == col ? 1.0f : 0.0f));
-                    const uint32_t keep = p.g != 0.0f && col < cols_left ? 0xFFFFu : 0u;
-                    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(Elem<DT>::from_f32(v) & keep), rd,
-                                                          col < cols8 && row < rows_left ? (uint32_t)row * drow + (uint32_t)col * 2 : OOB, 0, 0);
-                }
-            });
-        });
-        return;
-    }
-    // Statistics: of the lane's two columns, the half wave's 64, then the block's 256.
-    Stat* const stats = reinterpret_cast<Stat*>(lds + BM * sizeof(Row));   // [WGN][BM]
-    const float bar[FN] = {col0 < cols_left ? 0.0f : -__builtin_inff(), col0 + 32 < cols_left ? 0.0f : -__builtin_inff()};
+    // Each wave turns its totals in LDS of its own, 32 rows at a time: register r of a 32 x
+    // 32 tile is row 8 (r / 4) + 4 half + r % 4, column c; read back, eight lanes hold a
+    // row's 64 columns, eight each.
+    constexpr int S = WN + 4;   // floats of a row there
+    float* const turned = reinterpret_cast<float*>(lds) + wave * 32 * S;
+    Stat* const stats = reinterpret_cast<Stat*>(lds + WAVES * 32 * S * 4);   // [WGN][BM]
+    const int part = l & 7, col0 = wn * WN + 8 * part;   // the lane's first column in the tile
+    const uint32_t drow = (uint32_t)a.dz_stride * 2;
+    const __amdgpu_buffer_rsrc_t rd = rsrc(static_cast<char*>(a.dz) + (a.dz != nullptr ? (size_t)m0 * drow + (size_t)n0 * 2 : 0),
+                                           a.dz != nullptr ? (uint32_t)(rows_left < BM ? rows_left : BM) * drow - (uint32_t)n0 * 2 : 0u);
+    const float by = a.dz != nullptr ? a.scale[0] : 0.0f;
     static_for<FM>([&](auto I) {
+        constexpr int i = decltype(I)::value;
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(63));   // the last rows have been read
+        asm volatile("" ::: "memory");
         static_for<16>([&](auto R) {
-            constexpr int i = decltype(I)::value, r = decltype(R)::value;
-            const int row = row0 + 32 * i + 8 * (r >> 2) + (r & 3);
-            const float z0 = total[i][0][r] + bar[0], z1 = total[i][1][r] + bar[1];
-            const int32_t t = rows[row].target - col0;
-            if ((t & ~32) == 0)
-                a.picked[m0 + row] = t == 0 ? z0 : z1;
-            const float top = max32(fmaxf(z0, z1));
-            const float at = top == -__builtin_inff() ? 0.0f : top;   // no column: sums of 0
-            const float sum = sum32(exp_fast(z0 - at) + exp_fast(z1 - at));
-            if (c == 0)
-                stats[wn * BM + row] = Stat{top, sum};
+            constexpr int r = decltype(R)::value;
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                turned[(8 * (r >> 2) + 4 * half2 + (r & 3)) * S + 32 * j + c] = total[i][j][r];
         });
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(63));
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            const int tr = 8 * it + (l >> 3), row = wm * WM + 32 * i + tr;
+            const float* const p = turned + tr * S + 8 * part;
+            const f32x4_t z0 = *reinterpret_cast<const f32x4_t*>(p), z1 = *reinterpret_cast<const f32x4_t*>(p + 4);
+            float z[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                z[e] = e < 4 ? z0[e & 3] : z1[e & 3];
+            const bool in = row < rows_left;
+            const int32_t t = in ? a.targets[m0 + row] : -1;
+            const bool live = t >= 0 && t < a.vocab;
+            const int64_t at = (int64_t)t - a.v0 - n0 - col0;   // of the lane's eight
+            if (a.dz != nullptr) {
+                // dz, and zeros up to the next multiple of 8 columns. (A row without a target,
+                // or of g = 0, is zeros whatever its logits are.)
+                const float lse = in ? a.lse[m0 + row] : 0.0f, g = live ? a.dloss[m0 + row] * by : 0.0f;
+                u32x4_t w;
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    uint16_t v[2];
+#pragma unroll
+                    for (int o = 0; o < 2; ++o) {
+                        const float d = g * (exp_fast(z[e + o] - lse) - (at == e + o ? 1.0f : 0.0f));
+                        v[o] = Elem<DT>::from_f32(d) & (g != 0.0f && col0 + e + o < cols_left ? 0xFFFFu : 0u);
+                    }
+                    w[e / 2] = (uint32_t)v[0] | ((uint32_t)v[1] << 16);
+                }
+                __builtin_amdgcn_raw_buffer_store_b128(w, rd, in && col0 < cols_left ? (uint32_t)row * drow + (uint32_t)col0 * 2 : OOB,
+                                                       0, 0);
+                continue;
+            }
+            if (live && at >= 0 && at < 8)
+                a.picked[m0 + row] = p[at];
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                z[e] = col0 + e < cols_left ? z[e] : -__builtin_inff();
+                top = fmaxf(top, z[e]);
+            }
+            top = max8(top);
+            const float from = top == -__builtin_inff() ? 0.0f : top;   // no column: sums of 0
+            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sum += exp_fast(z[e] - from);
+            sum = sum8(sum);
+            if (part == 0)
+                stats[wn * BM + row] = Stat{top, sum};
+        }
     });
+    if (a.dz != nullptr)
+        return;
     __syncthreads();
     for (int r = wave * 64 + l; r < BM && r < rows_left; r += 64 * WAVES) {
         Stat s = stats[r];
@@ -448,20 +480,19 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
     }
 }
 
-// x [M, K] in the order of the code pairs: position 2 p (+ 1) of a unit of 32 holds its
-// code lo_code(p) (hi_code(p)). A row of 64 n + 32 features ends in a unit of zeros and
-// then its last, as the tile kernel's last step takes them. And the groups' sums X (fp16:
-// divided by 128), as their value in DT and what that leaves. A wave takes 64 units of
-// a row.
+// x [M, K] as the tile kernel's steps take it, rows of xn: first the groups' sums X (fp16:
+// divided by 128), 64 values for 32 groups: their value in DT and what that leaves, in
+// eights as the fragments take them; then x in the order of the code pairs: position 2 p
+// (+ 1) of a unit of 32 holds its code lo_code(p) (hi_code(p)). A row of 64 n + 32 features
+// ends in a unit of zeros and then its last. A wave takes 64 units of a row.
 template <int BITS, int DT>
 __global__ __launch_bounds__(256) void loss_prep_x_kernel(const uint16_t* __restrict__ x, int64_t m, int k, int gs,
-                                                          int kp, int gp, u32x4_t* __restrict__ xp,
-                                                          uint16_t* __restrict__ xs)
+                                                          int xn, int gp, uint16_t* __restrict__ xp)
 {
     using Order = CodeOrder<BITS>;
     using E = Elem<DT>;
     typedef u32x4_t Wide __attribute__((aligned(2)));
-    const int units = kp / 32, chunks = (units + 63) / 64, lane = (int)threadIdx.x & 63;
+    const int first = 2 * gp, units = (xn - first) / 32, chunks = (units + 63) / 64, lane = (int)threadIdx.x & 63;
     const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), row = w / chunks;
     if (row >= m)
         return;
@@ -484,6 +515,7 @@ __global__ __launch_bounds__(256) void loss_prep_x_kernel(const uint16_t* __rest
             }
         }
     }
+    uint16_t* const to = xp + row * xn;
     if (u < units) {
         auto elem = [&](int i) { return (e[i / 2] >> (16 * (i % 2))) & 0xFFFFu; };
 #pragma unroll
@@ -492,22 +524,29 @@ __global__ __launch_bounds__(256) void loss_prep_x_kernel(const uint16_t* __rest
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 v[j] = elem(Order::lo_code(4 * i + j)) | (elem(Order::hi_code(4 * i + j)) << 16);
-            xp[(row * units + u) * 4 + i] = v;
+            *reinterpret_cast<u32x4_t*>(to + first + 32 * u + 8 * i) = v;
         }
     }
     const int per = gs / 32;
     for (int off = 1; off < per; off <<= 1)
         sum += __shfl_xor(sum, off, 64);
-    const int g = src >= 0 && src % per == 0 ? src / per : -1;
-    uint16_t* const hi = xs + row * 2 * gp;
-    if (g >= 0) {
+    // Group g of a step of 32: its 16 (g / 16 % 2) are instructions 2 i and 2 i + 1, their
+    // halves of the wave eight each (a_frag's chunks, which differ with groups of 32).
+    auto put = [&](int g, uint16_t hi, uint16_t lo) {
+        const int i = g / 16 % 2, h = g / 8 % 2;
+        uint16_t* const t = to + g / 32 * 64 + g % 8;
+        const int c0 = gs == 32 ? 4 * i + 2 * h : 2 * i + 4 * h;   // the chunk of instruction 2 i
+        t[8 * c0] = hi;
+        t[8 * (c0 + 1)] = lo;
+    };
+    if (src >= 0 && src % per == 0) {
         if constexpr (DT == DT_F16)
             sum *= 1.0f / 128;
-        hi[g] = E::from_f32(sum);
-        hi[gp + g] = E::from_f32(sum - E::to_f32(hi[g]));
+        const uint16_t hi = E::from_f32(sum);
+        put(src / per, hi, E::from_f32(sum - E::to_f32(hi)));
     }
-    if (chunk == 0 && k / gs + lane < gp)   // fewer than 16 to fill up
-        hi[k / gs + lane] = hi[gp + k / gs + lane] = 0;
+    if (chunk == 0 && k / gs + lane < gp)   // fewer than 32 to fill up
+        put(k / gs + lane, 0, 0);
 }
 
 } // namespace losstile

@@ -78,13 +78,12 @@ hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t stream);
 constexpr int LOSS_BN = 256;   // columns of a tile, and of a part of the statistics
 struct Stat;
 struct LossTileArgs {
-    const void* xp;          // [M, kp]: x in the order of the code pairs (loss_prep_x)
-    const void* xs;          // [M, 2, gp]: the groups' sums, high and low part
+    const void* xp;          // [M, xn]: the groups' sums of x, then x (loss_prep_x)
     const uint32_t* wq;      // [N, K*bits/32]
     const void* st;          // [K/gs, np]: the scales, transposed (loss_prep_w)
     const void* bp;          // [N, gp]: the biases
     int M, N, K, gs;
-    int kp, gp, np;          // K, the groups and N filled up to 64, 16 and LOSS_BN
+    int xn, gp, np;          // the groups and N filled up to 32 and LOSS_BN; 2 gp + K filled up to 64
     int tiles_m, tiles, per_xcd;
     const int32_t* targets;  // [M]
     int64_t vocab, v0;       // the whole vocabulary; the piece's first token
