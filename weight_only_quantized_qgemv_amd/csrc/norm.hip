@@ -25,32 +25,45 @@ namespace {
 typedef u32x4_t Wide16 __attribute__((aligned(2)));
 typedef u32x4_t Wide32 __attribute__((aligned(4)));
 
-// Elements 8 c .. 8 c + 7 of a row of n; those past its end are zeros.
-template <int DT>
-__device__ __forceinline__ void load8(const void* p, int64_t at, int c, int n, float (&v)[8])
-{
-    using E = Elem<DT>;
-    const typename E::storage* const q = static_cast<const typename E::storage*>(p) + at + 8 * c;
-    const int left = n - 8 * c;
-    if (left >= 8) {
-        if constexpr (DT == DT_F32) {
-            const u32x4_t a = *reinterpret_cast<const Wide32*>(q), b = *reinterpret_cast<const Wide32*>(q + 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = __uint_as_float(a[i]);
-                v[4 + i] = __uint_as_float(b[i]);
-            }
-        } else {
-            const u32x4_t a = *reinterpret_cast<const Wide16*>(q);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = E::to_f32((uint16_t)(a[i / 2] >> (16 * (i % 2))));
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = i < left ? E::to_f32(q[i]) : 0.0f;
+// Eight elements as they are loaded: one 16-byte piece, or two (fp32).
+template <int DT> struct Pack {
+    static constexpr int N = DT == DT_F32 ? 2 : 1;
+    u32x4_t w[N];
+    __device__ __forceinline__ float operator[](int i) const
+    {
+        if constexpr (DT == DT_F32)
+            return __uint_as_float(w[i / 4][i % 4]);
+        else
+            return Elem<DT>::to_f32((uint16_t)(w[0][i / 2] >> (16 * (i % 2))));
     }
+};
+template <int DT> using WideOf = std::conditional_t<DT == DT_F32, Wide32, Wide16>;
+
+// Elements 8 c .. 8 c + 7 of a row of n at p; those past its end are zeros.
+template <int DT>
+__device__ __forceinline__ Pack<DT> load8(const void* p, int64_t at, int c, int n)
+{
+    const typename Elem<DT>::storage* const q = static_cast<const typename Elem<DT>::storage*>(p) + at + 8 * c;
+    const int left = n - 8 * c;
+    Pack<DT> v;
+    if (left >= 8) {
+#pragma unroll
+        for (int i = 0; i < Pack<DT>::N; ++i)
+            v.w[i] = *reinterpret_cast<const WideOf<DT>*>(q + 4 * i);
+        return v;
+    }
+#pragma unroll
+    for (int i = 0; i < Pack<DT>::N; ++i)
+        v.w[i] = u32x4_t{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (i < left) {
+            if constexpr (DT == DT_F32)
+                v.w[i / 4][i % 4] = __float_as_uint(q[i]);
+            else
+                v.w[0][i / 2] |= (uint32_t)q[i] << (16 * (i % 2));
+        }
+    return v;
 }
 
 template <int DT>
@@ -60,27 +73,41 @@ __device__ __forceinline__ void store8(void* p, int64_t at, int c, int n, const 
     typename E::storage* const q = static_cast<typename E::storage*>(p) + at + 8 * c;
     const int left = n - 8 * c;
     if (left >= 8) {
-        if constexpr (DT == DT_F32) {
-            u32x4_t a, b;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a[i] = __float_as_uint(v[i]);
-                b[i] = __float_as_uint(v[4 + i]);
-            }
-            *reinterpret_cast<Wide32*>(q) = a;
-            *reinterpret_cast<Wide32*>(q + 4) = b;
-        } else {
+        for (int i = 0; i < Pack<DT>::N; ++i) {
             u32x4_t a;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                a[i] = (uint32_t)E::from_f32(v[2 * i]) | ((uint32_t)E::from_f32(v[2 * i + 1]) << 16);
-            *reinterpret_cast<Wide16*>(q) = a;
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (DT == DT_F32)
+                    a[j] = __float_as_uint(v[4 * i + j]);
+                else
+                    a[j] = (uint32_t)E::from_f32(v[2 * j]) | ((uint32_t)E::from_f32(v[2 * j + 1]) << 16);
+            }
+            *reinterpret_cast<WideOf<DT>*>(q + 4 * i) = a;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 7; ++i)
             if (i < left)
                 q[i] = E::from_f32(v[i]);
+    }
+}
+
+// N sums over a wave, in all its lanes: moves between lanes, no trips to LDS.
+template <int N> __device__ __forceinline__ void wave_sums(float (&v)[N])
+{
+    reduce_slots<N, 16>(v);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint32_t t = __float_as_uint(v[i]);
+        const auto x = __builtin_amdgcn_permlane16_swap(t, t, false, false);
+        v[i] = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint32_t t = __float_as_uint(v[i]);
+        const auto x = __builtin_amdgcn_permlane32_swap(t, t, false, false);
+        v[i] = __uint_as_float(x[0]) + __uint_as_float(x[1]);
     }
 }
 
@@ -89,9 +116,7 @@ __device__ __forceinline__ void store8(void* p, int64_t at, int c, int n, const 
 template <int N, int THREADS>
 __device__ __forceinline__ void row_sums(float (&v)[N], float (&room)[2][3][16], int& turn)
 {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        v[i] = segment_sum<64>(v[i]);
+    wave_sums<N>(v);
     if constexpr (THREADS > 64) {
         const int wave = (int)threadIdx.x >> 6;
         if ((threadIdx.x & 63) == 0) {
@@ -126,69 +151,72 @@ __global__ __launch_bounds__(ROWT * kRowsPerBlock<ROWT>) void norm_kernel(NormAr
     if (RPB > 1 && row >= a.M)
         return;
     const int64_t at = row * a.D;
-    float v[C][8], t[C][8];
+    const bool block = a.y != nullptr, gated = a.gate != nullptr, last = a.weight == nullptr;
+    // Everything whose address is known is asked for first.
+    Pack<SDT> x[C];
+    Pack<DT> y[C], post[C], gate[C], weight[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-        load8<SDT>(a.x, at, lane + c * ROWT, n, v[c]);
-    if (a.y != nullptr) {
+    for (int c = 0; c < C; ++c) {
+        x[c] = load8<SDT>(a.x, at, lane + c * ROWT, n);
+        if (block)
+            y[c] = load8<DT>(a.y, at, lane + c * ROWT, n);
+    }
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-            load8<DT>(a.y, at, lane + c * ROWT, n, t[c]);
+    for (int c = 0; c < C; ++c) {
+        if (a.post != nullptr)
+            post[c] = load8<DT>(a.post, 0, lane + c * ROWT, n);
+        if (gated)
+            gate[c] = load8<DT>(a.gate, row / (a.M / a.gates) * a.D, lane + c * ROWT, n);
+        if (!last)
+            weight[c] = load8<DT>(a.weight, 0, lane + c * ROWT, n);
+    }
+    float v[C][8];
+    float q[1] = {0.0f};
+    if (block) {
+        float r = 1.0f;
         if (a.post != nullptr) {
-            float q[1] = {0.0f};
 #pragma unroll
             for (int c = 0; c < C; ++c)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    q[0] = __builtin_fmaf(t[c][i], t[c][i], q[0]);
+                    q[0] = __builtin_fmaf(y[c][i], y[c][i], q[0]);
             row_sums<1, ROWT>(q, room, turn);
-            const float r = 1.0f / sqrtf(q[0] / (float)n + a.eps);
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                float w[8];
-                load8<DT>(a.post, 0, lane + c * ROWT, n, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    t[c][i] = t[c][i] * r * (w[i] + a.offset);
-            }
+            r = 1.0f / sqrtf(q[0] / (float)n + a.eps);
         }
-        if (a.gate != nullptr) {
-            const int64_t g = row / (a.M / a.gates) * a.D;
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                float w[8];
-                load8<DT>(a.gate, g, lane + c * ROWT, n, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    t[c][i] *= w[i];
-            }
-        }
+        q[0] = 0.0f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[c][i] = __builtin_fmaf(a.factor, t[c][i], v[c][i]);
+            for (int i = 0; i < 8; ++i) {
+                float t = y[c][i];
+                if (a.post != nullptr)
+                    t = t * r * (post[c][i] + a.offset);
+                if (gated)
+                    t *= gate[c][i];
+                v[c][i] = __builtin_fmaf(a.factor, t, x[c][i]);
+                q[0] = __builtin_fmaf(v[c][i], v[c][i], q[0]);
+            }
             store8<SDT>(a.s, at, lane + c * ROWT, n, v[c]);
         }
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[c][i] = x[c][i];
+                q[0] = __builtin_fmaf(v[c][i], v[c][i], q[0]);
+            }
     }
-    if (a.weight == nullptr)
+    if (last)
         return;
-    float q[1] = {0.0f};
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            q[0] = __builtin_fmaf(v[c][i], v[c][i], q[0]);
     row_sums<1, ROWT>(q, room, turn);
     const float r = 1.0f / sqrtf(q[0] / (float)n + a.eps);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        float w[8];
-        load8<DT>(a.weight, 0, lane + c * ROWT, n, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            w[i] = v[c][i] * r * (w[i] + a.offset);
-        store8<DT>(a.a, at, lane + c * ROWT, n, w);
+            v[c][i] = v[c][i] * r * (weight[c][i] + a.offset);
+        store8<DT>(a.a, at, lane + c * ROWT, n, v[c]);
     }
 }
 
@@ -200,191 +228,334 @@ __global__ __launch_bounds__(ROWT * kRowsPerBlock<ROWT>) void norm_kernel(NormAr
 struct NormSplit {
     int64_t groups, parts;
 };
-NormSplit norm_split(int64_t m, int64_t gates)
+// Threads of a row in the backward pass, and so many blocks as the GPU holds at once
+// (two waves a SIMD): 8192 rows of 4096, bf16, 98 us, with twice as many 103; 4096
+// rows of 2048 34.1 us on 512 blocks of 256 threads, 38.8 on 256.
+int norm_threads(int64_t d) { return d <= 512 ? 64 : d <= 1024 ? 128 : d <= 2048 ? 256 : 512; }
+NormSplit norm_split(int64_t m, int64_t d, int64_t gates)
 {
-    constexpr int64_t kBlocks = 512;
-    const int64_t g = std::max<int64_t>(gates, 1), groups = std::min(g, kBlocks);
-    return {groups, std::clamp<int64_t>(kBlocks / groups, 1, std::max<int64_t>(m / g, 1))};
+    const int64_t blocks = 256 * (512 / norm_threads(d));
+    const int64_t g = std::max<int64_t>(gates, 1), groups = std::min(g, blocks);
+    return {groups, std::clamp<int64_t>(blocks / groups, 1, std::max<int64_t>(m / g, 1))};
 }
 
-// The column sums of a block: in registers, or (rows of more than 8192) in the
-// block's own part of the workspace, where each thread reads and writes the
-// columns that are its own.
-template <int DT, int SDT, int ROWT, int C, bool ACC_MEM>
-__global__ __launch_bounds__(ROWT) void norm_grad_kernel(NormGradArgs a, int64_t groups, int64_t parts)
+// Rows of up to 8192: the row, the weights and the block's column sums stay in
+// registers. A row of one chunk a thread is loaded while the row before it is summed
+// and closed.
+template <int DT, int SDT, int ROWT, int C>
+__global__ __launch_bounds__(ROWT, 2) void norm_grad_kernel(NormGradArgs a, int64_t groups, int64_t parts)
 {
     __shared__ float room[2][3][16];
     int turn = 0;
     const int n = (int)a.D, lane = (int)threadIdx.x;
     const int64_t blocks = groups * parts, block = blockIdx.x, p = block % parts;
     const int64_t gates = a.gate != nullptr ? a.gates : 1, per = a.M / gates;
+    const bool pre = a.weight != nullptr, post = a.post != nullptr, gated = a.gate != nullptr, whole = a.y != nullptr;
     float* const partial = static_cast<float*>(a.workspace);   // [3][blocks][D]: dweight, dpost, dgate
-    float acc[ACC_MEM ? 1 : 3][C][8];
+    float acc[3][C][8];
     auto clear = [&](int which) {
 #pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                acc[which][c][i] = 0.0f;
+    };
+    struct Row {
+        Pack<SDT> ds[C], s[C];
+        Pack<DT> da[C], y[C];
+    };
+    auto fetch = [&](int64_t row, Row& r) {
+        const int64_t at = row * a.D;
+#pragma unroll
         for (int c = 0; c < C; ++c) {
-            const float zero[8] = {};
-            if constexpr (ACC_MEM)
-                store8<DT_F32>(partial, (which * blocks + block) * a.D, lane + c * ROWT, n, zero);
-            else
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    acc[which][c][i] = 0.0f;
+            if (a.ds != nullptr)
+                r.ds[c] = load8<SDT>(a.ds, at, lane + c * ROWT, n);
+            if (pre) {
+                r.s[c] = load8<SDT>(a.s, at, lane + c * ROWT, n);
+                r.da[c] = load8<DT>(a.da, at, lane + c * ROWT, n);
+            }
+            if (whole)
+                r.y[c] = load8<DT>(a.y, at, lane + c * ROWT, n);
         }
     };
-    auto add = [&](int which, int c, const float (&v)[8]) {
-        if constexpr (ACC_MEM) {
-            float t[8];
-            load8<DT_F32>(partial, (which * blocks + block) * a.D, lane + c * ROWT, n, t);
+    Row cur;
+    fetch(block / parts * per + p, cur);
+    Pack<DT> weight[C], postw[C], gate[C];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                t[i] += v[i];
-            store8<DT_F32>(partial, (which * blocks + block) * a.D, lane + c * ROWT, n, t);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                acc[which][c][i] += v[i];
-        }
-    };
-    if (!ACC_MEM || a.weight != nullptr)
-        clear(0);
-    if (!ACC_MEM || a.post != nullptr)
-        clear(1);
+    for (int c = 0; c < C; ++c) {
+        if (pre)
+            weight[c] = load8<DT>(a.weight, 0, lane + c * ROWT, n);
+        if (post)
+            postw[c] = load8<DT>(a.post, 0, lane + c * ROWT, n);
+    }
+    clear(0);
+    clear(1);
     for (int64_t g = block / parts; g < gates; g += groups) {
-        if (!ACC_MEM || a.gate != nullptr)
+        if (gated) {
             clear(2);
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                gate[c] = load8<DT>(a.gate, g * a.D, lane + c * ROWT, n);
+        }
         for (int64_t row = g * per + p; row < (g + 1) * per; row += parts) {
             const int64_t at = row * a.D;
-            float G[C][8], v[C][8], u[C][8], y[C][8];
+            const int64_t after = row + parts < (g + 1) * per ? row + parts : g + groups < gates ? (g + groups) * per + p : -1;
+            constexpr bool AHEAD = C == 1;
+            Row next;
+            if constexpr (AHEAD) {
+                if (after >= 0)
+                    fetch(after, next);
+            }
             float q[3] = {0.0f, 0.0f, 0.0f};   // s s, u s, y y
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                if (a.ds != nullptr) {
-                    load8<SDT>(a.ds, at, lane + c * ROWT, n, G[c]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        G[c][i] = 0.0f;
-                }
-                if (a.weight != nullptr) {
-                    load8<SDT>(a.s, at, lane + c * ROWT, n, v[c]);
-                    load8<DT>(a.da, at, lane + c * ROWT, n, u[c]);
-                    float w[8];
-                    load8<DT>(a.weight, 0, lane + c * ROWT, n, w);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        q[0] = __builtin_fmaf(v[c][i], v[c][i], q[0]);
-                        q[1] = __builtin_fmaf(u[c][i] * (w[i] + a.offset), v[c][i], q[1]);
-                    }
-                }
-                if (a.y != nullptr) {
-                    load8<DT>(a.y, at, lane + c * ROWT, n, y[c]);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        q[2] = __builtin_fmaf(y[c][i], y[c][i], q[2]);
-                }
-            }
-            row_sums<3, ROWT>(q, room, turn);
-            if (a.weight != nullptr) {
-                const float r = 1.0f / sqrtf(q[0] / (float)n + a.eps);
-                const float k = r * r * r * (q[1] / (float)n);
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    float w[8], d[8];
-                    load8<DT>(a.weight, 0, lane + c * ROWT, n, w);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        d[i] = u[c][i] * v[c][i] * r;
-                        G[c][i] += r * (u[c][i] * (w[i] + a.offset)) - v[c][i] * k;
-                    }
-                    add(0, c, d);
-                }
-            }
-#pragma unroll
             for (int c = 0; c < C; ++c)
-                store8<SDT>(a.dx, at, lane + c * ROWT, n, G[c]);
-            if (a.y == nullptr)
-                continue;
-            const float ry = 1.0f / sqrtf(q[2] / (float)n + a.eps);
-            // t without the gate, then q and v over G and u.
-            float z[1] = {0.0f};
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                float w[8], t[8], d[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    t[i] = y[c][i];
-                    G[c][i] *= a.factor;
-                }
-                if (a.post != nullptr) {
-                    load8<DT>(a.post, 0, lane + c * ROWT, n, w);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        t[i] *= ry * (w[i] + a.offset);
-                }
-                if (a.gate != nullptr) {
-                    float gt[8];
-                    load8<DT>(a.gate, g * a.D, lane + c * ROWT, n, gt);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        d[i] = t[i] * G[c][i];
-                        G[c][i] *= gt[i];
+                    if (pre) {
+                        const float s = cur.s[c][i];
+                        q[0] = __builtin_fmaf(s, s, q[0]);
+                        q[1] = __builtin_fmaf(cur.da[c][i] * (weight[c][i] + a.offset), s, q[1]);
                     }
-                    add(2, c, d);
+                    if (post)
+                        q[2] = __builtin_fmaf(cur.y[c][i], cur.y[c][i], q[2]);
                 }
-                if (a.post != nullptr) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        d[i] = G[c][i] * y[c][i] * ry;
-                        G[c][i] *= w[i] + a.offset;
-                        z[0] = __builtin_fmaf(G[c][i], y[c][i], z[0]);
-                    }
-                    add(1, c, d);
-                }
-            }
-            if (a.post != nullptr) {
-                row_sums<1, ROWT>(z, room, turn);
-                const float k = ry * ry * ry * (z[0] / (float)n);
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        G[c][i] = ry * G[c][i] - y[c][i] * k;
-            }
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-                store8<DT>(a.dy, at, lane + c * ROWT, n, G[c]);
-        }
-        if (a.gate != nullptr && (!ACC_MEM || parts == 1)) {
+            row_sums<3, ROWT>(q, room, turn);
+            const float rs = pre ? 1.0f / sqrtf(q[0] / (float)n + a.eps) : 0.0f, ks = rs * rs * rs * (q[1] / (float)n);
+            const float ry = post ? 1.0f / sqrtf(q[2] / (float)n + a.eps) : 1.0f;
+            float G[C][8], z[1] = {0.0f};
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                float t[8];
-                if constexpr (ACC_MEM)
-                    load8<DT_F32>(partial, (2 * blocks + block) * a.D, lane + c * ROWT, n, t);
-                else
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        t[i] = acc[2][c][i];
+                for (int i = 0; i < 8; ++i)
+                    G[c][i] = a.ds != nullptr ? cur.ds[c][i] : 0.0f;
+                if (pre) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float s = cur.s[c][i], u = cur.da[c][i];
+                        acc[0][c][i] = __builtin_fmaf(u * s, rs, acc[0][c][i]);
+                        G[c][i] += rs * (u * (weight[c][i] + a.offset)) - s * ks;
+                    }
+                }
+                store8<SDT>(a.dx, at, lane + c * ROWT, n, G[c]);
+                if (!whole)
+                    continue;
+                // G is now q, and then v: t is y r(y) (post + offset).
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    G[c][i] *= a.factor;
+                if (gated) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float t = post ? cur.y[c][i] * (ry * (postw[c][i] + a.offset)) : cur.y[c][i];
+                        acc[2][c][i] = __builtin_fmaf(t, G[c][i], acc[2][c][i]);
+                        G[c][i] *= gate[c][i];
+                    }
+                }
+                if (post) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        acc[1][c][i] = __builtin_fmaf(G[c][i] * cur.y[c][i], ry, acc[1][c][i]);
+                        G[c][i] *= postw[c][i] + a.offset;
+                        z[0] = __builtin_fmaf(G[c][i], cur.y[c][i], z[0]);
+                    }
+                }
+            }
+            if (whole) {
+                float kz = 0.0f;
+                if (post) {
+                    row_sums<1, ROWT>(z, room, turn);
+                    kz = ry * ry * ry * (z[0] / (float)n);
+                }
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    if (post) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            G[c][i] = ry * G[c][i] - cur.y[c][i] * kz;
+                    }
+                    store8<DT>(a.dy, at, lane + c * ROWT, n, G[c]);
+                }
+            }
+            if constexpr (AHEAD)
+                cur = next;
+            else if (after >= 0)
+                fetch(after, cur);
+        }
+        if (gated) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
                 if (parts == 1)
-                    store8<DT>(a.dgate, g * a.D, lane + c * ROWT, n, t);
+                    store8<DT>(a.dgate, g * a.D, lane + c * ROWT, n, acc[2][c]);
                 else
-                    store8<DT_F32>(partial, (2 * blocks + block) * a.D, lane + c * ROWT, n, t);
+                    store8<DT_F32>(partial, (2 * blocks + block) * a.D, lane + c * ROWT, n, acc[2][c]);
             }
         }
     }
-    if constexpr (!ACC_MEM) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            if (a.weight != nullptr)
-                store8<DT_F32>(partial, block * a.D, lane + c * ROWT, n, acc[0][c]);
-            if (a.post != nullptr)
-                store8<DT_F32>(partial, (blocks + block) * a.D, lane + c * ROWT, n, acc[1][c]);
+    for (int c = 0; c < C; ++c) {
+        if (pre)
+            store8<DT_F32>(partial, block * a.D, lane + c * ROWT, n, acc[0][c]);
+        if (post)
+            store8<DT_F32>(partial, (blocks + block) * a.D, lane + c * ROWT, n, acc[1][c]);
+    }
+}
+
+// Wider rows: read again for each of the three passes over a row (from L2), a chunk at
+// a time, the column sums in the block's own part of the workspace, where each thread
+// reads and writes the columns that are its own. 2048 rows of 16384, bf16: WIDE_US us.
+template <int DT, int SDT>
+__global__ __launch_bounds__(512) void norm_grad_wide_kernel(NormGradArgs a, int64_t groups, int64_t parts)
+{
+    constexpr int T = 512;
+    __shared__ float room[2][3][16];
+    int turn = 0;
+    const int n = (int)a.D, lane = (int)threadIdx.x, chunks = (n + 7) / 8;
+    const int64_t blocks = groups * parts, block = blockIdx.x, p = block % parts;
+    const int64_t gates = a.gate != nullptr ? a.gates : 1, per = a.M / gates;
+    const bool pre = a.weight != nullptr, post = a.post != nullptr, gated = a.gate != nullptr, whole = a.y != nullptr;
+    float* const partial = static_cast<float*>(a.workspace);   // [3][blocks][D]: dweight, dpost, dgate
+    bool first[3] = {true, true, true};   // of the sums: nothing to add to yet
+    auto add = [&](int which, int c, const float (&v)[8]) {
+        const int64_t at = (which * blocks + block) * a.D;
+        float t[8];
+        if (first[which]) {
+            store8<DT_F32>(partial, at, c, n, v);
+        } else {
+            const Pack<DT_F32> old = load8<DT_F32>(partial, at, c, n);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                t[i] = old[i] + v[i];
+            store8<DT_F32>(partial, at, c, n, t);
+        }
+    };
+    for (int64_t g = block / parts; g < gates; g += groups) {
+        first[2] = true;
+        for (int64_t row = g * per + p; row < (g + 1) * per; row += parts) {
+            const int64_t at = row * a.D;
+            float q[3] = {0.0f, 0.0f, 0.0f};   // s s, u s, y y
+            for (int c = lane; c < chunks; c += T) {
+                if (pre) {
+                    const Pack<SDT> s = load8<SDT>(a.s, at, c, n);
+                    const Pack<DT> da = load8<DT>(a.da, at, c, n), w = load8<DT>(a.weight, 0, c, n);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        q[0] = __builtin_fmaf(s[i], s[i], q[0]);
+                        q[1] = __builtin_fmaf(da[i] * (w[i] + a.offset), s[i], q[1]);
+                    }
+                }
+                if (post) {
+                    const Pack<DT> y = load8<DT>(a.y, at, c, n);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        q[2] = __builtin_fmaf(y[i], y[i], q[2]);
+                }
+            }
+            row_sums<3, T>(q, room, turn);
+            const float rs = pre ? 1.0f / sqrtf(q[0] / (float)n + a.eps) : 0.0f, ks = rs * rs * rs * (q[1] / (float)n);
+            const float ry = post ? 1.0f / sqrtf(q[2] / (float)n + a.eps) : 1.0f;
+            // v (or q) of a chunk; with `sums`, what is summed and stored on the way to it.
+            float z[1] = {0.0f};
+            auto through = [&](int c, bool sums, const Pack<DT>& y, float (&G)[8]) {
+                if (a.ds != nullptr) {
+                    const Pack<SDT> ds = load8<SDT>(a.ds, at, c, n);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        G[i] = ds[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        G[i] = 0.0f;
+                }
+                float d[8];
+                if (pre) {
+                    const Pack<SDT> s = load8<SDT>(a.s, at, c, n);
+                    const Pack<DT> da = load8<DT>(a.da, at, c, n), w = load8<DT>(a.weight, 0, c, n);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        d[i] = da[i] * s[i] * rs;
+                        G[i] += rs * (da[i] * (w[i] + a.offset)) - s[i] * ks;
+                    }
+                    if (sums)
+                        add(0, c, d);
+                }
+                if (!whole) {
+                    store8<SDT>(a.dx, at, c, n, G);
+                    return;
+                }
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = G[i];
+                    G[i] *= a.factor;
+                }
+                const Pack<DT> w = post ? load8<DT>(a.post, 0, c, n) : Pack<DT>{};
+                if (gated) {
+                    const Pack<DT> gate = load8<DT>(a.gate, g * a.D, c, n);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float t = post ? y[i] * (ry * (w[i] + a.offset)) : y[i];
+                        d[i] = t * G[i];
+                        G[i] *= gate[i];
+                    }
+                    if (sums)
+                        add(2, c, d);
+                }
+                if (post) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        d[i] = G[i] * y[i] * ry;
+                        G[i] *= w[i] + a.offset;
+                    }
+                    if (sums)
+                        add(1, c, d);
+                }
+                // dx may be ds, and dy da or y: they are written when nothing of the chunk is
+                // read any more.
+                if (!sums || !post)
+                    store8<SDT>(a.dx, at, c, n, x);
+            };
+            if (post) {
+                for (int c = lane; c < chunks; c += T) {
+                    const Pack<DT> y = load8<DT>(a.y, at, c, n);
+                    float G[8];
+                    through(c, true, y, G);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        z[0] = __builtin_fmaf(G[i], y[i], z[0]);
+                }
+                row_sums<1, T>(z, room, turn);
+            }
+            const float kz = ry * ry * ry * (z[0] / (float)n);
+            for (int c = lane; c < chunks; c += T) {
+                const Pack<DT> y = whole ? load8<DT>(a.y, at, c, n) : Pack<DT>{};
+                float G[8];
+                through(c, !post, y, G);
+                if (!whole)
+                    continue;
+                if (post) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        G[i] = ry * G[i] - y[i] * kz;
+                }
+                store8<DT>(a.dy, at, c, n, G);
+            }
+            first[0] = first[1] = first[2] = false;
+        }
+        if (gated && parts == 1) {
+            for (int c = lane; c < chunks; c += T) {
+                const Pack<DT_F32> sum = load8<DT_F32>(partial, (2 * blocks + block) * a.D, c, n);
+                float t[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    t[i] = sum[i];
+                store8<DT>(a.dgate, g * a.D, c, n, t);
+            }
         }
     }
 }
 
 // out[j][d] = the sum of `count` rows of `partial` from row j count on, in a fixed
-// order: 64 columns a block, its 16 waves a share of the rows each.
+// order: 16 columns a block, its 64 groups of 16 threads a share of the rows each.
 struct NormJoin {
     const float* partial;
     void* out;
@@ -397,32 +568,33 @@ struct NormJoins {
 template <int DT>
 __global__ __launch_bounds__(1024) void norm_join_kernel(NormJoins a)
 {
-    __shared__ float room[16][64];
+    constexpr int COLS = 16, R = 1024 / COLS;
+    __shared__ float room[R][COLS];
     const NormJoin& j = a.j[blockIdx.z];
-    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    const int64_t col = (int64_t)blockIdx.x * 64 + lane, sum = blockIdx.y;
+    const int lane = (int)threadIdx.x % COLS, share = (int)threadIdx.x / COLS;
+    const int64_t col = (int64_t)blockIdx.x * COLS + lane, sum = blockIdx.y;
     if (sum >= j.rows)   // uniform
         return;
     const float* const p = j.partial + sum * j.count * a.D + (col < a.D ? col : 0);
     float v = 0.0f;
-    for (int64_t r = wave; r < j.count; r += 16 * 8) {
+    for (int64_t r = share; r < j.count; r += R * 8) {
         float t[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            t[i] = r + 16 * i < j.count ? p[(r + 16 * i) * a.D] : 0.0f;
+            t[i] = r + R * i < j.count ? p[(r + R * i) * a.D] : 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             v += t[i];
     }
-    room[wave][lane] = v;
-    __syncthreads();
-    if (wave == 0 && col < a.D) {
-        float t = 0.0f;
+    room[share][lane] = v;
 #pragma unroll
-        for (int w = 0; w < 16; ++w)
-            t += room[w][lane];
-        static_cast<typename Elem<DT>::storage*>(j.out)[sum * a.D + col] = Elem<DT>::from_f32(t);
+    for (int half = R / 2; half > 0; half /= 2) {
+        __syncthreads();
+        if (share < half)
+            room[share][lane] += room[share + half][lane];
     }
+    if (share == 0 && col < a.D)
+        static_cast<typename Elem<DT>::storage*>(j.out)[sum * a.D + col] = Elem<DT>::from_f32(room[0][lane]);
 }
 
 template <int DT, int SDT, int ROWT, int C>
@@ -447,13 +619,17 @@ hipError_t fwd(const NormArgs& a, hipStream_t st)
     return run_fwd<DT, SDT, 512, 4>(a, st);
 }
 
-template <int DT, int SDT, int ROWT, int C, bool ACC_MEM>
+template <int DT, int SDT, int ROWT, int C>
 hipError_t run_bwd(const NormGradArgs& a, hipStream_t st)
 {
-    const NormSplit p = norm_split(a.M, a.gate != nullptr ? a.gates : 1);
+    const NormSplit p = norm_split(a.M, a.D, a.gate != nullptr ? a.gates : 1);
     const int64_t blocks = p.groups * p.parts;
-    hipLaunchKernelGGL((norm_grad_kernel<DT, SDT, ROWT, C, ACC_MEM>), dim3((unsigned)blocks), dim3(ROWT), 0, st, a,
-                       p.groups, p.parts);
+    if constexpr (C > 0)
+        hipLaunchKernelGGL((norm_grad_kernel<DT, SDT, ROWT, C>), dim3((unsigned)blocks), dim3(ROWT), 0, st, a, p.groups,
+                           p.parts);
+    else
+        hipLaunchKernelGGL((norm_grad_wide_kernel<DT, SDT>), dim3((unsigned)blocks), dim3(ROWT), 0, st, a, p.groups,
+                           p.parts);
     if (hipError_t e = hipGetLastError(); e != hipSuccess)
         return e;
     NormJoins j{};
@@ -471,7 +647,7 @@ hipError_t run_bwd(const NormGradArgs& a, hipStream_t st)
     }
     if (n == 0)
         return hipSuccess;
-    hipLaunchKernelGGL((norm_join_kernel<DT>), dim3((unsigned)((a.D + 63) / 64), (unsigned)most, (unsigned)n),
+    hipLaunchKernelGGL((norm_join_kernel<DT>), dim3((unsigned)((a.D + 15) / 16), (unsigned)most, (unsigned)n),
                        dim3(1024), 0, st, j);
     return hipGetLastError();
 }
@@ -479,11 +655,12 @@ hipError_t run_bwd(const NormGradArgs& a, hipStream_t st)
 template <int DT, int SDT>
 hipError_t bwd(const NormGradArgs& a, hipStream_t st)
 {
-    if (a.D <= 512) return run_bwd<DT, SDT, 64, 1, false>(a, st);
-    if (a.D <= 2048) return run_bwd<DT, SDT, 256, 1, false>(a, st);
-    if (a.D <= 4096) return run_bwd<DT, SDT, 512, 1, false>(a, st);
-    if (a.D <= 8192) return run_bwd<DT, SDT, 512, 2, false>(a, st);
-    return run_bwd<DT, SDT, 512, 4, true>(a, st);
+    if (a.D <= 512) return run_bwd<DT, SDT, 64, 1>(a, st);
+    if (a.D <= 1024) return run_bwd<DT, SDT, 128, 1>(a, st);
+    if (a.D <= 2048) return run_bwd<DT, SDT, 256, 1>(a, st);
+    if (a.D <= 4096) return run_bwd<DT, SDT, 512, 1>(a, st);
+    if (a.D <= 8192) return run_bwd<DT, SDT, 512, 2>(a, st);
+    return run_bwd<DT, SDT, 512, 0>(a, st);
 }
 
 // f(types) for the block's type and the stream's.
@@ -515,7 +692,7 @@ size_t norm_grad_workspace_bytes(int64_t m, int64_t d, int64_t gates)
 {
     if (m == 0 || d == 0)
         return 0;
-    const NormSplit p = norm_split(m, gates);
+    const NormSplit p = norm_split(m, d, gates);
     return 3 * (size_t)(p.groups * p.parts) * (size_t)d * 4;
 }
 
