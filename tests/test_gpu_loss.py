@@ -8,7 +8,8 @@ product folds the scales out of the codes' sums) and G the groups of a row:
 * lse: the largest of its logits' bounds, and the roundings of exp, of sums that are
   never longer than some hundreds in a row, and of log: 2^-16 + 2^-22 |lse|; the loss: that
   and its target's logit;
-* dz = g (p - [target]): |g| p (bound of z + 2^-20 (1 + |z - lse|)) + half an ulp of the
+* dz = g (p - [target]): |g| p (bound of z + 2^-20 (1 + |z - lse|)), |g| 2^-126 (the exponential
+  instruction gives 0 where its result would be below fp32's normal range) + half an ulp of the
   products' operand (of 16 bits: times a factor that makes the largest |g| 2^14, and three
   roundings of 2^-24 for the factor);
 * dx: that of dz times |W|, TAU |dz| |W| and half an ulp; dscales and dbiases: that of dz
@@ -69,7 +70,7 @@ def backward64(x, w, t, lse, dloss, bits, gs, dt):
     dz.scatter_add_(1, at, torch.full_like(p[:, :1], -1.0))
     dz = dz * g
     floor = HALF_SUBNORMAL[dt] * (float(g.abs().max()) * 2.0 ** -14 if dt == F16 else 1.0)
-    b_dz = g.abs() * p * (1.01 * bz + 2.0 ** -20 * (1 + off.abs())) + dz.abs() * 2.0 ** -22
+    b_dz = g.abs() * p * (1.01 * bz + 2.0 ** -20 * (1 + off.abs())) + dz.abs() * 2.0 ** -22 + g.abs() * 2.0 ** -126
     b_dz = b_dz + torch.clamp(1.01 * dz.abs() * HALF_ULP[dt], min=floor)
     b_dz = torch.where(live[:, None], b_dz, 0.0)
     xd = x.double()

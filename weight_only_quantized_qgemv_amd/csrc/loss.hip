@@ -225,12 +225,12 @@ __global__ __launch_bounds__(1024) void loss_scale_kernel(const float* __restric
 
 // The scales [n, groups] transposed to [groups, np], zeros behind n, and the biases in
 // rows of gp (null: they lie so already). Tiles of 64 x 64.
-__global__ __launch_bounds__(256) void loss_prep_w_kernel(const uint16_t* __restrict__ scales,
-                                                          const uint16_t* __restrict__ biases, int64_t n, int groups,
-                                                          int64_t np, int gp, uint16_t* __restrict__ st,
-                                                          uint16_t* __restrict__ bp)
+template <class E>
+__global__ __launch_bounds__(256) void loss_prep_w_kernel(const E* __restrict__ scales, const E* __restrict__ biases,
+                                                          int64_t n, int groups, int64_t np, int gp,
+                                                          E* __restrict__ st, E* __restrict__ bp)
 {
-    __shared__ uint16_t room[64][66];
+    __shared__ E room[64][64 + 4 / sizeof(E)];
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
     const int tiles_g = (gp + 63) / 64;
     const int g0 = (int)(blockIdx.x % tiles_g) * 64;
@@ -240,9 +240,9 @@ __global__ __launch_bounds__(256) void loss_prep_w_kernel(const uint16_t* __rest
     for (int i = 0; i < 16; ++i) {
         const int64_t v = v0 + 4 * i + wave;
         const bool in = v < n && g < groups;
-        room[4 * i + wave][lane] = in ? scales[v * groups + g] : (uint16_t)0;
+        room[4 * i + wave][lane] = in ? scales[v * groups + g] : (E)0;
         if (bp != nullptr && v < n && g < gp)
-            bp[v * gp + g] = in ? biases[v * groups + g] : (uint16_t)0;
+            bp[v * gp + g] = in ? biases[v * groups + g] : (E)0;
     }
     __syncthreads();
 #pragma unroll
@@ -306,7 +306,7 @@ unsigned grid_of(int64_t n) { return (unsigned)std::min<int64_t>((n + 255) / 256
 
 // Whether the tile kernel takes a product (its last step holds a row's last 64 features;
 // up to 16 rows the decode kernels stream the weights once).
-bool tile_product(int64_t m, int64_t k, int dt) { return dt != DT_F32 && m > 16 && k >= 64 && k <= (1 << 20); }
+bool tile_product(int64_t m, int64_t k, int dt) { return (dt == DT_F32 || m > 16) && k >= 64 && k <= (1 << 18); }
 
 hipError_t tile_kernel(int bits, int dt, const LossTileArgs& a, hipStream_t st)
 {
@@ -332,38 +332,45 @@ hipError_t prep_x(int bits, int dt, const LossTileArgs& a, const void* x, hipStr
 }
 
 // Fills a.st and, where bp is given, bp.
-hipError_t prep_w(const LossTileArgs& a, const void* scales, const void* biases, void* bp, hipStream_t st)
+template <class E>
+hipError_t prep_w_of(const LossTileArgs& a, const void* scales, const void* biases, void* bp, hipStream_t st)
 {
     const int64_t blocks = (int64_t)(a.np / 64) * ((a.gp + 63) / 64);
     if (!grid_fits(blocks, 256))
         return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(loss_prep_w_kernel, dim3((unsigned)blocks), dim3(256), 0, st,
-                       static_cast<const uint16_t*>(scales), static_cast<const uint16_t*>(biases), (int64_t)a.N,
-                       a.K / a.gs, (int64_t)a.np, a.gp, static_cast<uint16_t*>(const_cast<void*>(a.st)),
-                       static_cast<uint16_t*>(bp));
+    hipLaunchKernelGGL(loss_prep_w_kernel<E>, dim3((unsigned)blocks), dim3(256), 0, st, static_cast<const E*>(scales),
+                       static_cast<const E*>(biases), (int64_t)a.N, a.K / a.gs, (int64_t)a.np, a.gp,
+                       static_cast<E*>(const_cast<void*>(a.st)), static_cast<E*>(bp));
     return hipGetLastError();
+}
+hipError_t prep_w(const LossTileArgs& a, int dt, const void* scales, const void* biases, void* bp, hipStream_t st)
+{
+    return dt == DT_F32 ? prep_w_of<uint32_t>(a, scales, biases, bp, st) : prep_w_of<uint16_t>(a, scales, biases, bp, st);
 }
 
 // What the tile kernel reads beside the codes, laid out once a call (x) or a piece (the
 // weight's): sizes in bytes.
 struct TileRoom {
     int64_t xn, gp;
-    size_t xp, st, bp;
-    size_t all() const { return xp + st + bp; }
+    size_t xp, xs, st, bp;
+    size_t all() const { return xp + xs + st + bp; }
 };
-TileRoom tile_room(int64_t m, int64_t k, int64_t piece, int gs)
+TileRoom tile_room(int64_t m, int64_t k, int64_t piece, int gs, int dt)
 {
-    const int64_t gp = (k / gs + 31) / 32 * 32, xn = 2 * gp + (k + 63) / 64 * 64;
-    const int64_t np = (piece + LOSS_BN - 1) / LOSS_BN * LOSS_BN;
-    return {xn, gp, up16((size_t)m * (size_t)xn * 2), up16((size_t)(k / gs) * (size_t)np * 2),
-            up16((size_t)piece * (size_t)gp * 2)};
+    const bool f32 = dt == DT_F32;
+    const size_t es = elem_size(dt);
+    const int64_t fill = f32 ? 8 : 32, gp = (k / gs + fill - 1) / fill * fill, kp = (k + 63) / 64 * 64;
+    const int64_t xn = f32 ? 3 * kp : 2 * gp + kp, np = (piece + LOSS_BN - 1) / LOSS_BN * LOSS_BN;
+    return {xn, gp, up16((size_t)m * (size_t)xn * 2), f32 ? up16((size_t)m * (size_t)gp * 4) : 0,
+            up16((size_t)(k / gs) * (size_t)np * es), up16((size_t)piece * (size_t)gp * es)};
 }
 // The kernel's arguments for x, which is laid out at `room`; the weight's follow it.
 hipError_t tile_begin(LossTileArgs& t, const TileRoom& r, char* room, const void* x, int dt, int64_t m, int64_t k,
                       int bits, int gs, int64_t vocab, const int32_t* targets, hipStream_t st)
 {
     t.xp = room;
-    t.st = room + r.xp;
+    t.xs = room + r.xp;
+    t.st = room + r.xp + r.xs;
     t.M = (int)m; t.K = (int)k; t.gs = gs;
     t.xn = (int)r.xn; t.gp = (int)r.gp;
     t.vocab = vocab;
@@ -381,9 +388,9 @@ hipError_t tile_piece(LossTileArgs& t, const TileRoom& r, char* room, const QWei
     t.part0 = (int)(v0 / LOSS_BN);
     // The biases as they lie, where their rows are whole 16-byte pieces.
     const bool as_is = t.gp == t.K / t.gs && aligned16(w.biases);
-    char* const bp = room + r.xp + r.st;
+    char* const bp = room + r.xp + r.xs + r.st;
     t.bp = as_is ? w.biases : bp;
-    if (hipError_t e = prep_w(t, w.scales, w.biases, as_is ? nullptr : bp, st); e != hipSuccess)
+    if (hipError_t e = prep_w(t, dt, w.scales, w.biases, as_is ? nullptr : bp, st); e != hipSuccess)
         return e;
     return tile_kernel(bits, dt, t, st);
 }
@@ -391,7 +398,7 @@ hipError_t tile_piece(LossTileArgs& t, const TileRoom& r, char* room, const QWei
 // about 128 MB, but not less than 2048 tokens.
 int64_t tile_piece_of(int64_t m, int64_t k, int64_t v, int gs, bool grad)
 {
-    int64_t most = std::max<int64_t>((int64_t(1) << 28) / (k / gs) / LOSS_BN * LOSS_BN, LOSS_BN);
+    int64_t most = std::max<int64_t>((int64_t(1) << 27) / (k / gs) / LOSS_BN * LOSS_BN, LOSS_BN);
     if (grad)
         most = std::min(most, std::max<int64_t>((int64_t(1) << 26) / m / LOSS_BN * LOSS_BN, 2048));
     return std::min(most, v);
@@ -416,7 +423,7 @@ LossRoom loss_room(int64_t m, int64_t k, int64_t v, int gs, int dt)
     r.stats = up16((size_t)r.parts * (size_t)m * sizeof(Stat));
     r.picked = up16((size_t)m * 4);
     if (r.tiles)
-        r.t = tile_room(m, k, r.piece, gs);
+        r.t = tile_room(m, k, r.piece, gs, dt);
     else
         r.z = up16((size_t)m * (size_t)r.piece * 4);
     if (rows_product(m, dt))
@@ -439,14 +446,14 @@ LossGradRoom loss_grad_room(int64_t m, int64_t k, int64_t v, int gs, int dt)
     LossGradRoom r{};
     r.tiles = tile_product(m, k, dt);
     r.piece = r.tiles ? tile_piece_of(m, k, v, gs, true) : piece_of(m, v);
-    r.stride = dt == DT_F32 ? r.piece : (r.piece + 7) & ~(int64_t)7;
+    r.stride = dt == DT_F32 && !r.tiles ? r.piece : (r.piece + 7) & ~(int64_t)7;
     r.scale = 16;
     r.sums = r.piece < v ? up16((size_t)m * (size_t)k * 4) : 0;
     if (r.tiles)
-        r.t = tile_room(m, k, r.piece, gs);
+        r.t = tile_room(m, k, r.piece, gs, dt);
     else
         r.z = up16((size_t)m * (size_t)r.piece * 4);
-    r.dz = dt == DT_F32 ? 0 : up16((size_t)m * (size_t)r.stride * 2);
+    r.dz = r.z != 0 && dt == DT_F32 ? 0 : up16((size_t)m * (size_t)r.stride * elem_size(dt));
     r.x = rows_product(m, dt) || grad_tile_sizes(r.piece, k, dt) ? piece_bytes(m, k) : 0;
     // The last piece may be shorter, and its plans others.
     for (const int64_t n : {r.piece, v - (v - 1) / r.piece * r.piece})
@@ -559,7 +566,7 @@ hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t st)
     float* const sums = reinterpret_cast<float*>(take(r.sums));
     float* const z = reinterpret_cast<float*>(take(r.z));
     char* const room = take(r.t.all());
-    void* const dz = a.dt == DT_F32 ? static_cast<void*>(z) : take(r.dz);
+    void* const dz = r.dz == 0 ? static_cast<void*>(z) : take(r.dz);   // (fp32: over the logits)
     char* const xcopy = take(r.x);
     float* const partial = reinterpret_cast<float*>(at);
     const bool half = a.dt != DT_F32, tiles = grad_tile_sizes(r.piece, a.K, a.dt);
@@ -578,14 +585,14 @@ hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t st)
     if (r.tiles) {
         t.dz = dz;
         t.dz_stride = r.stride;
-        t.lse = a.lse; t.dloss = a.dloss; t.scale = scale;
+        t.lse = a.lse; t.dloss = a.dloss; t.scale = half ? scale : nullptr;
         if (hipError_t e = tile_begin(t, r.t, room, a.x, a.dt, a.M, a.K, a.bits, a.gs, a.V, a.targets, st); e != hipSuccess)
             return e;
     }
     for (int64_t v0 = 0; v0 < a.V; v0 += r.piece) {
         const int64_t n = std::min(r.piece, a.V - v0), es = (int64_t)elem_size(a.dt);
         const QWeight w = rows_from(a.w, v0, a.K, a.bits, a.gs, a.dt);
-        const int64_t stride = a.dt == DT_F32 ? n : r.stride;
+        const int64_t stride = a.dt == DT_F32 && !r.tiles ? n : r.stride;
         if (r.tiles) {
             if (hipError_t e = tile_piece(t, r.t, room, w, a.bits, a.dt, v0, n, st); e != hipSuccess)
                 return e;

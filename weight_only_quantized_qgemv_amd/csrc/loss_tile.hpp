@@ -17,6 +17,9 @@
 // of a tile are then 512 bytes in a row) and the biases in rows of whole 16-byte
 // pieces. Both are a few microseconds beside the tiles.
 //
+// fp32 x is three steps of 16-bit parts, 24 bits together, so that its products are exact
+// on the same instructions, 16 times as fast as the fp32 ones.
+//
 // Waves of 32 FM rows x 64 columns, WMW x 4 of them; steps of 64 k; x in NA and codes
 // and scales in NC stages of LDS, by DMA, with the swizzles of gemm_core.hpp.
 #pragma once
@@ -61,10 +64,23 @@ __device__ __forceinline__ float sum8(float v)
     return v + dpp_f32<0x141>(v);
 }
 
+// fp32 x goes in three parts of 16 bits, each a step of its own.
+template <int DT> constexpr int OPERAND = DT == DT_F32 ? DT_BF16 : DT;
+template <int DT> constexpr int PARTS = DT == DT_F32 ? 3 : 1;
+
+// A step's scales: 256 columns of one group (of 32: two) in pieces of 256 bytes, a piece a
+// wave and instruction.
+template <int DT, int WMW, bool G32> struct ScaleStage {
+    static constexpr int PER_GROUP = DT == DT_F32 ? 4 : 2;
+    static constexpr int PIECES = PER_GROUP * (G32 ? 2 : 1), WAVES = 4 * WMW;
+    static constexpr int INSTR = (PIECES + WAVES - 1) / WAVES, STAGE = INSTR * WAVES * 256;
+};
+
 // Stages of the products, and then of the close.
-template <int BITS, int FM, int WMW> constexpr int lds_bytes()
+template <int BITS, int DT, int FM, int WMW, bool G32> constexpr int lds_bytes()
 {
-    constexpr int steps = NA * 32 * FM * WMW * 128 + NC<BITS> * (CodeStage<BITS, LOSS_BN, 4 * WMW>::STAGE + 4 * WMW * 256);
+    constexpr int steps = NA * 32 * FM * WMW * 128 + NC<BITS> * (CodeStage<BITS, LOSS_BN, 4 * WMW>::STAGE +
+                                                                 ScaleStage<DT, WMW, G32>::STAGE);
     constexpr int close = 4 * WMW * 32 * 68 * 4 + 4 * 32 * FM * WMW * (int)sizeof(Stat);
     return steps > close ? steps : close;
 }
@@ -86,18 +102,21 @@ __device__ __forceinline__ void dma4_at(__amdgpu_buffer_rsrc_t r, char* dst, uin
 template <int BITS, int DT, int FM, int WMW, bool G32>
 __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
 {
-    using T = MfmaTraits<DT>;
+    constexpr int OT = OPERAND<DT>, P3 = PARTS<DT>;
+    using T = MfmaTraits<OT>;
+    using St = typename Elem<DT>::storage;
+    using SS = ScaleStage<DT, WMW, G32>;
     using frag_t = typename T::frag_t;
     using CL = CodeLayout<BITS>;
     constexpr int WAVES = 4 * WMW, WGN = 4, FN = 2, WN = 64, WM = 32 * FM, BM = WM * WMW, BN = LOSS_BN, BK = 64;
     constexpr int A_STAGE = BM * 128, A_INSTR = A_STAGE / 1024 / WAVES;
     static_assert(A_INSTR * 1024 * WAVES == A_STAGE, "whole DMA blocks");
     constexpr int C_INSTR = CodeStage<BITS, BN, WAVES>::INSTR, C_STAGE = CodeStage<BITS, BN, WAVES>::STAGE;
-    constexpr int SB_STAGE = WAVES * 256;
+    constexpr int SB_STAGE = SS::STAGE, S_INSTR = SS::INSTR, ES = (int)sizeof(St);
     constexpr int NCS = NC<BITS>;
     // As in gemm_core.hpp: step kt + 1 reads the activations and codes of kt + 2 at
     // its end; what was issued after them may be in flight when step kt ends.
-    constexpr int IN_FLIGHT = NCS > NA ? C_INSTR + 1 : 0;
+    constexpr int IN_FLIGHT = NCS > NA ? C_INSTR + S_INSTR : 0;
     static_assert(NA == 3 && (NCS == 3 || NCS == 4), "prefetch depth");
     extern __shared__ __attribute__((aligned(16))) char lds[];
     char* const a_st = lds;
@@ -115,7 +134,8 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WGN, wn = wave % WGN;
     const uint32_t xrow = (uint32_t)a.xn * 2, wrow = (uint32_t)a.K * BITS / 8;
-    const int KT = (a.K + BK - 1) / BK, BT = a.gp / 32, groups = a.K / a.gs, rows_left = a.M - m0;
+    const int KT = (a.K + BK - 1) / BK * P3, BT = DT == DT_F32 ? 0 : a.gp / 32;   // steps of the codes, of the biases
+    const int groups = a.K / a.gs, rows_left = a.M - m0;
 
     // A tile's own rows as resources: their offsets are below 2^31 whatever M and N are.
     const __amdgpu_buffer_rsrc_t rx = rsrc(static_cast<const char*>(a.xp) + (size_t)m0 * xrow,
@@ -123,8 +143,8 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
     const int cols_left = a.N - n0;
     const __amdgpu_buffer_rsrc_t rw = rsrc(reinterpret_cast<const char*>(a.wq) + (size_t)n0 * wrow,
                                            (uint32_t)(cols_left < BN ? cols_left : BN) * wrow);
-    const __amdgpu_buffer_rsrc_t rs = rsrc(static_cast<const char*>(a.st) + (size_t)n0 * 2,
-                                           (uint32_t)(groups - 1) * (uint32_t)a.np * 2 + 2 * BN);
+    const __amdgpu_buffer_rsrc_t rs = rsrc(static_cast<const char*>(a.st) + (size_t)n0 * ES,
+                                           (uint32_t)(groups - 1) * (uint32_t)a.np * ES + ES * BN);
 
     uint32_t a_goff[A_INSTR];
 #pragma unroll
@@ -139,10 +159,8 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
         const int r = q / CL::CPR, part = (q % CL::CPR) ^ code_swz<BITS>(r);
         c_goff[i] = q < BN * CL::CPR && r < cols_left ? (uint32_t)r * wrow + part * CL::CS : OOB;
     }
-    // Scales: wave w takes 128 columns of a group, w % 2 of the tile's two halves; groups
-    // of 32 have two a step (waves 2, 3). The others' go to spare room.
-    constexpr int SB_WAVES = G32 ? 4 : 2;
-    const uint32_t s_goff = wave < SB_WAVES ? (uint32_t)(wave & 1) * 256 + (uint32_t)lane * 4 : OOB;
+    // Scales: piece q is part q % PER_GROUP of group q / PER_GROUP of the step's; waves
+    // without one read past the range, into spare room.
     const int gs_steps = a.gs == 128 ? 1 : 0;   // log2 of the steps of a group (of 64 and more)
 
     // DMA operation o of step kt's: A_INSTR of the activations, C_INSTR of the codes, the
@@ -155,18 +173,21 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
     auto dma_c = [&](int kt, int stage, int i) {
         // The last step of 64 n + 32 features holds the row's last two units; the biases'
         // steps, before step 0, have none of their own.
-        const int k = (kt > 0 ? kt : 0) * CL::RB, last = (int)wrow - CL::RB, off = k < last ? k : last;
+        const int k = (kt > 0 ? kt / P3 : 0) * CL::RB, last = (int)wrow - CL::RB, off = k < last ? k : last;
         char* const dst = c_st + stage * C_STAGE + (wave * C_INSTR + i) * 1024;
         if constexpr (CL::CS == 12)
             dma12_at(rw, dst, c_goff[i], off);
         else
             dma16_at(rw, dst, c_goff[i], off);
     };
-    auto dma_s = [&](int kt, int stage) {
-        int g = kt < 0 ? 0 : G32 ? 2 * kt : kt >> gs_steps;
+    auto dma_s = [&](int kt, int stage, int i) {
+        const int q = wave + WAVES * i;
+        kt = kt > 0 ? kt / P3 : 0;
+        int g = G32 ? 2 * kt : kt >> gs_steps;
         const int most = groups - (G32 ? 2 : 1);
-        g = (g < most ? g : most) + (G32 ? wave >> 1 : 0);
-        dma4_at(rs, sb_st + stage * SB_STAGE + wave * 256, s_goff, g * a.np * 2);
+        g = (g < most ? g : most) + (G32 ? q / SS::PER_GROUP % 2 : 0);
+        dma4_at(rs, sb_st + stage * SB_STAGE + q * 256,
+                q < SS::PIECES ? (uint32_t)(q % SS::PER_GROUP) * 256 + (uint32_t)lane * 4 : OOB, g * a.np * ES);
     };
     auto step_barrier = [&](auto VM) {
         __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(decltype(VM)::value));
@@ -183,7 +204,8 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
                 dma_a(s + NA - 1, s + NA - 1, i);
         for (int i = 0; i < C_INSTR; ++i)
             dma_c(s + NCS - 1 - BT, s + NCS - 1, i);
-        dma_s(s + NCS - 1 - BT, s + NCS - 1);
+        for (int i = 0; i < S_INSTR; ++i)
+            dma_s(s + NCS - 1 - BT, s + NCS - 1, i);
     }
     f32x16_t total[FM][FN];
 #pragma unroll
@@ -201,8 +223,34 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
     int a_cur = 0, c_cur = 0;
     // The biases: 32 groups a step, instructions 0 and 1 the high and the low part of X
     // times b of the first 16 groups, 2 and 3 of the others. b's fragments come from memory,
-    // a step ahead.
-    {
+    // a step ahead. With fp32 x, X and b are fp32 too, eight groups at a time on the fp32
+    // instruction.
+    if constexpr (DT == DT_F32) {
+        const uint32_t grow = (uint32_t)a.gp * 4;
+        const __amdgpu_buffer_rsrc_t rb = rsrc(static_cast<const char*>(a.bp) + (size_t)n0 * grow,
+                                               (uint32_t)(cols_left < BN ? cols_left : BN) * grow);
+        const __amdgpu_buffer_rsrc_t rg = rsrc(static_cast<const char*>(a.xs) + (size_t)m0 * grow,
+                                               (uint32_t)(rows_left < BM ? rows_left : BM) * grow);
+        for (uint32_t g = 0; g < grow; g += 32) {
+            f32x4_t bf[FN], xf[FM];
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                bf[j] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                    rb, (uint32_t)(wn * WN + 32 * j + c32) * grow + g + 16 * half, 0, 0));
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+                xf[i] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                    rg, (uint32_t)(wm * WM + 32 * i + c32) * grow + g + 16 * half, 0, 0));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+                        total[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(xf[i][e], bf[j][e], total[i][j], 0, 0, 0);
+        }
+        step_barrier(std::integral_constant<int, 0>{});
+    } else {
         const uint32_t grow = (uint32_t)a.gp * 2;
         const __amdgpu_buffer_rsrc_t rb = rsrc(static_cast<const char*>(a.bp) + (size_t)n0 * grow,
                                                (uint32_t)(cols_left < BN ? cols_left : BN) * grow);
@@ -233,7 +281,9 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
 #pragma unroll
             for (int i = 0; i < C_INSTR; ++i)
                 dma_c(bt + NCS - 1 - BT, c_new, i);
-            dma_s(bt + NCS - 1 - BT, c_new);
+#pragma unroll
+            for (int i = 0; i < S_INSTR; ++i)
+                dma_s(bt + NCS - 1 - BT, c_new, i);
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -262,7 +312,7 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
     // parts (groups of 32: two).
     uint32_t bq[FN][16], raw[FN][BITS];
     float sc[FN][G32 ? 2 : 1];
-    uint16_t raws[FN][G32 ? 2 : 1];
+    St raws[FN][G32 ? 2 : 1];
     auto load_codes = [&](auto J, int stage) {
         constexpr int j = decltype(J)::value;
         const int r = wn * WN + 32 * j + c32;
@@ -286,15 +336,15 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
                 w[2 * i + 1] = v[1];
             }
         }
-        const char* const sb = sb_st + stage * SB_STAGE + 2 * r;
+        const char* const sb = sb_st + stage * SB_STAGE + ES * r;
 #pragma unroll
         for (int u = 0; u < (G32 ? 2 : 1); ++u)
-            raws[j][u] = *reinterpret_cast<const uint16_t*>(sb + 512 * u);
+            raws[j][u] = *reinterpret_cast<const St*>(sb + BN * ES * u);
     };
     auto convert = [&](auto J, auto P) {
         constexpr int j = decltype(J)::value, p = decltype(P)::value;
         uint32_t q[16];
-        code_pairs<BITS, DT>(raw[j], 0u, q);   // (of which the rest is dropped)
+        code_pairs<BITS, OT>(raw[j], 0u, q);   // (of which the rest is dropped)
         if constexpr (G32) {
             if constexpr (p < 2) {
 #pragma unroll
@@ -324,7 +374,7 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
     // chains of a row block take the next one's fragments into the registers that they
     // have read; column block 0's codes of the next step are converted under the last
     // chain, block 1's under the next step's first; the DMA is spread over the first.
-    constexpr int U = G32 ? 2 : 1, L = 4 / U, CHAINS = FM * FN * U, DMAS = A_INSTR + C_INSTR + 1;
+    constexpr int U = G32 ? 2 : 1, L = 4 / U, CHAINS = FM * FN * U, DMAS = A_INSTR + C_INSTR + S_INSTR;
     frag_t af[4];
     f32x16_t acc[2];
     auto scale_part = [&](auto C, auto R0, auto R1) {   // registers R0 .. R1 - 1 of chain C's sums
@@ -362,7 +412,7 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
                 else if constexpr (q < A_INSTR + C_INSTR)
                     dma_c(kt + NCS - 1, c_new, q - A_INSTR);
                 else
-                    dma_s(kt + NCS - 1, c_new);
+                    dma_s(kt + NCS - 1, c_new, q - A_INSTR - C_INSTR);
             }
             constexpr int R0 = L == 4 ? (l == 0 ? 0 : l == 1 ? 0 : l == 2 ? 6 : 11) : (l == 0 ? 0 : 4);
             constexpr int R1 = L == 4 ? (l == 0 ? 0 : l == 1 ? 6 : l == 2 ? 11 : 16) : (l == 0 ? 4 : 16);
@@ -401,10 +451,10 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
     float* const turned = reinterpret_cast<float*>(lds) + wave * 32 * S;
     Stat* const stats = reinterpret_cast<Stat*>(lds + WAVES * 32 * S * 4);   // [WGN][BM]
     const int part = l & 7, col0 = wn * WN + 8 * part;   // the lane's first column in the tile
-    const uint32_t drow = (uint32_t)a.dz_stride * 2;
-    const __amdgpu_buffer_rsrc_t rd = rsrc(static_cast<char*>(a.dz) + (a.dz != nullptr ? (size_t)m0 * drow + (size_t)n0 * 2 : 0),
-                                           a.dz != nullptr ? (uint32_t)(rows_left < BM ? rows_left : BM) * drow - (uint32_t)n0 * 2 : 0u);
-    const float by = a.dz != nullptr ? a.scale[0] : 0.0f;
+    const uint32_t drow = (uint32_t)a.dz_stride * ES;
+    const __amdgpu_buffer_rsrc_t rd = rsrc(static_cast<char*>(a.dz) + (a.dz != nullptr ? (size_t)m0 * drow + (size_t)n0 * ES : 0),
+                                           a.dz != nullptr ? (uint32_t)(rows_left < BM ? rows_left : BM) * drow - (uint32_t)n0 * ES : 0u);
+    const float by = a.dz != nullptr && a.scale != nullptr ? a.scale[0] : 1.0f;
     static_for<FM>([&](auto I) {
         constexpr int i = decltype(I)::value;
         __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(63));   // the last rows have been read
@@ -434,19 +484,23 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
                 // dz, and zeros up to the next multiple of 8 columns. (A row without a target,
                 // or of g = 0, is zeros whatever its logits are.)
                 const float lse = in ? a.lse[m0 + row] : 0.0f, g = live ? a.dloss[m0 + row] * by : 0.0f;
-                u32x4_t w;
+                uint32_t w[2 * ES];
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    uint16_t v[2];
-#pragma unroll
-                    for (int o = 0; o < 2; ++o) {
-                        const float d = g * (exp_fast(z[e + o] - lse) - (at == e + o ? 1.0f : 0.0f));
-                        v[o] = Elem<DT>::from_f32(d) & (g != 0.0f && col0 + e + o < cols_left ? 0xFFFFu : 0u);
+                for (int e = 0; e < 8; ++e) {
+                    const float d = g * (exp_fast(z[e] - lse) - (at == e ? 1.0f : 0.0f));
+                    const bool keep = g != 0.0f && col0 + e < cols_left;
+                    if constexpr (DT == DT_F32) {
+                        w[e] = keep ? __float_as_uint(d) : 0u;
+                    } else {
+                        const uint32_t v = keep ? Elem<DT>::from_f32(d) : 0u;
+                        w[e / 2] = e % 2 ? w[e / 2] | (v << 16) : v;
                     }
-                    w[e / 2] = (uint32_t)v[0] | ((uint32_t)v[1] << 16);
                 }
-                __builtin_amdgcn_raw_buffer_store_b128(w, rd, in && col0 < cols_left ? (uint32_t)row * drow + (uint32_t)col0 * 2 : OOB,
-                                                       0, 0);
+#pragma unroll
+                for (int e = 0; e < ES / 2; ++e)
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        u32x4_t{w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]}, rd,
+                        in && col0 < cols_left ? (uint32_t)row * drow + (uint32_t)col0 * ES + 16 * e : OOB, 0, 0);
                 continue;
             }
             if (live && at >= 0 && at < 8)
@@ -547,6 +601,68 @@ __global__ __launch_bounds__(256) void loss_prep_x_kernel(const uint16_t* __rest
     }
     if (chunk == 0 && k / gs + lane < gp)   // fewer than 32 to fill up
         put(k / gs + lane, 0, 0);
+}
+
+// fp32 x: each 64 features are three steps, x in parts of 16 bits (what the parts before
+// leave, which is exact: 24 bits in all); X in fp32, rows of gp.
+template <int BITS>
+__global__ __launch_bounds__(256) void loss_prep_x32_kernel(const float* __restrict__ x, int64_t m, int k, int gs,
+                                                            int xn, int gp, uint16_t* __restrict__ xp,
+                                                            float* __restrict__ xs)
+{
+    using Order = CodeOrder<BITS>;
+    using E = Elem<DT_BF16>;
+    typedef f32x4_t Wide __attribute__((aligned(4)));
+    const int units = xn / 96, chunks = (units + 63) / 64, lane = (int)threadIdx.x & 63;
+    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), row = w / chunks;
+    if (row >= m)
+        return;
+    const int chunk = (int)(w % chunks), u = chunk * 64 + lane, n = k / 32;
+    const int src = u < n - (n & 1) ? u : u == units - 1 ? n - 1 : -1;   // (n odd: the last step)
+    float e[32];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        e[i] = 0.0f;
+    if (src >= 0) {
+        const float* const p = x + row * k + src * 32;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const f32x4_t v = *reinterpret_cast<const Wide*>(p + 4 * i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                e[4 * i + j] = v[j];
+                sum += v[j];
+            }
+        }
+    }
+    if (u < units) {
+        uint16_t* const to = xp + row * xn + u / 2 * 192 + u % 2 * 32;
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+            uint32_t h[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                h[i] = E::from_f32(e[i]);
+                e[i] -= E::to_f32((uint16_t)h[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                u32x4_t v;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[j] = h[Order::lo_code(4 * i + j)] | (h[Order::hi_code(4 * i + j)] << 16);
+                *reinterpret_cast<u32x4_t*>(to + 64 * part + 8 * i) = v;
+            }
+        }
+    }
+    const int per = gs / 32;
+    for (int off = 1; off < per; off <<= 1)
+        sum += __shfl_xor(sum, off, 64);
+    if (src >= 0 && src % per == 0)
+        xs[row * gp + src / per] = sum;
+    if (chunk == 0 && k / gs + lane < gp)   // fewer than 8 to fill up
+        xs[row * gp + k / gs + lane] = 0.0f;
 }
 
 } // namespace losstile

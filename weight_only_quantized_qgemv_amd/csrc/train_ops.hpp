@@ -73,17 +73,19 @@ struct LossGradArgs {
 size_t loss_grad_workspace_bytes(int64_t m, int64_t k, int64_t v, int bits, int gs, int dt);
 hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t stream);
 
-// The tile kernel of the loss (loss_tile.hpp): rows of 16-bit x times a piece of the
+// The tile kernel of the loss (loss_tile.hpp): rows of x times a piece of the
 // vocabulary, closed to statistics or (dz) to the logits' gradient.
 constexpr int LOSS_BN = 256;   // columns of a tile, and of a part of the statistics
 struct Stat;
 struct LossTileArgs {
-    const void* xp;          // [M, xn]: the groups' sums of x, then x (loss_prep_x)
+    const void* xp;          // [M, xn] of 16 bits: the groups' sums of x, then x (fp32: x in three parts)
+    const void* xs;          // [M, gp]: the groups' sums (fp32 x)
     const uint32_t* wq;      // [N, K*bits/32]
     const void* st;          // [K/gs, np]: the scales, transposed (loss_prep_w)
     const void* bp;          // [N, gp]: the biases
     int M, N, K, gs;
-    int xn, gp, np;          // the groups and N filled up to 32 and LOSS_BN; 2 gp + K filled up to 64
+    int xn, gp, np;          // the groups filled up to 32 (fp32: 8), N to LOSS_BN; xn: 2 gp + K filled
+                             // up to 64 (fp32: three times that K)
     int tiles_m, tiles, per_xcd;
     const int32_t* targets;  // [M]
     int64_t vocab, v0;       // the whole vocabulary; the piece's first token
