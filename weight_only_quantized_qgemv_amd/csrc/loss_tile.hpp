@@ -146,18 +146,19 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
     const __amdgpu_buffer_rsrc_t rs = rsrc(static_cast<const char*>(a.st) + (size_t)n0 * ES,
                                            (uint32_t)(groups - 1) * (uint32_t)a.np * ES + ES * BN);
 
-    uint32_t a_goff[A_INSTR];
+    // Instruction i's rows are 8 i on, where the swizzle has one bit the other way round.
+    // (Past the tile's rows: past the range.)
+    const int a_r = 8 * wave * A_INSTR + (lane >> 3);
+    uint32_t a_goff = (uint32_t)a_r * xrow + (uint32_t)(((lane & 7) ^ swz(a_r)) * 16);
+    // Codes: where an instruction's 64 chunks are whole rows, instruction i's rows are so many
+    // rows on, with the same swizzle.
+    constexpr bool WHOLE = 64 % CL::CPR == 0;
+    uint32_t c_goff[WHOLE ? 1 : C_INSTR];
 #pragma unroll
-    for (int i = 0; i < A_INSTR; ++i) {
-        const int r = 8 * (wave * A_INSTR + i) + (lane >> 3);
-        a_goff[i] = (uint32_t)r * xrow + (uint32_t)(((lane & 7) ^ swz(r)) * 16);   // (past the rows: past the range)
-    }
-    uint32_t c_goff[C_INSTR];
-#pragma unroll
-    for (int i = 0; i < C_INSTR; ++i) {
+    for (int i = 0; i < (WHOLE ? 1 : C_INSTR); ++i) {
         const int q = 64 * (wave * C_INSTR + i) + lane;
         const int r = q / CL::CPR, part = (q % CL::CPR) ^ code_swz<BITS>(r);
-        c_goff[i] = q < BN * CL::CPR && r < cols_left ? (uint32_t)r * wrow + part * CL::CS : OOB;
+        c_goff[i] = WHOLE || q < BN * CL::CPR ? (uint32_t)r * wrow + part * CL::CS : OOB;   // (past the tile: past the range)
     }
     // Scales: piece q is part q % PER_GROUP of group q / PER_GROUP of the step's; waves
     // without one read past the range, into spare room.
@@ -168,17 +169,19 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
     // checked: rows past the tile are past the range by their own, and the activations'
     // last steps read on into the workspace behind them.
     auto dma_a = [&](int kt, int stage, int i) {
-        dma16_at(rx, a_st + stage * A_STAGE + (wave * A_INSTR + i) * 1024, a_goff[i], kt * BK * 2);
+        dma16_at(rx, a_st + stage * A_STAGE + (wave * A_INSTR + i) * 1024, (a_goff ^ (i % 2 ? 64u : 0u)) + (uint32_t)(8 * i) * xrow,
+                 kt * BK * 2);
     };
     auto dma_c = [&](int kt, int stage, int i) {
         // The last step of 64 n + 32 features holds the row's last two units; the biases'
         // steps, before step 0, have none of their own.
         const int k = (kt > 0 ? kt / P3 : 0) * CL::RB, last = (int)wrow - CL::RB, off = k < last ? k : last;
         char* const dst = c_st + stage * C_STAGE + (wave * C_INSTR + i) * 1024;
+        const uint32_t at = WHOLE ? c_goff[0] + (uint32_t)(i * (64 / CL::CPR)) * wrow : c_goff[WHOLE ? 0 : i];
         if constexpr (CL::CS == 12)
-            dma12_at(rw, dst, c_goff[i], off);
+            dma12_at(rw, dst, at, off);
         else
-            dma16_at(rw, dst, c_goff[i], off);
+            dma16_at(rw, dst, at, off);
     };
     auto dma_s = [&](int kt, int stage, int i) {
         const int q = wave + WAVES * i;
@@ -309,7 +312,7 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
     // B fragments of column block j for a step: the unit `half` of its row as 16 code
     // pairs, four a matrix instruction; with groups of 32 the halves of the wave swap so
     // that an instruction's two halves are of one unit. Loaded, and converted in four
-    // parts (groups of 32: two).
+    // parts.
     uint32_t bq[FN][16], raw[FN][BITS];
     float sc[FN][G32 ? 2 : 1];
     St raws[FN][G32 ? 2 : 1];
@@ -346,13 +349,11 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
         uint32_t q[16];
         code_pairs<BITS, OT>(raw[j], 0u, q);   // (of which the rest is dropped)
         if constexpr (G32) {
-            if constexpr (p < 2) {
 #pragma unroll
-                for (int i = 4 * p; i < 4 * p + 4; ++i) {
-                    const auto x = __builtin_amdgcn_permlane32_swap(q[i], q[8 + i], false, false);
-                    bq[j][i] = x[0];
-                    bq[j][8 + i] = x[1];
-                }
+            for (int i = 2 * p; i < 2 * p + 2; ++i) {
+                const auto x = __builtin_amdgcn_permlane32_swap(q[i], q[8 + i], false, false);
+                bq[j][i] = x[0];
+                bq[j][8 + i] = x[1];
             }
         } else {
 #pragma unroll
@@ -397,6 +398,9 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
         const int c_new = c_cur == 0 ? NCS - 1 : c_cur - 1;
         const int a_nxt = a_cur + 1 == NA ? 0 : a_cur + 1;
         const int c_nxt = c_cur + 1 == NCS ? 0 : c_cur + 1;
+        // Opaque, so that each instruction's offset is formed at its place and not kept in a
+        // register of its own through the steps: there are none to spare.
+        asm volatile("" : "+v"(a_goff), "+v"(c_goff[0]));
         static_for<CHAINS * L>([&](auto Q) {
             constexpr int q = decltype(Q)::value, c = q / L, l = q % L, i = c / (FN * U), j = c / U % FN, u = c % U;
             constexpr int kk = L * u + l, prev = (c + CHAINS - 1) % CHAINS;
@@ -422,8 +426,8 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
                 convert(std::integral_constant<int, 1>{}, std::integral_constant<int, q>{});
             if constexpr (q == CHAINS * L - 6)
                 load_codes(std::integral_constant<int, 0>{}, c_nxt);
-            if constexpr (q >= CHAINS * L - (G32 ? 2 : 4))
-                convert(std::integral_constant<int, 0>{}, std::integral_constant<int, q - (CHAINS * L - (G32 ? 2 : 4))>{});
+            if constexpr (q >= CHAINS * L - 4)
+                convert(std::integral_constant<int, 0>{}, std::integral_constant<int, q - (CHAINS * L - 4)>{});
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (q == CHAINS * L - 1)
                 take_scales(std::integral_constant<int, 0>{});
@@ -438,9 +442,9 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
     scale_part(std::integral_constant<int, CHAINS - 1>{}, std::integral_constant<int, 0>{}, std::integral_constant<int, 16>{});
     __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
     __builtin_amdgcn_s_barrier();   // the LDS is free
-    // Opaque here, so that the close's addresses are formed now and not kept in
-    // registers through the steps.
-    int l = lane;
+    // The lane's number anew, and opaque, so that neither it nor the close's addresses are
+    // kept in registers through the steps.
+    int l = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
     asm volatile("" : "+v"(l));
     const int half2 = l >> 5, c = l & 31;
 
