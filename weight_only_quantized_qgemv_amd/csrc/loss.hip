@@ -48,9 +48,7 @@ __global__ __launch_bounds__(256) void loss_parts_kernel(const float* __restrict
 #pragma unroll
     for (int i = 0; i < kPart / 256; ++i)
         s.sum += expf(v[i] - at);
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1)
-        s = join_stats(s, Stat{__shfl_xor(s.top, off, 64), __shfl_xor(s.sum, off, 64)});
+    s = wave_stat(s);
     if ((tid & 63) == 0)
         room[tid >> 6] = s;
     __syncthreads();
@@ -104,7 +102,6 @@ __global__ __launch_bounds__(1024) void loss_rows_kernel(const float* __restrict
     const float* const p = z + row * vocab;
     const int32_t target = targets[row];
     const bool live = target >= 0 && target < vocab;
-    const float picked = live ? p[target] : 0.0f;
     f32x4_t v[2][V];
     auto fetch = [&](int64_t c0, f32x4_t (&to)[V]) {
 #pragma unroll
@@ -137,6 +134,7 @@ __global__ __launch_bounds__(1024) void loss_rows_kernel(const float* __restrict
         s = Stat{top, sum};
     };
     fetch(0, v[0]);
+    const float picked = live ? p[target] : 0.0f;
     for (int64_t c = 0; c < vocab; c += 2 * STEP) {
         fetch(c + STEP, v[1]);
         take(v[0]);
@@ -145,19 +143,18 @@ __global__ __launch_bounds__(1024) void loss_rows_kernel(const float* __restrict
         fetch(c + 2 * STEP, v[0]);
         take(v[1]);
     }
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1)
-        s = join_stats(s, Stat{__shfl_xor(s.top, off, 64), __shfl_xor(s.sum, off, 64)});
+    s = wave_stat(s);
     if ((tid & 63) == 0)
         room[tid >> 6] = s;
     __syncthreads();
-    if (tid != 0)
+    if (tid >= 64)
         return;
-    for (int w = 1; w < 16; ++w)
-        s = join_stats(s, room[w]);
+    s = wave_stat<16>(room[tid & 15]);
     const float l = s.top + logf(s.sum);
-    lse[row] = l;
-    loss[row] = live ? l - picked : 0.0f;
+    if (tid == 0) {
+        lse[row] = l;
+        loss[row] = live ? l - picked : 0.0f;
+    }
 }
 
 // No features: every logit is 0. No vocabulary: lse is log 0.
@@ -509,9 +506,10 @@ hipError_t launch_loss(const LossArgs& a, hipStream_t st)
         if (hipError_t e = tile_begin(t, r.t, room, a.x, a.dt, a.M, a.K, a.bits, a.gs, a.V, a.targets, st); e != hipSuccess)
             return e;
     }
-    // Few rows whose logits are one piece, of a vocabulary that a block reads in some
-    // microseconds, need no parts.
-    const bool few = !r.tiles && a.M <= 16 && r.piece == a.V && a.V <= (1 << 18);
+    // Few rows whose logits are one piece, of a vocabulary that a block reads in two steps,
+    // need no parts: one row of 32000 6.7 us (in parts 3.9 and 3.8); 12 of 131071 18.9 (4.7 and
+    // 4.5).
+    const bool few = !r.tiles && a.M <= 16 && r.piece == a.V && a.V <= (1 << 16);
     const void* x = a.x;
     if (rows_product(a.M, a.dt)) {
         int64_t stride = a.K;   // whole pieces: it stays
