@@ -168,6 +168,15 @@ __global__ __launch_bounds__(256) void loss_even_kernel(int64_t m, int64_t vocab
     }
 }
 
+// The factor of dz, for the logits that are formed in full (the tiles' is found as x is
+// laid out).
+__global__ __launch_bounds__(256) void loss_scale_kernel(const float* __restrict__ dloss, int64_t m,
+                                                         const int32_t* __restrict__ targets, int64_t vocab,
+                                                         float* __restrict__ scale)
+{
+    dz_factor(dloss, m, targets, vocab, scale);
+}
+
 // dz of a piece from its logits; columns up to the next multiple of 8 are zeros
 // (the gradient products read 16-bit rows in 16-byte pieces). dz may be z (fp32).
 template <int DT>
@@ -186,66 +195,6 @@ __global__ __launch_bounds__(256) void loss_dz_kernel(const float* z, int64_t m,
             v = g * (expf(z[r * n + c] - lse[r]) - (t == v0 + c ? 1.0f : 0.0f));
         store_elem<DT>(dz, r * stride + c, v);
     }
-}
-
-// The factor that makes the rows' largest |dloss| 2^14, and what takes it out of the
-// sums again. dz is the products' 16-bit operand: most of it is p - 1 or a small p times
-// one and the same dloss, whose own rounding would not average out (2048 rows, a mean
-// over 1843 of them, in bf16: the gradients 0.0040 of their size off 64 bits, with
-// the factor 0.0024); and in fp16 a mean over many rows would leave the normal range
-// (2^-14) for a token of probability 1e-2 already.
-__global__ __launch_bounds__(1024) void loss_scale_kernel(const float* __restrict__ dloss, int64_t m,
-                                                          const int32_t* __restrict__ targets, int64_t vocab,
-                                                          float* __restrict__ scale)
-{
-    __shared__ float room[16];
-    float top = 0.0f;
-    for (int64_t i = threadIdx.x; i < m; i += 1024) {
-        const float g = fabsf(dloss[i]);
-        if (targets[i] >= 0 && targets[i] < vocab && g < __builtin_inff())
-            top = fmaxf(top, g);
-    }
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1)
-        top = fmaxf(top, __shfl_xor(top, off, 64));
-    if ((threadIdx.x & 63) == 0)
-        room[threadIdx.x >> 6] = top;
-    __syncthreads();
-    if (threadIdx.x != 0)
-        return;
-    for (int w = 1; w < 16; ++w)
-        top = fmaxf(top, room[w]);
-    top = top > 0.0f ? fmaxf(top, 0x1p-100f) : 16384.0f;   // (both factors stay finite)
-    scale[0] = 16384.0f / top;
-    scale[1] = top / 16384.0f;
-}
-
-// The scales [n, groups] transposed to [groups, np], zeros behind n, and the biases in
-// rows of gp (null: they lie so already). Tiles of 64 x 64.
-template <class E>
-__global__ __launch_bounds__(256) void loss_prep_w_kernel(const E* __restrict__ scales, const E* __restrict__ biases,
-                                                          int64_t n, int groups, int64_t np, int gp,
-                                                          E* __restrict__ st, E* __restrict__ bp)
-{
-    __shared__ E room[64][64 + 4 / sizeof(E)];
-    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    const int tiles_g = (gp + 63) / 64;
-    const int g0 = (int)(blockIdx.x % tiles_g) * 64;
-    const int64_t v0 = (int64_t)(blockIdx.x / tiles_g) * 64;
-    const int g = g0 + lane;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int64_t v = v0 + 4 * i + wave;
-        const bool in = v < n && g < groups;
-        room[4 * i + wave][lane] = in ? scales[v * groups + g] : (E)0;
-        if (bp != nullptr && v < n && g < gp)
-            bp[v * gp + g] = in ? biases[v * groups + g] : (E)0;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (g0 + 4 * i + wave < groups)
-            st[(int64_t)(g0 + 4 * i + wave) * np + v0 + lane] = room[lane][4 * i + wave];
 }
 
 // Vocabulary of a piece: logits of about 256 MB in fp32, whole parts, or all of it.
@@ -316,33 +265,16 @@ hipError_t tile_kernel(int bits, int dt, const LossTileArgs& a, hipStream_t st)
     }
     return hipErrorInvalidValue;
 }
-hipError_t prep_x(int bits, int dt, const LossTileArgs& a, const void* x, hipStream_t st)
+hipError_t prep(int bits, int dt, const LossTileArgs& a, const LossPrepArgs& p, hipStream_t st)
 {
     switch (bits) {
-    case 2: return launch_loss_prep_x_b2(dt, a, x, st);
-    case 3: return launch_loss_prep_x_b3(dt, a, x, st);
-    case 4: return launch_loss_prep_x_b4(dt, a, x, st);
-    case 6: return launch_loss_prep_x_b6(dt, a, x, st);
-    case 8: return launch_loss_prep_x_b8(dt, a, x, st);
+    case 2: return launch_loss_prep_b2(dt, a, p, st);
+    case 3: return launch_loss_prep_b3(dt, a, p, st);
+    case 4: return launch_loss_prep_b4(dt, a, p, st);
+    case 6: return launch_loss_prep_b6(dt, a, p, st);
+    case 8: return launch_loss_prep_b8(dt, a, p, st);
     }
     return hipErrorInvalidValue;
-}
-
-// Fills a.st and, where bp is given, bp.
-template <class E>
-hipError_t prep_w_of(const LossTileArgs& a, const void* scales, const void* biases, void* bp, hipStream_t st)
-{
-    const int64_t blocks = (int64_t)(a.np / 64) * ((a.gp + 63) / 64);
-    if (!grid_fits(blocks, 256))
-        return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(loss_prep_w_kernel<E>, dim3((unsigned)blocks), dim3(256), 0, st, static_cast<const E*>(scales),
-                       static_cast<const E*>(biases), (int64_t)a.N, a.K / a.gs, (int64_t)a.np, a.gp,
-                       static_cast<E*>(const_cast<void*>(a.st)), static_cast<E*>(bp));
-    return hipGetLastError();
-}
-hipError_t prep_w(const LossTileArgs& a, int dt, const void* scales, const void* biases, void* bp, hipStream_t st)
-{
-    return dt == DT_F32 ? prep_w_of<uint32_t>(a, scales, biases, bp, st) : prep_w_of<uint16_t>(a, scales, biases, bp, st);
 }
 
 // What the tile kernel reads beside the codes, laid out once a call (x) or a piece (the
@@ -361,9 +293,10 @@ TileRoom tile_room(int64_t m, int64_t k, int64_t piece, int gs, int dt)
     return {xn, gp, up16((size_t)m * (size_t)xn * 2), f32 ? up16((size_t)m * (size_t)gp * 4) : 0,
             up16((size_t)(k / gs) * (size_t)np * es), up16((size_t)piece * (size_t)gp * es)};
 }
-// The kernel's arguments for x, which is laid out at `room`; the weight's follow it.
-hipError_t tile_begin(LossTileArgs& t, const TileRoom& r, char* room, const void* x, int dt, int64_t m, int64_t k,
-                      int bits, int gs, int64_t vocab, const int32_t* targets, hipStream_t st)
+// The kernel's arguments that all pieces share: x is laid out at `room`, the weight's
+// follow it.
+void tile_begin(LossTileArgs& t, const TileRoom& r, char* room, int64_t m, int64_t k, int gs, int64_t vocab,
+                const int32_t* targets)
 {
     t.xp = room;
     t.xs = room + r.xp;
@@ -373,10 +306,10 @@ hipError_t tile_begin(LossTileArgs& t, const TileRoom& r, char* room, const void
     t.vocab = vocab;
     t.targets = targets;
     t.stat_rows = m;
-    return prep_x(bits, dt, t, x, st);
 }
-hipError_t tile_piece(LossTileArgs& t, const TileRoom& r, char* room, const QWeight& w, int bits, int dt, int64_t v0,
-                      int64_t n, hipStream_t st)
+// A piece: what it reads is laid out (x and the factor of dz with the first), then its tiles.
+hipError_t tile_piece(LossTileArgs& t, const TileRoom& r, char* room, const void* x, float* scale, const QWeight& w,
+                      int bits, int dt, int64_t v0, int64_t n, hipStream_t st)
 {
     t.wq = w.wq;
     t.N = (int)n;
@@ -387,7 +320,8 @@ hipError_t tile_piece(LossTileArgs& t, const TileRoom& r, char* room, const QWei
     const bool as_is = t.gp == t.K / t.gs && aligned16(w.biases);
     char* const bp = room + r.xp + r.xs + r.st;
     t.bp = as_is ? w.biases : bp;
-    if (hipError_t e = prep_w(t, dt, w.scales, w.biases, as_is ? nullptr : bp, st); e != hipSuccess)
+    const LossPrepArgs p{v0 == 0 ? x : nullptr, w.scales, w.biases, as_is ? nullptr : bp, v0 == 0 ? scale : nullptr};
+    if (hipError_t e = prep(bits, dt, t, p, st); e != hipSuccess)
         return e;
     return tile_kernel(bits, dt, t, st);
 }
@@ -503,8 +437,7 @@ hipError_t launch_loss(const LossArgs& a, hipStream_t st)
     if (r.tiles) {
         t.stats = stats;
         t.picked = picked;
-        if (hipError_t e = tile_begin(t, r.t, room, a.x, a.dt, a.M, a.K, a.bits, a.gs, a.V, a.targets, st); e != hipSuccess)
-            return e;
+        tile_begin(t, r.t, room, a.M, a.K, a.gs, a.V, a.targets);
     }
     // Few rows whose logits are one piece, of a vocabulary that a block reads in two steps,
     // need no parts: one row of 32000 6.7 us (in parts 3.9 and 3.8); 12 of 131071 18.9 (4.7 and
@@ -519,7 +452,8 @@ hipError_t launch_loss(const LossArgs& a, hipStream_t st)
     for (int64_t v0 = 0; v0 < a.V; v0 += r.piece) {
         const int64_t n = std::min(r.piece, a.V - v0), parts = (n + kPart - 1) / kPart;
         if (r.tiles) {
-            if (hipError_t e = tile_piece(t, r.t, room, rows_from(a.w, v0, a.K, a.bits, a.gs, a.dt), a.bits, a.dt, v0, n, st);
+            if (hipError_t e = tile_piece(t, r.t, room, a.x, nullptr, rows_from(a.w, v0, a.K, a.bits, a.gs, a.dt), a.bits,
+                                          a.dt, v0, n, st);
                 e != hipSuccess)
                 return e;
             continue;
@@ -568,8 +502,8 @@ hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t st)
     char* const xcopy = take(r.x);
     float* const partial = reinterpret_cast<float*>(at);
     const bool half = a.dt != DT_F32, tiles = grad_tile_sizes(r.piece, a.K, a.dt);
-    if (half) {
-        hipLaunchKernelGGL(loss_scale_kernel, dim3(1), dim3(1024), 0, st, a.dloss, a.M, a.targets, a.V, scale);
+    if (half && !r.tiles) {
+        hipLaunchKernelGGL(loss_scale_kernel, dim3(1), dim3(256), 0, st, a.dloss, a.M, a.targets, a.V, scale);
         if (hipError_t e = hipGetLastError(); e != hipSuccess)
             return e;
     }
@@ -584,15 +518,15 @@ hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t st)
         t.dz = dz;
         t.dz_stride = r.stride;
         t.lse = a.lse; t.dloss = a.dloss; t.scale = half ? scale : nullptr;
-        if (hipError_t e = tile_begin(t, r.t, room, a.x, a.dt, a.M, a.K, a.bits, a.gs, a.V, a.targets, st); e != hipSuccess)
-            return e;
+        tile_begin(t, r.t, room, a.M, a.K, a.gs, a.V, a.targets);
     }
     for (int64_t v0 = 0; v0 < a.V; v0 += r.piece) {
         const int64_t n = std::min(r.piece, a.V - v0), es = (int64_t)elem_size(a.dt);
         const QWeight w = rows_from(a.w, v0, a.K, a.bits, a.gs, a.dt);
         const int64_t stride = a.dt == DT_F32 && !r.tiles ? n : r.stride;
         if (r.tiles) {
-            if (hipError_t e = tile_piece(t, r.t, room, w, a.bits, a.dt, v0, n, st); e != hipSuccess)
+            if (hipError_t e = tile_piece(t, r.t, room, a.x, half ? scale : nullptr, w, a.bits, a.dt, v0, n, st);
+                e != hipSuccess)
                 return e;
         } else {
             if (hipError_t e = logits(xs, a.dt, a.M, a.K, a.w, a.bits, a.gs, v0, n, z, st); e != hipSuccess)

@@ -62,21 +62,16 @@ hipError_t by_rows(const LossTileArgs& a, hipStream_t st)
     return run<DT, 4, 2, G32>(a, st);
 }
 
-// One launch lays out x.
-template <int DT> hipError_t prep_x(const LossTileArgs& a, const void* x, hipStream_t st)
+template <int DT> hipError_t prep(const LossTileArgs& a, const LossPrepArgs& p, hipStream_t st)
 {
     const int units = DT == DT_F32 ? a.xn / 96 : (a.xn - 2 * a.gp) / 32;
-    const int64_t waves = (int64_t)a.M * ((units + 63) / 64), blocks = (waves + 3) / 4;
+    const int64_t waves = p.x != nullptr ? (int64_t)a.M * ((units + 63) / 64) : 0, x_blocks = (waves + 3) / 4;
+    const int64_t w_blocks = (int64_t)(a.np / 64) * ((a.gp + 63) / 64);
+    const int64_t blocks = w_blocks + x_blocks + (p.factor != nullptr ? 1 : 0);
     if (!grid_fits(blocks, 256))
         return hipErrorInvalidConfiguration;
-    uint16_t* const xp = static_cast<uint16_t*>(const_cast<void*>(a.xp));
-    if constexpr (DT == DT_F32)
-        hipLaunchKernelGGL((losstile::loss_prep_x32_kernel<QP_BITS>), dim3((unsigned)blocks), dim3(256), 0, st,
-                           static_cast<const float*>(x), (int64_t)a.M, a.K, a.gs, a.xn, a.gp, xp,
-                           static_cast<float*>(const_cast<void*>(a.xs)));
-    else
-        hipLaunchKernelGGL((losstile::loss_prep_x_kernel<QP_BITS, DT>), dim3((unsigned)blocks), dim3(256), 0, st,
-                           static_cast<const uint16_t*>(x), (int64_t)a.M, a.K, a.gs, a.xn, a.gp, xp);
+    hipLaunchKernelGGL((losstile::loss_prep_kernel<QP_BITS, DT>), dim3((unsigned)blocks), dim3(256), 0, st, a, p, w_blocks,
+                       x_blocks);
     return hipGetLastError();
 }
 
@@ -87,9 +82,9 @@ template <int DT> hipError_t tile(const LossTileArgs& a, hipStream_t st)
 
 } // namespace
 
-hipError_t QP_CAT(launch_loss_prep_x_b, QP_BITS)(int dt, const LossTileArgs& a, const void* x, hipStream_t st)
+hipError_t QP_CAT(launch_loss_prep_b, QP_BITS)(int dt, const LossTileArgs& a, const LossPrepArgs& p, hipStream_t st)
 {
-    return dt == DT_F32 ? prep_x<DT_F32>(a, x, st) : dt == DT_F16 ? prep_x<DT_F16>(a, x, st) : prep_x<DT_BF16>(a, x, st);
+    return dt == DT_F32 ? prep<DT_F32>(a, p, st) : dt == DT_F16 ? prep<DT_F16>(a, p, st) : prep<DT_BF16>(a, p, st);
 }
 
 hipError_t QP_CAT(launch_loss_tile_b, QP_BITS)(int dt, LossTileArgs a, hipStream_t st)

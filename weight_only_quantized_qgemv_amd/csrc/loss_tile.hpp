@@ -12,10 +12,10 @@
 // short contraction over the groups, with X in two 16-bit parts: exact to 2^-17 of X
 // (bf16; fp16 2^-22), G / 32 steps of 64 more.
 //
-// loss_prep_x writes x once in the order that a unit's code pairs come in, rows filled
-// up to whole 64-wide steps, and X; loss_prep_w the scales transposed (a step's scales
+// prep_x writes x once in the order that a unit's code pairs come in, rows filled
+// up to whole 64-wide steps, and X; prep_w the scales transposed (a step's scales
 // of a tile are then 512 bytes in a row) and the biases in rows of whole 16-byte
-// pieces. Both are a few microseconds beside the tiles.
+// pieces. Together a few microseconds beside the tiles.
 //
 // fp32 x is three steps of 16-bit parts, 24 bits together, so that its products are exact
 // on the same instructions, 16 times as fast as the fp32 ones.
@@ -544,14 +544,14 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
 // (+ 1) of a unit of 32 holds its code lo_code(p) (hi_code(p)). A row of 64 n + 32 features
 // ends in a unit of zeros and then its last. A wave takes 64 units of a row.
 template <int BITS, int DT>
-__global__ __launch_bounds__(256) void loss_prep_x_kernel(const uint16_t* __restrict__ x, int64_t m, int k, int gs,
-                                                          int xn, int gp, uint16_t* __restrict__ xp)
+__device__ __forceinline__ void prep_x(int64_t block, const uint16_t* __restrict__ x, int64_t m, int k, int gs, int xn,
+                                       int gp, uint16_t* __restrict__ xp)
 {
     using Order = CodeOrder<BITS>;
     using E = Elem<DT>;
     typedef u32x4_t Wide __attribute__((aligned(2)));
     const int first = 2 * gp, units = (xn - first) / 32, chunks = (units + 63) / 64, lane = (int)threadIdx.x & 63;
-    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), row = w / chunks;
+    const int64_t w = block * 4 + (threadIdx.x >> 6), row = w / chunks;
     if (row >= m)
         return;
     const int chunk = (int)(w % chunks), u = chunk * 64 + lane, n = k / 32;
@@ -610,15 +610,14 @@ __global__ __launch_bounds__(256) void loss_prep_x_kernel(const uint16_t* __rest
 // fp32 x: each 64 features are three steps, x in parts of 16 bits (what the parts before
 // leave, which is exact: 24 bits in all); X in fp32, rows of gp.
 template <int BITS>
-__global__ __launch_bounds__(256) void loss_prep_x32_kernel(const float* __restrict__ x, int64_t m, int k, int gs,
-                                                            int xn, int gp, uint16_t* __restrict__ xp,
-                                                            float* __restrict__ xs)
+__device__ __forceinline__ void prep_x32(int64_t block, const float* __restrict__ x, int64_t m, int k, int gs, int xn,
+                                         int gp, uint16_t* __restrict__ xp, float* __restrict__ xs)
 {
     using Order = CodeOrder<BITS>;
     using E = Elem<DT_BF16>;
     typedef f32x4_t Wide __attribute__((aligned(4)));
     const int units = xn / 96, chunks = (units + 63) / 64, lane = (int)threadIdx.x & 63;
-    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), row = w / chunks;
+    const int64_t w = block * 4 + (threadIdx.x >> 6), row = w / chunks;
     if (row >= m)
         return;
     const int chunk = (int)(w % chunks), u = chunk * 64 + lane, n = k / 32;
@@ -667,6 +666,54 @@ __global__ __launch_bounds__(256) void loss_prep_x32_kernel(const float* __restr
         xs[row * gp + src / per] = sum;
     if (chunk == 0 && k / gs + lane < gp)   // fewer than 8 to fill up
         xs[row * gp + k / gs + lane] = 0.0f;
+}
+
+// The scales [n, groups] transposed to [groups, np], zeros behind n, and the biases in
+// rows of gp (null: they lie so already). Tiles of 64 x 64.
+template <class E>
+__device__ __forceinline__ void prep_w(int64_t block, const E* __restrict__ scales, const E* __restrict__ biases, int64_t n,
+                                       int groups, int64_t np, int gp, E* __restrict__ st, E* __restrict__ bp)
+{
+    __shared__ E room[64][64 + 4 / sizeof(E)];
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    const int tiles_g = (gp + 63) / 64;
+    const int g0 = (int)(block % tiles_g) * 64;
+    const int64_t v0 = block / tiles_g * 64;
+    const int g = g0 + lane;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int64_t v = v0 + 4 * i + wave;
+        const bool in = v < n && g < groups;
+        room[4 * i + wave][lane] = in ? scales[v * groups + g] : (E)0;
+        if (bp != nullptr && v < n && g < gp)
+            bp[v * gp + g] = in ? biases[v * groups + g] : (E)0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (g0 + 4 * i + wave < groups)
+            st[(int64_t)(g0 + 4 * i + wave) * np + v0 + lane] = room[lane][4 * i + wave];
+}
+
+// What the tiles read, in one launch: blocks of the weight's, then of x's (with the first
+// piece), then one for the factor of dz (where it has one). Three launches of a small call
+// take 18 us (77 rows, 1024 x 50001), one 9.
+template <int BITS, int DT>
+__global__ __launch_bounds__(256) void loss_prep_kernel(LossTileArgs a, LossPrepArgs p, int64_t w_blocks, int64_t x_blocks)
+{
+    using E = typename Elem<DT>::storage;
+    const int64_t block = blockIdx.x;
+    uint16_t* const xp = static_cast<uint16_t*>(const_cast<void*>(a.xp));
+    if (block < w_blocks)
+        prep_w(block, static_cast<const E*>(p.scales), static_cast<const E*>(p.biases), (int64_t)a.N, a.K / a.gs,
+               (int64_t)a.np, a.gp, static_cast<E*>(const_cast<void*>(a.st)), static_cast<E*>(p.bp));
+    else if (block >= w_blocks + x_blocks)
+        dz_factor(a.dloss, a.M, a.targets, a.vocab, p.factor);
+    else if constexpr (DT == DT_F32)
+        prep_x32<BITS>(block - w_blocks, static_cast<const float*>(p.x), a.M, a.K, a.gs, a.xn, a.gp, xp,
+                       static_cast<float*>(const_cast<void*>(a.xs)));
+    else
+        prep_x<BITS, DT>(block - w_blocks, static_cast<const uint16_t*>(p.x), a.M, a.K, a.gs, a.xn, a.gp, xp);
 }
 
 } // namespace losstile

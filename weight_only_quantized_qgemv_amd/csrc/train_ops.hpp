@@ -81,7 +81,7 @@ struct LossTileArgs {
     const void* xp;          // [M, xn] of 16 bits: the groups' sums of x, then x (fp32: x in three parts)
     const void* xs;          // [M, gp]: the groups' sums (fp32 x)
     const uint32_t* wq;      // [N, K*bits/32]
-    const void* st;          // [K/gs, np]: the scales, transposed (loss_prep_w)
+    const void* st;          // [K/gs, np]: the scales, transposed (prep_w)
     const void* bp;          // [N, gp]: the biases
     int M, N, K, gs;
     int xn, gp, np;          // the groups filled up to 32 (fp32: 8), N to LOSS_BN; xn: 2 gp + K filled
@@ -97,9 +97,16 @@ struct LossTileArgs {
     int64_t dz_stride;
     const float *lse, *dloss, *scale;   // [M], [M], and scale[0] a factor of dloss
 };
+// What is laid out before a piece's tiles, where they read it.
+struct LossPrepArgs {
+    const void* x;           // [M, K], or null: it has been
+    const void *scales, *biases;
+    void* bp;                // null: the biases are read as they lie
+    float* factor;           // dz's factor and its inverse, or null
+};
 // Logits of up to 16 rows of 16-bit x (16-byte aligned) as fp32 y (loss_rows.hip).
 #define QP_LOSS_DECL(B)                                                                                          \
-    hipError_t launch_loss_prep_x_b##B(int dt, const LossTileArgs& a, const void* x, hipStream_t stream);       \
+    hipError_t launch_loss_prep_b##B(int dt, const LossTileArgs& a, const LossPrepArgs& p, hipStream_t stream); \
     hipError_t launch_loss_tile_b##B(int dt, LossTileArgs a, hipStream_t stream);                               \
     hipError_t launch_loss_rows_b##B(const GemvArgs& a, hipStream_t stream);
 QP_LOSS_DECL(2)
