@@ -1,12 +1,15 @@
 """A small next-byte model on packed weights: trained, then decoded.
 
-    python examples/tiny_lm.py [--steps N] [--bits B] [--seed S]
+    python examples/tiny_lm.py [--steps N] [--bits B] [--seed S] [--norms]
 
 The model is an embedding table, gated feed-forward blocks with residual
 connections and an output head, every weight packed. Training keeps the codes
 as they are and moves the scales and biases: forward (qembedding, qffn,
 qmatmul), a cross entropy, then the backward passes (qmatmul_backward,
-qffn_backward, qembedding_backward) and one Adam step over fp32 copies.
+qffn_backward, qembedding_backward) and one Adam step over fp32 copies. With
+--norms, each block's output goes through qblock_norm (the residual sum and the
+norm before the next block, its weights trained too), and the loss and its
+gradients come from qcross_entropy, without logits.
 Decoding takes one token per sequence and step: the same forward at a few rows,
 then qlogits_adjust (penalties from each sequence's own tokens, a mask of the
 bytes that may appear) and the largest logit.
@@ -29,7 +32,7 @@ VOCAB = 256
 
 class TinyLM:
     def __init__(self, bits=4, group_size=32, d_model=256, d_ff=512, layers=2, act="silu",
-                 dtype=torch.bfloat16, seed=0):
+                 dtype=torch.bfloat16, seed=0, norms=False):
         self.bits, self.gs, self.act, self.dtype = bits, group_size, act, dtype
         gen = torch.Generator(device="cuda").manual_seed(seed)
 
@@ -42,12 +45,15 @@ class TinyLM:
                        for _ in range(layers)]
         self.head = weight(VOCAB, d_model)
         self.factor = d_model ** 0.5
+        self.norms = [torch.ones(d_model, dtype=dtype, device="cuda") for _ in range(layers + 1)] if norms else []
 
     def weights(self):
         return [self.table, *(w for b in self.blocks for w in b), self.head]
 
     def forward(self, ids, keep=None):
         """Logits [tokens, VOCAB] of ids [tokens]; `keep`, a list, receives what backward() needs."""
+        if self.norms:
+            return qp.qmatmul(self.normed(ids), *self.head, self.bits, self.gs)
         x = qp.qembedding(ids, *self.table, self.bits, self.gs, self.factor)
         for block in self.blocks:
             saved = None
@@ -70,22 +76,55 @@ class TinyLM:
             dx = dx + dxb
         return [qp.qembedding_backward(ids, dx, self.table[0], self.bits, self.gs, self.factor), *grads]
 
+    def normed(self, ids, keep=None):
+        """The head's input, of a model with norms: one before each block and one before the head."""
+        s, a = qp.qblock_norm(qp.qembedding(ids, *self.table, self.bits, self.gs, self.factor), weight=self.norms[0])
+        for block, weight in zip(self.blocks, self.norms[1:]):
+            saved = None
+            if keep is not None:
+                saved = torch.empty((2, a.shape[0], block[0][0].shape[0]), dtype=a.dtype, device=a.device)
+                keep.append((s, a, saved))
+            s, a = qp.qblock_norm(s, qp.qffn(a, *block, self.bits, self.gs, self.act, saved=saved), weight)
+        if keep is not None:
+            keep.append(s)
+        return a
+
+    def loss_and_gradients(self, ids, targets):
+        """Of a model with norms: the mean loss, the gradients of weights() and of the norms."""
+        keep, q = [], (self.bits, self.gs)
+        a = self.normed(ids, keep)
+        loss, lse = qp.qcross_entropy(a, targets, *self.head, *q)
+        dloss = torch.full_like(loss, 1.0 / loss.numel())
+        da, *head = qp.qcross_entropy_backward(a, targets, lse, dloss, *self.head, *q)
+        s, ds, grads, norms = keep.pop(), None, [tuple(head)], []
+        for block, weight in zip(reversed(self.blocks), reversed(self.norms)):
+            before, a, saved = keep.pop()
+            # The residual sum hands ds on to both its terms.
+            ds, _, dw, _, _ = qp.qblock_norm_backward(s, da, ds, weight=weight)
+            da, *pairs = qp.qffn_backward(a, ds, saved, *block, *q, self.act)
+            grads, norms, s = [*pairs, *grads], [dw, *norms], before
+        ds, _, dw, _, _ = qp.qblock_norm_backward(s, da, ds, weight=self.norms[0])
+        table = qp.qembedding_backward(ids, ds, self.table[0], *q, self.factor)
+        return loss.mean(), [table, *grads], [dw, *norms]
+
 
 class Adam:
     """Adam over fp32 copies of the scales and biases; the model's own are rounded from them. A
-    step is relative to the weight's first scales: a scale of 0.02 moves codes up to 255."""
+    step is relative to the weight's first scales: a scale of 0.02 moves codes up to 255.
+    (`norms`: more tensors, of their own first size.)"""
 
-    def __init__(self, weights, lr):
+    def __init__(self, weights, lr, norms=()):
         self.t = 0
         self.lr = [lr * float(w[1].float().abs().mean()) for w in weights for _ in range(2)]
-        self.params = [t for w in weights for t in w[1:]]
+        self.lr += [lr * float(t.float().abs().mean()) for t in norms]
+        self.params = [t for w in weights for t in w[1:]] + list(norms)
         self.master = [t.float() for t in self.params]
         self.m = [torch.zeros_like(t) for t in self.master]
         self.v = [torch.zeros_like(t) for t in self.master]
 
-    def step(self, pairs):
+    def step(self, pairs, norms=()):
         self.t += 1
-        grads = [g.float() for ds in pairs for g in ds]
+        grads = [g.float() for ds in pairs for g in ds] + [g.float() for g in norms]
         for p, w, m, v, g, lr in zip(self.params, self.master, self.m, self.v, grads, self.lr):
             m.lerp_(g, 0.1)
             v.lerp_(g * g, 0.01)
@@ -97,17 +136,22 @@ def train(model, steps, batch=256, lr=1e-2, seed=1, say=lambda s: None):
     """The mean loss of each step."""
     data = torch.tensor(list(TEXT.encode()), dtype=torch.int32, device="cuda")
     gen = torch.Generator().manual_seed(seed)
-    opt = Adam(model.weights(), lr)
+    opt = Adam(model.weights(), lr, model.norms)
     losses = []
     for step in range(steps):
         at = torch.randint(0, data.numel() - 1, (batch,), generator=gen).cuda()
         ids, target = data[at], data[at + 1].long()
-        keep = []
-        logits = model.forward(ids, keep).float()
-        probs = torch.softmax(logits, 1)
-        losses.append(torch.nn.functional.cross_entropy(logits, target))
-        probs[torch.arange(batch, device="cuda"), target] -= 1
-        opt.step(model.backward(ids, keep, (probs / batch).to(model.dtype)))
+        if model.norms:
+            loss, pairs, norms = model.loss_and_gradients(ids, data[at + 1])
+            losses.append(loss)
+            opt.step(pairs, norms)
+        else:
+            keep = []
+            logits = model.forward(ids, keep).float()
+            probs = torch.softmax(logits, 1)
+            losses.append(torch.nn.functional.cross_entropy(logits, target))
+            probs[torch.arange(batch, device="cuda"), target] -= 1
+            opt.step(model.backward(ids, keep, (probs / batch).to(model.dtype)))
         if step % 20 == 0 or step == steps - 1:
             say(f"step {step}: loss {losses[-1].item():.3f}")
     return torch.stack(losses).tolist()
@@ -144,8 +188,9 @@ def main():
     ap.add_argument("--steps", type=int, default=200)
     ap.add_argument("--bits", type=int, default=4, choices=(2, 3, 4, 6, 8))
     ap.add_argument("--seed", type=int, default=0)
+    ap.add_argument("--norms", action="store_true", help="norms between the blocks, and the loss without logits")
     a = ap.parse_args()
-    model = TinyLM(bits=a.bits, seed=a.seed)
+    model = TinyLM(bits=a.bits, seed=a.seed, norms=a.norms)
     train(model, a.steps, say=lambda s: print(s, flush=True))
     for line in decode(model, ["the c", "a rou", "step "], 24, "abcdefghijklmnopqrstuvwxyz .,"):
         print(repr(line))
