@@ -512,7 +512,8 @@ qp_status qlogits_adjust(const void* logits, qp_dtype dtype, int64_t rows, int64
  *            loss is 0, and it has no gradient
  *   wq, scales, biases  device, the head [vocab, k] as in qmatmul
  *   loss, lse  device, fp32 [m] (outputs)
- *   workspace device, >= qcross_entropy_workspace_bytes(...), 16-byte aligned
+ *   workspace device, >= qcross_entropy_workspace_bytes(...), 16-byte aligned; a
+ *            call's own until it has run (so for each captured graph)
  * The logits are formed and reduced in fp32, in pieces of the vocabulary;
  * nothing of them is rounded to 16 bits. vocab == 0: lse is -infinity. A row of x
  * with an infinity or a NaN gives NaN in its own row. Deterministic.
@@ -536,7 +537,8 @@ qp_status qcross_entropy(const void* x, qp_dtype x_dtype, int64_t m, int64_t k, 
  *   workspace device, >= qcross_entropy_backward_workspace_bytes(...), 16-byte aligned
  * The logits are formed again, a piece of the vocabulary at a time. dz is rounded
  * to x_dtype as the products' operand (16-bit types: times a factor that makes the
- * largest |dloss| 2^14, taken out of the sums again); everything else is fp32. Rows of x must be finite where there is no target too.
+ * largest |dloss| 2^14, taken out of the sums again); everything else is fp32. Rows
+ * of x must be finite where there is no target too.
  * Deterministic. m == 0 or vocab == 0 writes zeros.
  */
 size_t qcross_entropy_backward_workspace_bytes(int64_t m, int64_t k, int64_t vocab, int32_t bits,

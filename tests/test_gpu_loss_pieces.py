@@ -27,13 +27,16 @@ def test_pieces(m, k, v, bits, gs, dt):
     run_and_check(m, k, v, bits, gs, dt, "pieces")
 
 
-@pytest.mark.parametrize("m,dt", [(20, BF16), (20, F32), (130, F16), (5, BF16)])
-def test_the_widest_head(m, dt):
-    """2^18 features, 33068 tokens, 2 bits: 2.2 GB of codes, pieces of 16384 tokens. x has a few
-    features in each row's step that are not 0, so that the 64-bit form needs only these: a
-    product with 0 adds exactly nothing, and the sums' roundings are those of the others."""
-    k, v, bits, gs = 1 << 18, 33068, 2, 32
-    log(f"widest head: m={m} dt={dt}")
+@pytest.mark.parametrize("m,k,v,dt", [
+    (20, 1 << 18, 33068, BF16), (20, 1 << 18, 33068, F32), (130, 1 << 18, 33068, F16), (5, 1 << 18, 33068, BF16),
+    (20, (1 << 18) + 32, 300, BF16), (3, (1 << 18) + 32, 300, F32)])
+def test_the_widest_heads(m, k, v, dt):
+    """2^18 features, 33068 tokens, 2 bits: 2.2 GB of codes, pieces of 16384 tokens; and the first
+    width past the tiles'. x has a few features that are not 0, so that the 64-bit form needs
+    only these: a product with 0 adds exactly nothing, and the sums' roundings are those of
+    the others."""
+    bits, gs = 2, 32
+    log(f"widest head: m={m} k={k} dt={dt}")
     g = torch.Generator(device="cuda").manual_seed(m + dt)
     wq = torch.randint(-2 ** 31, 2 ** 31, (v, k * bits // 32), generator=g, device=dev(), dtype=torch.int32)
     s = ((torch.rand((v, k // gs), generator=g, device=dev()) + 0.5) * 0.25).to(TORCH_DT[dt])
@@ -88,3 +91,30 @@ def test_the_widest_head(m, dt):
         oh.check(got[:, cols], ref, 1.01 * sums(e, xd.abs()) + gam * sums(dz.abs(), xd.abs()) + oh.half_ulp(ref, dt), name)
         got[:, cols] = 0
         assert not got.any(), name
+
+
+def test_the_most_rows():
+    """2^20 rows and more tokens than one launch of tiles takes. The rows are 64 patterns, so the
+    64-bit form has 64 rows of logits."""
+    if torch.cuda.get_device_properties(0).total_memory < 60 * 2 ** 30:
+        pytest.skip("needs 60 GiB of GPU memory")
+    m, k, v, bits, gs = 1 << 20, 64, (1 << 19) + 5, 2, 64
+    log(f"most rows: {m}")
+    g = oh.rng(9)
+    pattern = oh.normal((64, k), 2.0, BF16, g)
+    w = oh.weight(v, k, bits, gs, BF16, g)
+    W = oh.dense(w, bits, gs).to(dev())
+    mags = (oh.codes(w[0], bits) * oh.spread(w[1], gs).abs() + oh.spread(w[2], gs).abs()).to(dev())
+    pd = pattern.to(dev()).double()
+    which = torch.arange(m, device=dev()) * 37 % 64
+    t = (torch.arange(m, device=dev()) * 7919 % v).to(torch.int32)
+    loss, lse = qp.qcross_entropy(pattern.to(dev())[which], t, *oh.cuda(w), bits, gs)
+    torch.cuda.synchronize()
+    per = (k + 2 + 64) * 2.0 ** -24 + 2.0 ** -17
+    r_lse = torch.logsumexp(pd @ W.t(), 1)
+    b_lse = per * (pd.abs() @ mags.t()).max(1).values + 2.0 ** -16 + 2.0 ** -22 * r_lse.abs()
+    at = t.long()
+    r_loss = r_lse[which] - (pd[which] * W[at]).sum(1)
+    b_loss = b_lse[which] + per * (pd[which].abs() * mags[at]).sum(1) + 2.0 ** -23 * (r_loss.abs() + r_lse[which].abs())
+    oh.check(lse, r_lse[which].cpu(), b_lse[which].cpu(), "lse")
+    oh.check(loss, r_loss.cpu(), b_loss.cpu(), "loss")

@@ -325,11 +325,13 @@ hipError_t tile_piece(LossTileArgs& t, const TileRoom& r, char* room, const void
         return e;
     return tile_kernel(bits, dt, t, st);
 }
-// Vocabulary of a piece: scales of up to 2^29 bytes, whole tiles, and (backward) dz of
-// about 128 MB, but not less than 2048 tokens.
+// Vocabulary of a piece: scales of up to 2^29 bytes, whole tiles, fewer than 2^31 threads
+// (256 for 32 rows of 256 tokens at most), and (backward) dz of about 128 MB, but not
+// less than 2048 tokens.
 int64_t tile_piece_of(int64_t m, int64_t k, int64_t v, int gs, bool grad)
 {
-    int64_t most = std::max<int64_t>((int64_t(1) << 27) / (k / gs) / LOSS_BN * LOSS_BN, LOSS_BN);
+    int64_t most = std::min((int64_t(1) << 27) / (k / gs), (int64_t(1) << 36) / m);
+    most = std::max<int64_t>(most / LOSS_BN * LOSS_BN, LOSS_BN);
     if (grad)
         most = std::min(most, std::max<int64_t>((int64_t(1) << 26) / m / LOSS_BN * LOSS_BN, 2048));
     return std::min(most, v);
