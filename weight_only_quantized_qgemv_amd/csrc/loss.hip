@@ -62,30 +62,42 @@ __global__ __launch_bounds__(256) void loss_parts_kernel(const float* __restrict
         picked[row] = p[t - v0];
 }
 
-// The rows' losses from their parts: 64 rows a block, 16 waves a share of the parts
-// each.
+// The rows' losses from their parts: 16 rows a block, 64 threads a row, each a share of
+// the parts, four of them on their way at a time.
 __global__ __launch_bounds__(1024) void loss_finish_kernel(const Stat* __restrict__ stats, int64_t parts, int64_t m,
                                                            int64_t vocab, const int32_t* __restrict__ targets,
                                                            const float* __restrict__ picked, float* __restrict__ loss,
                                                            float* __restrict__ lse)
 {
     __shared__ Stat room[16][64];
-    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    const int64_t row = (int64_t)blockIdx.x * 64 + lane;
+    const int tid = (int)threadIdx.x, share = tid >> 4;
+    const int64_t row = (int64_t)blockIdx.x * 16 + (tid & 15), at = row < m ? row : m - 1;
     Stat s{-__builtin_inff(), 0.0f};
-    if (row < m)
-        for (int64_t i = wave; i < parts; i += 16)
-            s = join_stats(s, stats[i * m + row]);
-    room[wave][lane] = s;
+    for (int64_t i = share; i < parts; i += 256) {
+        Stat p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t part = i + 64 * j;
+            p[j] = stats[(part < parts ? part : i) * m + at];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + 64 * j < parts)
+                s = join_stats(s, p[j]);
+    }
+    room[tid & 15][share] = s;
     __syncthreads();
-    if (wave != 0 || row >= m)
+    // A wave a row.
+    const int64_t out = (int64_t)blockIdx.x * 16 + (tid >> 6);
+    if (out >= m)
         return;
-    for (int w = 1; w < 16; ++w)
-        s = join_stats(s, room[w][lane]);
-    const float l = s.top + logf(s.sum);
-    const int32_t t = targets[row];
-    lse[row] = l;
-    loss[row] = t >= 0 && t < vocab ? l - picked[row] : 0.0f;
+    s = wave_stat(room[tid >> 6][tid & 63]);
+    const int32_t t = targets[out];
+    const float l = s.top + logf(s.sum), z = picked[out];
+    if ((tid & 63) == 0) {
+        lse[out] = l;
+        loss[out] = t >= 0 && t < vocab ? l - z : 0.0f;
+    }
 }
 
 // The losses of few rows, a block each, from all their logits at once: 32 a thread at a
@@ -471,7 +483,7 @@ hipError_t launch_loss(const LossArgs& a, hipStream_t st)
         if (hipError_t e = hipGetLastError(); e != hipSuccess)
             return e;
     }
-    hipLaunchKernelGGL(loss_finish_kernel, dim3((unsigned)((a.M + 63) / 64)), dim3(1024), 0, st, stats, r.parts, a.M,
+    hipLaunchKernelGGL(loss_finish_kernel, dim3((unsigned)((a.M + 15) / 16)), dim3(1024), 0, st, stats, r.parts, a.M,
                        a.V, a.targets, picked, a.loss, a.lse);
     return hipGetLastError();
 }

@@ -680,13 +680,20 @@ __device__ __forceinline__ void prep_w(int64_t block, const E* __restrict__ scal
     const int g0 = (int)(block % tiles_g) * 64;
     const int64_t v0 = block / tiles_g * 64;
     const int g = g0 + lane;
+    // (All the loads first, with their indexes held inside and no branch around them.)
+    E s[16], b[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int64_t v = v0 + 4 * i + wave, at = (v < n ? v : n - 1) * groups + (g < groups ? g : groups - 1);
+        s[i] = scales[at];
+        b[i] = biases[at];
+    }
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const int64_t v = v0 + 4 * i + wave;
-        const bool in = v < n && g < groups;
-        room[4 * i + wave][lane] = in ? scales[v * groups + g] : (E)0;
+        room[4 * i + wave][lane] = v < n && g < groups ? s[i] : (E)0;
         if (bp != nullptr && v < n && g < gp)
-            bp[v * gp + g] = in ? biases[v * groups + g] : (E)0;
+            bp[v * gp + g] = g < groups ? b[i] : (E)0;
     }
     __syncthreads();
 #pragma unroll
