@@ -20,6 +20,12 @@
 // fp32 x is three steps of 16-bit parts, 24 bits together, so that its products are exact
 // on the same instructions, 16 times as fast as the fp32 ones.
 //
+// 4096 rows of 4096 x 32000, 4-bit bf16: 1000 us with its layout and close, 1.07 PFLOP/s
+// where a large library product of 16-bit weights reaches 1.36. It is bound by the vector
+// units beside the matrix pipes, and by power: of 1.93 million cycles (1.74 GHz) the
+// matrix pipes are busy in 55%, and 7 vector instructions stand beside each matrix
+// instruction of 32 cycles, 4 of them the scaling.
+//
 // Waves of 32 FM rows x 64 columns, WMW x 4 of them; steps of 64 k; x in NA and codes
 // and scales in NC stages of LDS, by DMA, with the swizzles of gemm_core.hpp.
 #pragma once
@@ -704,7 +710,7 @@ __device__ __forceinline__ void prep_w(int64_t block, const E* __restrict__ scal
 
 // What the tiles read, in one launch: blocks of the weight's, then of x's (with the first
 // piece), then one for the factor of dz (where it has one). Three launches of a small call
-// take 18 us (77 rows, 1024 x 50001), one 9.
+// take 18 us (77 rows, 1024 x 50001), one 6.
 template <int BITS, int DT>
 __global__ __launch_bounds__(256) void loss_prep_kernel(LossTileArgs a, LossPrepArgs p, int64_t w_blocks, int64_t x_blocks)
 {

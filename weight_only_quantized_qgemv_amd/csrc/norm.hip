@@ -230,13 +230,20 @@ struct NormSplit {
 };
 // Threads of a row in the backward pass, and so many blocks as the GPU holds at once
 // (two waves a SIMD): 8192 rows of 4096, bf16, 98 us, with twice as many 103; 4096
-// rows of 2048 34.1 us on 512 blocks of 256 threads, 38.8 on 256.
+// rows of 2048 34.1 us on 512 blocks of 256 threads, 38.8 on 256, and in another run
+// 37.5 and, on 768, 39.7. Of as many rounds the fewest blocks (600 rows of 1027 on 300
+// blocks 17.6 us, on 512 17.9: less to join).
 int norm_threads(int64_t d) { return d <= 512 ? 64 : d <= 1024 ? 128 : d <= 2048 ? 256 : 512; }
 NormSplit norm_split(int64_t m, int64_t d, int64_t gates)
 {
     const int64_t blocks = 256 * (512 / norm_threads(d));
-    const int64_t g = std::max<int64_t>(gates, 1), groups = std::min(g, blocks);
-    return {groups, std::clamp<int64_t>(blocks / groups, 1, std::max<int64_t>(m / g, 1))};
+    auto even = [](int64_t n, int64_t most) {   // the fewest blocks that are as many rounds
+        const int64_t rounds = (n + most - 1) / most;
+        return (n + rounds - 1) / rounds;
+    };
+    const int64_t g = std::max<int64_t>(gates, 1), groups = even(g, std::min(g, blocks));
+    const int64_t per = std::max<int64_t>(m / g, 1);
+    return {groups, even(per, std::clamp<int64_t>(blocks / groups, 1, per))};
 }
 
 // Rows of up to 8192: the row, the weights and the block's column sums stay in
@@ -402,7 +409,8 @@ __global__ __launch_bounds__(ROWT, 2) void norm_grad_kernel(NormGradArgs a, int6
 
 // Wider rows: read again for each of the three passes over a row (from L2), a chunk at
 // a time, the column sums in the block's own part of the workspace, where each thread
-// reads and writes the columns that are its own. 2048 rows of 16384, bf16: 300 us.
+// reads and writes the columns that are its own. 2048 rows of 16384, bf16: 310 us; the
+// sums' way through the workspace is 0.8 GB, twice the tensors.
 template <int DT, int SDT>
 __global__ __launch_bounds__(512) void norm_grad_wide_kernel(NormGradArgs a, int64_t groups, int64_t parts)
 {
