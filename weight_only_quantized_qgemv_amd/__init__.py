@@ -515,7 +515,7 @@ def _check_packed(w, like, name, n, k, bits, group_size):
 def _workspace(nbytes, like, workspace):
     import torch
     if workspace is None:
-        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=like.device)
+        return like.new_empty(max(nbytes, 1), dtype=torch.uint8)
     return _like(workspace, like, "workspace")
 
 
@@ -836,7 +836,7 @@ def qblock_norm(x, y=None, weight=None, post_weight=None, gate=None, scale: floa
         if out is not None:
             raise ValueError("out: without weight there is none")
     elif out is None:
-        out = torch.empty((m, d), dtype=dt, device=x.device)
+        out = torch.empty_like(y) if y is not None else torch.empty_like(x, dtype=dt)
     else:
         _like(out, x, "out", (m, d), dt)
     check(lib().qblock_norm(_ptr(x), dtype_code(x.dtype), m, d, _opt(y), dtype_code(dt), _opt(weight),
