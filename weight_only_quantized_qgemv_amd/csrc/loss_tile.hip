@@ -32,9 +32,9 @@ hipError_t run(LossTileArgs a, hipStream_t st)
 // The rows of a tile, by an estimate of what a step costs, in us: 32 and 64 rows are two
 // blocks a CU once there are more tiles than CUs, the others one. Rounds of the GPU count
 // half as whole ones, half as tiles (a round's blocks do not end together). Measured,
-// 4096 features, 32000 tokens, 4-bit bf16, tiles of 32 / 64 / 128 / 256 rows: 24 rows 55, 65,
-// 86, 120 us; 64 rows 57, 66, 87, 120; 100 rows 83, 75, 89, 122; 200 rows 137, 109, 100,
-// 130; 500 rows 257, 199, 188, 168; 1000 rows 474, 351, 335, 294.
+// 4096 features, 32000 tokens, 4-bit bf16, tiles of 32 / 64 / 128 / 256 rows: 24 rows 37, 48,
+// 71, 104 us; 64 rows 39, 49, 72, 106; 100 rows 63, 53, 73, 106; 200 rows 114, 83, 80,
+// 112; 500 rows 242, 165, 159, 135; 1000 rows 508, 352, 337, 263.
 template <int DT, bool G32>
 hipError_t by_rows(const LossTileArgs& a, hipStream_t st)
 {
@@ -42,7 +42,7 @@ hipError_t by_rows(const LossTileArgs& a, hipStream_t st)
         int64_t rows, resident;
         double few, step;   // a step's us with a tile a CU or fewer, with all resident
     };
-    constexpr Tile kTiles[] = {{32, 512, 0.64, 1.0}, {64, 512, 0.9, 1.41}, {128, 256, 1.29, 1.29}, {256, 256, 2.1, 2.1}};
+    constexpr Tile kTiles[] = {{32, 512, 0.52, 0.97}, {64, 512, 0.76, 1.33}, {128, 256, 1.2, 1.29}, {256, 256, 2.1, 2.1}};
     const int64_t tiles_n = (a.N + LOSS_BN - 1) / LOSS_BN;
     int64_t rows = 0;
     double best = 0.0;

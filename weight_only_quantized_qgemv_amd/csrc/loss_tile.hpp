@@ -50,8 +50,6 @@ using gemm::swz;
 using gemm::waitcnt_vm_lgkm0;
 
 constexpr uint32_t OOB = 0x80000000u;
-constexpr int NA = 3;
-template <int BITS> constexpr int NC = BITS >= 6 ? 3 : 4;
 
 // e^x for the closes: 2^-24 (1 + |x|) of itself, half the instructions of expf.
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
@@ -82,11 +80,24 @@ template <int DT, int WMW, bool G32> struct ScaleStage {
     static constexpr int INSTR = (PIECES + WAVES - 1) / WAVES, STAGE = INSTR * WAVES * 256;
 };
 
-// Stages of the products, and then of the close.
+// Stages of x and of the codes and scales. Three of x, and four of the codes up to 4 bits;
+// tiles of 32 and 64 rows, whose steps are short beside a memory latency, as many of both
+// as leave room for two blocks a CU (24 rows of 4096 x 32000, 4-bit, 125 tiles: 0.64 us a
+// step with three and four, 0.52 with six; 64-row tiles of 100 rows and 131072 tokens 184
+// us and, with four of each, 171; with eight and one block a CU 214).
+template <int BITS, int DT, int FM, int WMW, bool G32> struct Depth {
+    static constexpr int A = 32 * FM * WMW * 128;
+    static constexpr int C = CodeStage<BITS, LOSS_BN, 4 * WMW>::STAGE + ScaleStage<DT, WMW, G32>::STAGE;
+    static constexpr int MOST = 80 * 1024 / (A + C), EVEN = MOST < 3 ? 3 : MOST > 8 ? 8 : MOST;
+    static constexpr int NA = FM <= 2 ? EVEN : 3;
+    static constexpr int NC = FM <= 2 ? EVEN : BITS >= 6 ? 3 : 4;
+    static constexpr int BYTES = NA * A + NC * C;
+};
+
+// LDS of the products, and then of the close.
 template <int BITS, int DT, int FM, int WMW, bool G32> constexpr int lds_bytes()
 {
-    constexpr int steps = NA * 32 * FM * WMW * 128 + NC<BITS> * (CodeStage<BITS, LOSS_BN, 4 * WMW>::STAGE +
-                                                                 ScaleStage<DT, WMW, G32>::STAGE);
+    constexpr int steps = Depth<BITS, DT, FM, WMW, G32>::BYTES;
     constexpr int close = 4 * WMW * 32 * 68 * 4 + 4 * 32 * FM * WMW * (int)sizeof(Stat);
     return steps > close ? steps : close;
 }
@@ -119,11 +130,11 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
     static_assert(A_INSTR * 1024 * WAVES == A_STAGE, "whole DMA blocks");
     constexpr int C_INSTR = CodeStage<BITS, BN, WAVES>::INSTR, C_STAGE = CodeStage<BITS, BN, WAVES>::STAGE;
     constexpr int SB_STAGE = SS::STAGE, S_INSTR = SS::INSTR, ES = (int)sizeof(St);
-    constexpr int NCS = NC<BITS>;
-    // As in gemm_core.hpp: step kt + 1 reads the activations and codes of kt + 2 at
-    // its end; what was issued after them may be in flight when step kt ends.
-    constexpr int IN_FLIGHT = NCS > NA ? C_INSTR + S_INSTR : 0;
-    static_assert(NA == 3 && (NCS == 3 || NCS == 4), "prefetch depth");
+    constexpr int NA = Depth<BITS, DT, FM, WMW, G32>::NA, NCS = Depth<BITS, DT, FM, WMW, G32>::NC;
+    // Step kt + 1 reads the activations and codes of kt + 2 at its end, so those have
+    // landed when step kt ends; what was issued for later steps may be in flight.
+    constexpr int IN_FLIGHT = (NA - 3) * (A_INSTR + C_INSTR + S_INSTR) + (NCS > NA ? C_INSTR + S_INSTR : 0);
+    static_assert(NA >= 3 && (NCS == NA || NCS == NA + 1) && IN_FLIGHT < 64, "prefetch depth");
     extern __shared__ __attribute__((aligned(16))) char lds[];
     char* const a_st = lds;
     char* const c_st = a_st + NA * A_STAGE;
@@ -172,11 +183,12 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
 
     // DMA operation o of step kt's: A_INSTR of the activations, C_INSTR of the codes, the
     // scales. A row's place in the step goes into the scalar offset, which is not range
-    // checked: rows past the tile are past the range by their own, and the activations'
-    // last steps read on into the workspace behind them.
+    // checked: rows past the tile are past the range by their own, and what is asked for
+    // past the last step is the last step again.
+    const int last_a = BT + KT - 1;
     auto dma_a = [&](int kt, int stage, int i) {
         dma16_at(rx, a_st + stage * A_STAGE + (wave * A_INSTR + i) * 1024, (a_goff ^ (i % 2 ? 64u : 0u)) + (uint32_t)(8 * i) * xrow,
-                 kt * BK * 2);
+                 (kt < last_a ? kt : last_a) * BK * 2);
     };
     auto dma_c = [&](int kt, int stage, int i) {
         // The last step of 64 n + 32 features holds the row's last two units; the biases'
