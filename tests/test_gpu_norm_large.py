@@ -7,9 +7,20 @@ import torch
 
 import weight_only_quantized_qgemv_amd as qp
 import ophelpers as oh
-from qhelpers import BF16, dev, log
+from qhelpers import BF16, F16, F32, dev, log
+from test_gpu_norm import Case, run_and_check
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("m,d,dt,sdt,post,gates,pre,y", [
+    (700, 8200, BF16, BF16, True, 1, True, True), (700, 8208, F16, F32, True, 2, True, True),
+    (1100, 8193, F32, F32, True, 1, True, True), (520, 16384, BF16, F32, False, 1, True, True),
+    (800, 8200, BF16, BF16, False, 0, True, True), (800, 8200, BF16, BF16, False, 0, True, False),
+    (800, 8200, BF16, F32, True, 4, False, True), (258, 8200, F16, F16, True, 129, True, True)])
+def test_wide_rows_several_to_a_block(m, d, dt, sdt, post, gates, pre, y):
+    """Three rows at a time, of which the last group has one, two or three."""
+    run_and_check(Case(m, d, dt, sdt, post, gates, pre, y=y), "wide")
 
 
 @pytest.mark.parametrize("m,d", [((1 << 20) + 3, 4096), ((1 << 17) + 5, 16384)])

@@ -409,12 +409,12 @@ __global__ __launch_bounds__(ROWT, 2) void norm_grad_kernel(NormGradArgs a, int6
 
 // Wider rows: read again for each of the three passes over a row (from L2), a chunk at
 // a time, the column sums in the block's own part of the workspace, where each thread
-// reads and writes the columns that are its own. 2048 rows of 16384, bf16: 310 us; the
-// sums' way through the workspace is 0.8 GB, twice the tensors.
+// reads and writes the columns that are its own, once for three rows. 2048 rows of
+// 16384, bf16: 232 us; with every row, 0.8 GB of sums' way through the workspace, 310.
 template <int DT, int SDT>
 __global__ __launch_bounds__(512) void norm_grad_wide_kernel(NormGradArgs a, int64_t groups, int64_t parts)
 {
-    constexpr int T = 512;
+    constexpr int T = 512, R = 3;
     __shared__ float room[2][3][16];
     int turn = 0;
     const int n = (int)a.D, lane = (int)threadIdx.x, chunks = (n + 7) / 8;
@@ -438,32 +438,47 @@ __global__ __launch_bounds__(512) void norm_grad_wide_kernel(NormGradArgs a, int
     };
     for (int64_t g = block / parts; g < gates; g += groups) {
         first[2] = true;
-        for (int64_t row = g * per + p; row < (g + 1) * per; row += parts) {
-            const int64_t at = row * a.D;
-            float q[3] = {0.0f, 0.0f, 0.0f};   // s s, u s, y y
-            for (int c = lane; c < chunks; c += T) {
-                if (pre) {
-                    const Pack<SDT> s = load8<SDT>(a.s, at, c, n);
-                    const Pack<DT> da = load8<DT>(a.da, at, c, n), w = load8<DT>(a.weight, 0, c, n);
+        const int64_t end = (g + 1) * per;
+        for (int64_t row = g * per + p; row < end; row += R * parts) {
+            float rs[R], ks[R], ry[R], z[R];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        q[0] = __builtin_fmaf(s[i], s[i], q[0]);
-                        q[1] = __builtin_fmaf(da[i] * (w[i] + a.offset), s[i], q[1]);
+            for (int r = 0; r < R; ++r) {
+                rs[r] = ks[r] = z[r] = 0.0f;
+                ry[r] = 1.0f;
+                const int64_t at = (row + r * parts) * a.D;
+                if (row + r * parts >= end)   // (the same for the whole block)
+                    continue;
+                float q[3] = {0.0f, 0.0f, 0.0f};   // s s, u s, y y
+                for (int c = lane; c < chunks; c += T) {
+                    if (pre) {
+                        const Pack<SDT> s = load8<SDT>(a.s, at, c, n);
+                        const Pack<DT> da = load8<DT>(a.da, at, c, n), w = load8<DT>(a.weight, 0, c, n);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            q[0] = __builtin_fmaf(s[i], s[i], q[0]);
+                            q[1] = __builtin_fmaf(da[i] * (w[i] + a.offset), s[i], q[1]);
+                        }
+                    }
+                    if (post) {
+                        const Pack<DT> y = load8<DT>(a.y, at, c, n);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            q[2] = __builtin_fmaf(y[i], y[i], q[2]);
                     }
                 }
-                if (post) {
-                    const Pack<DT> y = load8<DT>(a.y, at, c, n);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        q[2] = __builtin_fmaf(y[i], y[i], q[2]);
+                row_sums<3, T>(q, room, turn);
+                if (pre) {
+                    rs[r] = 1.0f / sqrtf(q[0] / (float)n + a.eps);
+                    ks[r] = rs[r] * rs[r] * rs[r] * (q[1] / (float)n);
                 }
+                if (post)
+                    ry[r] = 1.0f / sqrtf(q[2] / (float)n + a.eps);
             }
-            row_sums<3, T>(q, room, turn);
-            const float rs = pre ? 1.0f / sqrtf(q[0] / (float)n + a.eps) : 0.0f, ks = rs * rs * rs * (q[1] / (float)n);
-            const float ry = post ? 1.0f / sqrtf(q[2] / (float)n + a.eps) : 1.0f;
-            // v (or q) of a chunk; with `sums`, what is summed and stored on the way to it.
-            float z[1] = {0.0f};
-            auto through = [&](int c, bool sums, const Pack<DT>& y, float (&G)[8]) {
+            // v (or q) of row r's chunk c; with `sums`, what is summed on the way to it goes
+            // to d. dx may be ds, and dy da or y: they are written when nothing of the chunk
+            // is read any more.
+            auto through = [&](int r, int c, bool sums, const Pack<DT>& y, float (&G)[8], float (&d)[3][8]) {
+                const int64_t at = (row + r * parts) * a.D;
                 if (a.ds != nullptr) {
                     const Pack<SDT> ds = load8<SDT>(a.ds, at, c, n);
 #pragma unroll
@@ -474,79 +489,83 @@ __global__ __launch_bounds__(512) void norm_grad_wide_kernel(NormGradArgs a, int
                     for (int i = 0; i < 8; ++i)
                         G[i] = 0.0f;
                 }
-                float d[8];
                 if (pre) {
                     const Pack<SDT> s = load8<SDT>(a.s, at, c, n);
                     const Pack<DT> da = load8<DT>(a.da, at, c, n), w = load8<DT>(a.weight, 0, c, n);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        d[i] = da[i] * s[i] * rs;
-                        G[i] += rs * (da[i] * (w[i] + a.offset)) - s[i] * ks;
+                        d[0][i] = __builtin_fmaf(da[i] * s[i], rs[r], d[0][i]);
+                        G[i] += rs[r] * (da[i] * (w[i] + a.offset)) - s[i] * ks[r];
                     }
-                    if (sums)
-                        add(0, c, d);
                 }
-                if (!whole) {
+                if (!sums || !post)
                     store8<SDT>(a.dx, at, c, n, G);
+                if (!whole)
                     return;
-                }
-                float x[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] = G[i];
+                for (int i = 0; i < 8; ++i)
                     G[i] *= a.factor;
-                }
                 const Pack<DT> w = post ? load8<DT>(a.post, 0, c, n) : Pack<DT>{};
                 if (gated) {
                     const Pack<DT> gate = load8<DT>(a.gate, g * a.D, c, n);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float t = post ? y[i] * (ry * (w[i] + a.offset)) : y[i];
-                        d[i] = t * G[i];
+                        const float t = post ? y[i] * (ry[r] * (w[i] + a.offset)) : y[i];
+                        d[2][i] = __builtin_fmaf(t, G[i], d[2][i]);
                         G[i] *= gate[i];
                     }
-                    if (sums)
-                        add(2, c, d);
                 }
                 if (post) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        d[i] = G[i] * y[i] * ry;
+                        d[1][i] = __builtin_fmaf(G[i] * y[i], ry[r], d[1][i]);
                         G[i] *= w[i] + a.offset;
                     }
-                    if (sums)
-                        add(1, c, d);
                 }
-                // dx may be ds, and dy da or y: they are written when nothing of the chunk is
-                // read any more.
-                if (!sums || !post)
-                    store8<SDT>(a.dx, at, c, n, x);
+            };
+            // A pass over the rows' chunks; the columns' sums of all R rows go out together.
+            auto pass = [&](bool sums, auto close) {
+                for (int c = lane; c < chunks; c += T) {
+                    float d[3][8] = {};
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const int64_t at = (row + r * parts) * a.D;
+                        if (row + r * parts >= end)
+                            continue;
+                        const Pack<DT> y = whole ? load8<DT>(a.y, at, c, n) : Pack<DT>{};
+                        float G[8];
+                        through(r, c, sums, y, G, d);
+                        close(r, c, at, y, G);
+                    }
+                    if (sums) {
+                        if (pre)
+                            add(0, c, d[0]);
+                        if (post)
+                            add(1, c, d[1]);
+                        if (gated)
+                            add(2, c, d[2]);
+                    }
+                }
             };
             if (post) {
-                for (int c = lane; c < chunks; c += T) {
-                    const Pack<DT> y = load8<DT>(a.y, at, c, n);
-                    float G[8];
-                    through(c, true, y, G);
+                pass(true, [&](int r, int, int64_t, const Pack<DT>& y, const float (&G)[8]) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        z[0] = __builtin_fmaf(G[i], y[i], z[0]);
-                }
-                row_sums<1, T>(z, room, turn);
+                        z[r] = __builtin_fmaf(G[i], y[i], z[r]);
+                });
+                row_sums<R, T>(z, room, turn);
             }
-            const float kz = ry * ry * ry * (z[0] / (float)n);
-            for (int c = lane; c < chunks; c += T) {
-                const Pack<DT> y = whole ? load8<DT>(a.y, at, c, n) : Pack<DT>{};
-                float G[8];
-                through(c, !post, y, G);
+            pass(!post, [&](int r, int c, int64_t at, const Pack<DT>& y, float (&G)[8]) {
                 if (!whole)
-                    continue;
+                    return;
                 if (post) {
+                    const float kz = ry[r] * ry[r] * ry[r] * (z[r] / (float)n);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        G[i] = ry * G[i] - y[i] * kz;
+                        G[i] = ry[r] * G[i] - y[i] * kz;
                 }
                 store8<DT>(a.dy, at, c, n, G);
-            }
+            });
             first[0] = first[1] = first[2] = false;
         }
         if (gated && parts == 1) {
