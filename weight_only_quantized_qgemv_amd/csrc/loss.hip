@@ -135,14 +135,14 @@ __global__ __launch_bounds__(1024) void loss_rows_kernel(const float* __restrict
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 top = fmaxf(top, t[i][j]);
-        if (top == -__builtin_inff())
-            top = 0.0f;   // nothing yet: sums of 0
-        float sum = s.sum * expf(s.top - top);
+        // A thread without any logit keeps -infinity: the row's maximum is of logits alone.
+        const float at = top == -__builtin_inff() ? 0.0f : top;   // nothing yet: sums of 0
+        float sum = s.sum * expf(s.top - at);
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                sum += expf(t[i][j] - top);
+                sum += expf(t[i][j] - at);
         s = Stat{top, sum};
     };
     fetch(0, v[0]);
