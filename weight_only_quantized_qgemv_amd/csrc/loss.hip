@@ -302,7 +302,8 @@ TileRoom tile_room(int64_t m, int64_t k, int64_t piece, int gs, int dt)
     const size_t es = elem_size(dt);
     const int64_t fill = f32 ? 8 : 32, gp = (k / gs + fill - 1) / fill * fill, kp = (k + 63) / 64 * 64;
     const int64_t xn = f32 ? 3 * kp : 2 * gp + kp, np = (piece + LOSS_BN - 1) / LOSS_BN * LOSS_BN;
-    return {xn, gp, up16((size_t)m * (size_t)xn * 2), f32 ? up16((size_t)m * (size_t)gp * 4) : 0,
+    return {xn, gp, up16((size_t)m * (size_t)xn * 2),
+            f32 ? up16((size_t)m * (size_t)gp * 4) : dt == DT_F16 ? up16((size_t)m * 4) : 0,
             up16((size_t)(k / gs) * (size_t)np * es), up16((size_t)piece * (size_t)gp * es)};
 }
 // The kernel's arguments that all pieces share: x is laid out at `room`, the weight's

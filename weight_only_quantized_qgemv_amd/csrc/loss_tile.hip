@@ -65,7 +65,7 @@ hipError_t by_rows(const LossTileArgs& a, hipStream_t st)
 template <int DT> hipError_t prep(const LossTileArgs& a, const LossPrepArgs& p, hipStream_t st)
 {
     const int units = DT == DT_F32 ? a.xn / 96 : (a.xn - 2 * a.gp) / 32;
-    const int64_t waves = p.x != nullptr ? (int64_t)a.M * ((units + 63) / 64) : 0, x_blocks = (waves + 3) / 4;
+    const int64_t waves = p.x != nullptr ? (int64_t)a.M * losstile::prep_waves(DT, (units + 63) / 64) : 0, x_blocks = (waves + 3) / 4;
     const int64_t w_blocks = (int64_t)(a.np / 64) * ((a.gp + 63) / 64);
     const int64_t blocks = w_blocks + x_blocks + (p.factor != nullptr ? 1 : 0);
     if (!grid_fits(blocks, 256))

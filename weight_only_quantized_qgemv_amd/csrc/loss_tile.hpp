@@ -10,7 +10,8 @@
 // matrix instructions in fp32 and is scaled and added by the vector units, 16 FMAs for
 // each 4 (groups of 32: 2) of 32x32x16, beside the next tile's. The biases are a second,
 // short contraction over the groups, with X in two 16-bit parts: exact to 2^-17 of X
-// (bf16; fp16 2^-22), G / 32 steps of 64 more.
+// (bf16; fp16, where a power of two brings the row's largest |X| to 2^14 .. 2^15: 2^-22
+// of X, and 2^-39 of the largest where that is more), G / 32 steps of 64 more.
 //
 // prep_x writes x once in the order that a unit's code pairs come in, rows filled
 // up to whole 64-wide steps, and X; prep_w the scales transposed (a step's scales
@@ -318,12 +319,23 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
             a_cur = a_cur + 1 == NA ? 0 : a_cur + 1;
             c_cur = c_cur + 1 == NCS ? 0 : c_cur + 1;
         }
-        if constexpr (DT == DT_F16) {   // X was divided by 128, which keeps it inside fp16's range
+        if constexpr (DT == DT_F16) {   // each row's X was brought into fp16's range
+            const __amdgpu_buffer_rsrc_t rf = rsrc(static_cast<const float*>(a.xs) + m0,
+                                                   (uint32_t)((rows_left < BM ? rows_left : BM) + 3) / 4 * 16);
 #pragma unroll
-            for (int i = 0; i < FM; ++i)
+            for (int i = 0; i < FM; ++i) {
+                f32x4_t f[4];   // registers 4 q .. 4 q + 3 are four rows
 #pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    total[i][j] *= 128.0f;
+                for (int q = 0; q < 4; ++q)
+                    f[q] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                        rf, (uint32_t)(wm * WM + 32 * i + 8 * q + 4 * half) * 4, 0, 0));
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+                        total[i][j][r] *= f[r >> 2][r & 3];
+                __builtin_amdgcn_sched_barrier(0);   // (no room for all of them at once)
+            }
         }
     }
 
@@ -556,56 +568,79 @@ __global__ __launch_bounds__(256 * WMW, 2) void loss_tile_kernel(LossTileArgs a)
     }
 }
 
-// x [M, K] as the tile kernel's steps take it, rows of xn: first the groups' sums X (fp16:
-// divided by 128), 64 values for 32 groups: their value in DT and what that leaves, in
-// eights as the fragments take them; then x in the order of the code pairs: position 2 p
-// (+ 1) of a unit of 32 holds its code lo_code(p) (hi_code(p)). A row of 64 n + 32 features
-// ends in a unit of zeros and then its last. A wave takes 64 units of a row.
+// Waves of a row where x is laid out, 64 units each at a time. fp16 rows, whose largest |X|
+// all of them need, stay in a block.
+__host__ __device__ constexpr int prep_waves(int dt, int chunks) { return dt != DT_F16 ? chunks : chunks > 2 ? 4 : chunks; }
+
+// x [M, K] as the tile kernel's steps take it, rows of xn: first the groups' sums X, 64
+// values for 32 groups: their value in DT and what that leaves, in eights as the fragments
+// take them; then x in the order of the code pairs: position 2 p (+ 1) of a unit of 32
+// holds its code lo_code(p) (hi_code(p)). A row of 64 n + 32 features ends in a unit of
+// zeros and then its last. fp16: X times a power of two that brings the row's largest to
+// 2^14 .. 2^15 (128 values may sum to more than the range, and the part that is left of a
+// small X would be subnormal: with 1 / 128 for all rows a loss of 6.2 from x of 1e-4 was 5e-4
+// off); its inverse goes to xf.
 template <int BITS, int DT>
 __device__ __forceinline__ void prep_x(int64_t block, const uint16_t* __restrict__ x, int64_t m, int k, int gs, int xn,
-                                       int gp, uint16_t* __restrict__ xp)
+                                       int gp, uint16_t* __restrict__ xp, float* __restrict__ xf)
 {
     using Order = CodeOrder<BITS>;
     using E = Elem<DT>;
     typedef u32x4_t Wide __attribute__((aligned(2)));
     const int first = 2 * gp, units = (xn - first) / 32, chunks = (units + 63) / 64, lane = (int)threadIdx.x & 63;
-    const int64_t w = block * 4 + (threadIdx.x >> 6), row = w / chunks;
-    if (row >= m)
-        return;
-    const int chunk = (int)(w % chunks), u = chunk * 64 + lane, n = k / 32;
-    const int src = u < n - (n & 1) ? u : u == units - 1 ? n - 1 : -1;   // (n odd: the last step)
+    const int waves = prep_waves(DT, chunks), n = k / 32, per = gs / 32;
+    const int64_t w = block * 4 + (threadIdx.x >> 6), row = w / waves;
+    const int chunk0 = (int)(w % waves);
+    uint16_t* const to = xp + row * xn;
+    // Lane's unit of a chunk, and its group's sum.
     uint32_t e[16];
+    int u = 0, src = -1;
     float sum = 0.0f;
+    auto load = [&](int chunk) {
+        u = chunk * 64 + lane;
+        src = row >= m ? -1 : u < n - (n & 1) ? u : u == units - 1 ? n - 1 : -1;   // (n odd: the last step)
+        sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        e[i] = 0u;
-    if (src >= 0) {
-        const uint16_t* const p = x + row * k + src * 32;
+        for (int i = 0; i < 16; ++i)
+            e[i] = 0u;
+        if (src >= 0) {
+            const uint16_t* const p = x + row * k + src * 32;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const u32x4_t v = *reinterpret_cast<const Wide*>(p + 8 * i);
+            for (int i = 0; i < 4; ++i) {
+                const u32x4_t v = *reinterpret_cast<const Wide*>(p + 8 * i);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                e[4 * i + j] = v[j];
-                sum += E::to_f32((uint16_t)v[j]) + E::to_f32((uint16_t)(v[j] >> 16));
+                for (int j = 0; j < 4; ++j) {
+                    e[4 * i + j] = v[j];
+                    sum += E::to_f32((uint16_t)v[j]) + E::to_f32((uint16_t)(v[j] >> 16));
+                }
             }
         }
-    }
-    uint16_t* const to = xp + row * xn;
-    if (u < units) {
-        auto elem = [&](int i) { return (e[i / 2] >> (16 * (i % 2))) & 0xFFFFu; };
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            u32x4_t v;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[j] = elem(Order::lo_code(4 * i + j)) | (elem(Order::hi_code(4 * i + j)) << 16);
-            *reinterpret_cast<u32x4_t*>(to + first + 32 * u + 8 * i) = v;
+        for (int off = 1; off < per; off <<= 1)
+            sum += __shfl_xor(sum, off, 64);
+    };
+    float by = 1.0f;
+    if constexpr (DT == DT_F16) {
+        __shared__ float room[4];
+        float top = 0.0f;
+        for (int chunk = chunk0; chunk < chunks; chunk += waves) {
+            load(chunk);
+            const float size = fabsf(sum);
+            top = fmaxf(top, size < __builtin_inff() ? size : 0.0f);
         }
+        top = wave_stat(Stat{top, 0.0f}).top;
+        if (lane == 0)
+            room[threadIdx.x >> 6] = top;
+        __syncthreads();
+        const int wave0 = (int)(threadIdx.x >> 6) - chunk0;   // the row's first
+        for (int i = 0; i < waves; ++i)
+            top = fmaxf(top, room[wave0 + i]);
+        const int exponent = top > 0.0f ? (int)(__float_as_uint(top) >> 23) - 127 - 14 : 0;   // (top is normal)
+        by = __uint_as_float((uint32_t)(127 - exponent) << 23);
+        if (chunk0 == 0 && lane == 0 && row < m)
+            xf[row] = __uint_as_float((uint32_t)(127 + exponent) << 23);
     }
-    const int per = gs / 32;
-    for (int off = 1; off < per; off <<= 1)
-        sum += __shfl_xor(sum, off, 64);
+    if (row >= m)
+        return;
     // Group g of a step of 32: its 16 (g / 16 % 2) are instructions 2 i and 2 i + 1, their
     // halves of the wave eight each (a_frag's chunks, which differ with groups of 32).
     auto put = [&](int g, uint16_t hi, uint16_t lo) {
@@ -615,13 +650,27 @@ __device__ __forceinline__ void prep_x(int64_t block, const uint16_t* __restrict
         t[8 * c0] = hi;
         t[8 * (c0 + 1)] = lo;
     };
-    if (src >= 0 && src % per == 0) {
-        if constexpr (DT == DT_F16)
-            sum *= 1.0f / 128;
-        const uint16_t hi = E::from_f32(sum);
-        put(src / per, hi, E::from_f32(sum - E::to_f32(hi)));
+    for (int chunk = chunk0; chunk < chunks; chunk += waves) {
+        if (DT != DT_F16 || chunks > waves)   // (or it is there)
+            load(chunk);
+        if (u < units) {
+            auto elem = [&](int i) { return (e[i / 2] >> (16 * (i % 2))) & 0xFFFFu; };
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                u32x4_t v;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[j] = elem(Order::lo_code(4 * i + j)) | (elem(Order::hi_code(4 * i + j)) << 16);
+                *reinterpret_cast<u32x4_t*>(to + first + 32 * u + 8 * i) = v;
+            }
+        }
+        if (src >= 0 && src % per == 0) {
+            const float part = sum * by;
+            const uint16_t hi = E::from_f32(part);
+            put(src / per, hi, E::from_f32(part - E::to_f32(hi)));
+        }
     }
-    if (chunk == 0 && k / gs + lane < gp)   // fewer than 32 to fill up
+    if (chunk0 == 0 && k / gs + lane < gp)   // fewer than 32 to fill up
         put(k / gs + lane, 0, 0);
 }
 
@@ -738,7 +787,8 @@ __global__ __launch_bounds__(256) void loss_prep_kernel(LossTileArgs a, LossPrep
         prep_x32<BITS>(block - w_blocks, static_cast<const float*>(p.x), a.M, a.K, a.gs, a.xn, a.gp, xp,
                        static_cast<float*>(const_cast<void*>(a.xs)));
     else
-        prep_x<BITS, DT>(block - w_blocks, static_cast<const uint16_t*>(p.x), a.M, a.K, a.gs, a.xn, a.gp, xp);
+        prep_x<BITS, DT>(block - w_blocks, static_cast<const uint16_t*>(p.x), a.M, a.K, a.gs, a.xn, a.gp, xp,
+                         static_cast<float*>(const_cast<void*>(a.xs)));
 }
 
 } // namespace losstile

@@ -79,7 +79,8 @@ constexpr int LOSS_BN = 256;   // columns of a tile, and of a part of the statis
 struct Stat;
 struct LossTileArgs {
     const void* xp;          // [M, xn] of 16 bits: the groups' sums of x, then x (fp32: x in three parts)
-    const void* xs;          // [M, gp]: the groups' sums (fp32 x)
+    const void* xs;          // [M, gp]: the groups' sums (fp32 x); [M] fp32: what takes the rows' factor
+                             // out of the biases' products again (fp16 x)
     const uint32_t* wq;      // [N, K*bits/32]
     const void* st;          // [K/gs, np]: the scales, transposed (prep_w)
     const void* bp;          // [N, gp]: the biases
