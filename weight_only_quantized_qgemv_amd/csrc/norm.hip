@@ -246,6 +246,11 @@ NormSplit norm_split(int64_t m, int64_t d, int64_t gates)
     return {groups, even(per, std::clamp<int64_t>(blocks / groups, 1, per))};
 }
 
+// r^3 mean(u v), of a row v and r = 1 / rms(v): from the mean on, which is of the row's own
+// size, so that only powers that the squares' sums allow too are formed (r^3 alone is
+// infinite for rows of 1e-13 and eps = 0, and subnormal for rows of 1e13).
+__device__ __forceinline__ float thrice(float r, float mean) { return r * (r * (r * mean)); }
+
 // Rows of up to 8192: the row, the weights and the block's column sums stay in
 // registers. A row of one chunk a thread is loaded while the row before it is summed
 // and closed.
@@ -327,7 +332,7 @@ __global__ __launch_bounds__(ROWT, 2) void norm_grad_kernel(NormGradArgs a, int6
                         q[2] = __builtin_fmaf(cur.y[c][i], cur.y[c][i], q[2]);
                 }
             row_sums<3, ROWT>(q, room, turn);
-            const float rs = pre ? 1.0f / sqrtf(q[0] / (float)n + a.eps) : 0.0f, ks = rs * rs * rs * (q[1] / (float)n);
+            const float rs = pre ? 1.0f / sqrtf(q[0] / (float)n + a.eps) : 0.0f, ks = thrice(rs, q[1] / (float)n);
             const float ry = post ? 1.0f / sqrtf(q[2] / (float)n + a.eps) : 1.0f;
             float G[C][8], z[1] = {0.0f};
 #pragma unroll
@@ -371,7 +376,7 @@ __global__ __launch_bounds__(ROWT, 2) void norm_grad_kernel(NormGradArgs a, int6
                 float kz = 0.0f;
                 if (post) {
                     row_sums<1, ROWT>(z, room, turn);
-                    kz = ry * ry * ry * (z[0] / (float)n);
+                    kz = thrice(ry, z[0] / (float)n);
                 }
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
@@ -469,7 +474,7 @@ __global__ __launch_bounds__(512) void norm_grad_wide_kernel(NormGradArgs a, int
                 row_sums<3, T>(q, room, turn);
                 if (pre) {
                     rs[r] = 1.0f / sqrtf(q[0] / (float)n + a.eps);
-                    ks[r] = rs[r] * rs[r] * rs[r] * (q[1] / (float)n);
+                    ks[r] = thrice(rs[r], q[1] / (float)n);
                 }
                 if (post)
                     ry[r] = 1.0f / sqrtf(q[2] / (float)n + a.eps);
@@ -559,7 +564,7 @@ __global__ __launch_bounds__(512) void norm_grad_wide_kernel(NormGradArgs a, int
                 if (!whole)
                     return;
                 if (post) {
-                    const float kz = ry[r] * ry[r] * ry[r] * (z[r] / (float)n);
+                    const float kz = thrice(ry[r], z[r] / (float)n);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         G[i] = ry[r] * G[i] - y[i] * kz;
