@@ -42,7 +42,7 @@ qp_status check_norm(const char* what, int sdt, int dt, int64_t m, int64_t d, bo
     if (d > qp::kNormMaxWidth)
         return fail(QP_ERR_UNSUPPORTED, "%s: rows of %lld elements (at most %lld)", what, (long long)d,
                     (long long)qp::kNormMaxWidth);
-    if (m > kMaxDim / 512)
+    if (m > qp::kNormMaxRows)
         return fail(QP_ERR_INVALID_ARG, "%s: size too large", what);
     if (gate && (gates < 0 || (gates == 0 ? m != 0 : m % gates != 0)))
         return fail(QP_ERR_SHAPE, "%s: %lld gate rows do not divide %lld rows", what, (long long)gates, (long long)m);

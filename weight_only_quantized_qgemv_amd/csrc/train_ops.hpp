@@ -10,7 +10,7 @@
 namespace qp {
 
 // ---- norms around a block (norm.hip)
-constexpr int64_t kNormMaxWidth = 16384;
+constexpr int64_t kNormMaxWidth = 16384, kNormMaxRows = int64_t(1) << 22;   // (rows of 512 threads: 2^31)
 
 struct NormArgs {
     const void* x;           // [M, D] of sdt: the stream
