@@ -30,6 +30,8 @@ UNITS = ([("api.cpp", "api", {}), ("quantize.hip", "quantize", {}), ("moe.hip", 
           ("loss.hip", "loss", {})]
          + [("qgemv.hip", f"qgemv_b{b}", {"QP_BITS": b}) for b in BITS]
          + [(f"{f}.hip", f"{f}_b{b}", {"QP_BITS": b}) for f in ("xgrad", "wgrad", "gate_up", "ffn_any", "loss_tile", "loss_rows") for b in BITS]
+         + [("xgrad.hip", f"xgrad_pieces_b{b}", {"QP_BITS": b, "QP_PIECES": 1}) for b in BITS]
+         + [("wgrad.hip", f"wgrad_scaled_b{b}", {"QP_BITS": b, "QP_SCALED": 1}) for b in BITS]
          + [("moe_compute.hip", f"moe_b{b}_n{n}", {"QP_BITS": b, "QP_NMAT": n})
             for b in BITS for n in (1, 2)])
 

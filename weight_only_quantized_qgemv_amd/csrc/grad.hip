@@ -20,24 +20,26 @@ namespace qp {
 
 hipError_t launch_xgrad(const XgradArgs& a, const GradPlan& p, hipStream_t st)
 {
+    const bool pieces = a.sums != nullptr;
     switch (a.bits) {
-    case 2: return launch_xgrad_b2(a, p, st);
-    case 3: return launch_xgrad_b3(a, p, st);
-    case 4: return launch_xgrad_b4(a, p, st);
-    case 6: return launch_xgrad_b6(a, p, st);
-    case 8: return launch_xgrad_b8(a, p, st);
+    case 2: return pieces ? launch_xgrad_pieces_b2(a, p, st) : launch_xgrad_b2(a, p, st);
+    case 3: return pieces ? launch_xgrad_pieces_b3(a, p, st) : launch_xgrad_b3(a, p, st);
+    case 4: return pieces ? launch_xgrad_pieces_b4(a, p, st) : launch_xgrad_b4(a, p, st);
+    case 6: return pieces ? launch_xgrad_pieces_b6(a, p, st) : launch_xgrad_b6(a, p, st);
+    case 8: return pieces ? launch_xgrad_pieces_b8(a, p, st) : launch_xgrad_b8(a, p, st);
     }
     return hipErrorInvalidValue;
 }
 
 hipError_t launch_wgrad(const WgradArgs& a, const GradPlan& p, hipStream_t st)
 {
+    const bool scaled = a.scale != nullptr;
     switch (a.bits) {
-    case 2: return launch_wgrad_b2(a, p, st);
-    case 3: return launch_wgrad_b3(a, p, st);
-    case 4: return launch_wgrad_b4(a, p, st);
-    case 6: return launch_wgrad_b6(a, p, st);
-    case 8: return launch_wgrad_b8(a, p, st);
+    case 2: return scaled ? launch_wgrad_scaled_b2(a, p, st) : launch_wgrad_b2(a, p, st);
+    case 3: return scaled ? launch_wgrad_scaled_b3(a, p, st) : launch_wgrad_b3(a, p, st);
+    case 4: return scaled ? launch_wgrad_scaled_b4(a, p, st) : launch_wgrad_b4(a, p, st);
+    case 6: return scaled ? launch_wgrad_scaled_b6(a, p, st) : launch_wgrad_b6(a, p, st);
+    case 8: return scaled ? launch_wgrad_scaled_b8(a, p, st) : launch_wgrad_b8(a, p, st);
     }
     return hipErrorInvalidValue;
 }

@@ -128,7 +128,8 @@ template <int VM> __device__ __forceinline__ void step_barrier()
 // A: dy [BM][64] by DMA; B: W [64][BN] turned and dequantized. Waves WMW x WNW.
 template <int BM, int BN> constexpr int xgrad_lds() { return 3 * BM * 128 + 2 * BN * 128; }
 
-template <int BITS, int DT, int BM, int BN, int WMW>
+// PIECES: a call of several over pieces of the contraction (XgradArgs::sums).
+template <int BITS, int DT, int BM, int BN, int WMW, bool PIECES>
 __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPlan plan, int tiles_k, int tiles,
                                                             int per_xcd)
 {
@@ -351,8 +352,7 @@ __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPla
                                                       at == OOB ? OOB : 4 * (at + reg_off(R)), 0, 0);
             });
         });
-    } else if (a.sums != nullptr) {
-        // A call of several over pieces of the contraction (16 loads at a time).
+    } else if constexpr (PIECES) {   // (16 loads at a time)
         const __amdgpu_buffer_rsrc_t rs = rows_of(a.sums, m0, 4), ro = rows_of(a.out, m0, 2);
         const float scale = a.last && a.scale != nullptr ? *a.scale : 1.0f;
         each_tile([&](const f32x16_t& v, uint32_t at) {
@@ -420,9 +420,10 @@ __global__ __launch_bounds__(2 * BN) void xgrad_tile_kernel(XgradArgs a, GradPla
 // Tile i, register r: k = kw + 32 i + 8 (r / 4) + 4 half + r % 4 of weight row
 // nw + 32 j + lane % 32: unit i of the wave's four. All the codes are asked
 // for before any is used; a unit is moved down by the half's four codes once.
-template <int BITS, int DT, int FN, bool WIDE = false>
+// SCALED: the results are multiplied by `scale`.
+template <int BITS, int DT, int FN, bool SCALED, bool WIDE = false>
 __device__ __forceinline__ void wgrad_close(const WgradArgs& a, int splits, int mat, int split, int64_t kw,
-                                            int64_t nw, int lane, const f32x16_t (&acc)[4][FN])
+                                            int64_t nw, int lane, float scale, const f32x16_t (&acc)[4][FN])
 {
     // Opaque here, so that the addresses are formed at the tile's end and not
     // kept in registers through the steps.
@@ -486,7 +487,6 @@ __device__ __forceinline__ void wgrad_close(const WgradArgs& a, int splits, int 
     using St = typename Elem<DT>::storage;
     const int64_t groups = a.K / a.gs, count = a.N * groups, at = (nw + (lane & 31)) * groups + kw / a.gs;
     const bool parts = splits > 1;
-    const float scale = !parts && a.scale != nullptr ? *a.scale : 1.0f;
     float* const pd = parts ? a.partial + (((int64_t)split * a.nmat + mat) * 2 + half) * count + at : nullptr;
     St* const sd = parts ? nullptr : static_cast<St*>(half ? a.dbiases[mat] : a.dscales[mat]) + at;
     const int per = a.gs / 32;                                      // units of a group
@@ -497,7 +497,7 @@ __device__ __forceinline__ void wgrad_close(const WgradArgs& a, int splits, int 
             if (parts)
                 pd[o] = v;
             else
-                sd[o] = Elem<DT>::from_f32(v * scale);
+                sd[o] = Elem<DT>::from_f32(SCALED ? v * scale : v);
         }
     };
     if (per == 1) {
@@ -516,7 +516,17 @@ __device__ __forceinline__ void wgrad_close(const WgradArgs& a, int splits, int 
 // WKW x WNW waves, each 128 k (every group closes inside a wave) x WN n.
 template <int BK, int BN> constexpr int wgrad_lds() { return 2 * (BK + BN) * 128; }
 
-template <int BITS, int DT, int BK, int BN>
+// The factor of a call's results, read before the steps: at the tiles' ends it is waited
+// for behind the codes (8 rows of 4096 x 32000 65.8 us, now 61).
+template <bool SCALED> __device__ __forceinline__ float wgrad_factor(const WgradArgs& a)
+{
+    if constexpr (SCALED)
+        return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, *a.scale)));
+    else
+        return 1.0f;
+}
+
+template <int BITS, int DT, int BK, int BN, bool SCALED>
 __global__ __launch_bounds__(2 * BN) void wgrad_tile_kernel(WgradArgs a, GradPlan plan, int tiles_k, int tiles,
                                                             int per_xcd)
 {
@@ -537,6 +547,7 @@ __global__ __launch_bounds__(2 * BN) void wgrad_tile_kernel(WgradArgs a, GradPla
     const int tid = (int)threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wk = wave / WNW, wn = wave % WNW;
+    const float scale = wgrad_factor<SCALED>(a);
     const int lo = (int)blockIdx.y * (int)plan.per_split;
     int hi = lo + (int)plan.per_split;
     const int steps = (int)((a.M + STEP - 1) / STEP);
@@ -627,7 +638,7 @@ __global__ __launch_bounds__(2 * BN) void wgrad_tile_kernel(WgradArgs a, GradPla
             run_step(kt + 1, std::integral_constant<int, 1>{});
     }
 
-    wgrad_close<BITS, DT, FN>(a, plan.splits, mat, (int)blockIdx.y, k0 + 128 * wk, n0 + wn * WN, lane, acc);
+    wgrad_close<BITS, DT, FN, SCALED>(a, plan.splits, mat, (int)blockIdx.y, k0 + 128 * wk, n0 + wn * WN, lane, scale, acc);
 }
 
 // The same product with four waves of 128 k x 128 n, one on each SIMD: a
@@ -657,7 +668,7 @@ __device__ __forceinline__ void band_order(int tile, int tiles_n, int tiles_k, i
     tk = 8 * band + in % width;
 }
 
-template <int BITS, int DT>
+template <int BITS, int DT, bool SCALED>
 __global__ __launch_bounds__(256) void wgrad_wide_kernel(WgradArgs a, int tiles_n, int tiles_k)
 {
     using T = MfmaTraits<DT>;
@@ -670,6 +681,7 @@ __global__ __launch_bounds__(256) void wgrad_wide_kernel(WgradArgs a, int tiles_
     const int tid = (int)threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wk = wave >> 1, wn = wave & 1;
+    const float scale = wgrad_factor<SCALED>(a);
     const int steps = (int)((a.M + STEP - 1) / STEP);
     // Items: tiles of every weight, XCD by XCD.
     const int tiles = tiles_n * tiles_k, items = tiles * a.nmat, per_xcd = (items + 7) / 8;
@@ -819,7 +831,7 @@ __global__ __launch_bounds__(256) void wgrad_wide_kernel(WgradArgs a, int tiles_
         stage = 1 - stage;
       }
       acc_settle();
-      wgrad_close<BITS, DT, 4, true>(a, 1, cur.mat, 0, cur.k0 + 128 * wk, cur.n0 + 128 * wn, lane, acc);
+      wgrad_close<BITS, DT, 4, SCALED, true>(a, 1, cur.mat, 0, cur.k0 + 128 * wk, cur.n0 + 128 * wn, lane, scale, acc);
     }
 }
 

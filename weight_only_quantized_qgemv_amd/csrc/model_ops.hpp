@@ -150,16 +150,19 @@ struct GradPlan {
 // (16-bit activations in rows of whole 16-byte pieces, 16-byte aligned).
 GradPlan xgrad_plan(int64_t m, int64_t n, int64_t k, int nmat, bool tiles);
 GradPlan wgrad_plan(int64_t m, int64_t n, int64_t k, int nmat, int gs, bool tiles);
-#define QP_GRAD_DECL(B)                                                                        \
-    hipError_t launch_xgrad_b##B(const XgradArgs& a, const GradPlan& p, hipStream_t stream);   \
-    hipError_t launch_wgrad_b##B(const WgradArgs& a, const GradPlan& p, hipStream_t stream);
+#define QP_GRAD_DECL(B)                                                                              \
+    hipError_t launch_xgrad_b##B(const XgradArgs& a, const GradPlan& p, hipStream_t stream);         \
+    hipError_t launch_xgrad_pieces_b##B(const XgradArgs& a, const GradPlan& p, hipStream_t stream);  \
+    hipError_t launch_wgrad_b##B(const WgradArgs& a, const GradPlan& p, hipStream_t stream);         \
+    hipError_t launch_wgrad_scaled_b##B(const WgradArgs& a, const GradPlan& p, hipStream_t stream);
 QP_GRAD_DECL(2)
 QP_GRAD_DECL(3)
 QP_GRAD_DECL(4)
 QP_GRAD_DECL(6)
 QP_GRAD_DECL(8)
 #undef QP_GRAD_DECL
-// By a.bits (grad.hip), and what the callers of the products share.
+// By a.bits, and by whether there are sums, a factor (grad.hip), and what the callers of
+// the products share.
 hipError_t launch_xgrad(const XgradArgs& a, const GradPlan& p, hipStream_t stream);
 hipError_t launch_wgrad(const WgradArgs& a, const GradPlan& p, hipStream_t stream);
 // Whether the tile kernels' 32-bit offsets reach a tile's rows: rows of at

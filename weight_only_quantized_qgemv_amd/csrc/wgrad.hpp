@@ -17,13 +17,13 @@
 namespace qp {
 
 // Sums the splits' partial sums [split][scales, biases][N * G] in split order.
-template <int DT>
+template <int DT, bool SCALED>
 __global__ __launch_bounds__(256) void wgrad_finish_kernel(const float* __restrict__ partial, int splits,
                                                            int64_t per_split, int64_t count, void* dscales,
                                                            void* dbiases, const float* scale)
 {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < 2 * count; i += (int64_t)gridDim.x * 256) {
-        const float v = scaled(sum_splits(partial, splits, per_split, i), scale);
+        const float sum = sum_splits(partial, splits, per_split, i), v = SCALED ? sum * *scale : sum;
         if (i < count)
             store_elem<DT>(dscales, i, v);
         else
@@ -33,7 +33,7 @@ __global__ __launch_bounds__(256) void wgrad_finish_kernel(const float* __restri
 
 // One group's two sums of weight row n: to the outputs, or to the split's
 // partial sums.
-template <int DT>
+template <int DT, bool SCALED>
 __device__ __forceinline__ void wgrad_store(const WgradArgs& a, const GradPlan& plan, int mat, int split,
                                             int64_t n, int64_t g, bool bias, float v)
 {
@@ -41,7 +41,7 @@ __device__ __forceinline__ void wgrad_store(const WgradArgs& a, const GradPlan& 
     if (plan.splits > 1)
         a.partial[(((int64_t)split * a.nmat + mat) * 2 + (bias ? 1 : 0)) * count + i] = v;
     else
-        store_elem<DT>(bias ? a.dbiases[mat] : a.dscales[mat], i, scaled(v, a.scale));
+        store_elem<DT>(bias ? a.dbiases[mat] : a.dscales[mat], i, SCALED ? v * *a.scale : v);
 }
 
 // Any type, size and alignment: fp32 products on the 32x32x2 matrix
@@ -51,7 +51,7 @@ __device__ __forceinline__ void wgrad_store(const WgradArgs& a, const GradPlan& 
 // its products.
 constexpr int WG_BK = 128, WG_BN = 128, WG_M = 16;
 
-template <int BITS, int DT>
+template <int BITS, int DT, bool SCALED>
 __global__ __launch_bounds__(256) void wgrad_f32_kernel(WgradArgs a, GradPlan plan)
 {
     __shared__ float xs[WG_M][WG_BK];
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(256) void wgrad_f32_kernel(WgradArgs a, GradPlan pl
             if (j >= i && j < i + tiles)
                 v += half ? pb[j] : ps[j];
         });
-        wgrad_store<DT>(a, plan, mat, split, n, (k0 + 32 * i) / a.gs, half != 0, v);
+        wgrad_store<DT, SCALED>(a, plan, mat, split, n, (k0 + 32 * i) / a.gs, half != 0, v);
     }
 }
 

@@ -45,11 +45,11 @@ __device__ __forceinline__ void xgrad_add(const XgradArgs& a, int64_t i, float v
         a.sums[i] = v;
 }
 
-// The result v of element i = m K + k: stored, or closed as above.
-template <int DT>
+// The result v of element i = m K + k: stored, or closed as above (PIECES: added).
+template <int DT, bool PIECES>
 __device__ __forceinline__ void xgrad_store(const XgradArgs& a, int64_t i, float v)
 {
-    if (a.sums != nullptr) {
+    if constexpr (PIECES) {
         xgrad_add<DT>(a, i, v);
         return;
     }
@@ -83,12 +83,12 @@ __device__ __forceinline__ float sum_splits(const float* partial, int splits, in
 }
 
 // Sums the splits' partial sums and closes.
-template <int DT>
+template <int DT, bool PIECES>
 __global__ __launch_bounds__(256) void xgrad_finish_kernel(XgradArgs a, int splits)
 {
     const int64_t total = a.M * a.K;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256)
-        xgrad_store<DT>(a, i, sum_splits(a.partial, splits, total, i));
+        xgrad_store<DT, PIECES>(a, i, sum_splits(a.partial, splits, total, i));
 }
 
 // v, or zero: by its bits, since a select around a loaded value becomes a branch
@@ -105,7 +105,7 @@ __device__ __forceinline__ float live_or_zero(bool live, float v)
 // of a 14336 x 4096 weight 2150 us (112 TFLOP/s).
 constexpr int XG_BM = 128, XG_BK = 128, XG_N = 32;
 
-template <int BITS, int DT>
+template <int BITS, int DT, bool PIECES>
 __global__ __launch_bounds__(256) void xgrad_f32_kernel(XgradArgs a, GradPlan plan)
 {
     using C8 = Codes8<BITS>;
@@ -218,12 +218,12 @@ __global__ __launch_bounds__(256) void xgrad_f32_kernel(XgradArgs a, GradPlan pl
     if (plan.splits > 1) {
         float* const part = a.partial + (int64_t)blockIdx.y * a.M * a.K;
         each([&](int64_t i, float v) { part[i] = v; });
-    } else if (a.sums != nullptr) {
+    } else if constexpr (PIECES) {
         each([&](int64_t i, float v) { xgrad_add<DT>(a, i, v); });
     } else if (a.g == nullptr) {
         each([&](int64_t i, float v) { store_elem<DT>(a.out, i, v); });
     } else {
-        each([&](int64_t i, float v) { xgrad_store<DT>(a, i, v); });
+        each([&](int64_t i, float v) { xgrad_store<DT, false>(a, i, v); });
     }
 }
 
