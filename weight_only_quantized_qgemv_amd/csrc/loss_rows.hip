@@ -73,11 +73,8 @@ template <int DT> hipError_t run(const GemvArgs& a, hipStream_t st)
     SkinnyShape sh{};
     dim3 grid;
     skinny_dense_shape(a.N, a.K, &sh, &grid);
-    // The row-contiguous form where qmatmul takes it (qgemv.hip).
     if constexpr (QP_BITS != 8) {
-        const bool wide = QP_BITS != 6 || (a.gs >= 64 && a.N * a.K >= (int64_t(1) << 25));
-        if (wide && (2 * (a.K / a.gs)) % 16 == 0 && aligned16(a.scales) && aligned16(a.biases) && aligned16(a.wq) &&
-            sh.rows_per_block % 16 == 0)
+        if (skinny4_takes<QP_BITS>(a, sh))
             return skinny4_launch<QP_BITS, DT, DT_F32>(k, sh, grid, st);
     }
     return skinny_launch<QP_BITS, DT, 1, DT_F32>(k, sh, grid, st);

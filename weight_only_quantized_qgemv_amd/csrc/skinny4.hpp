@@ -346,6 +346,22 @@ __global__ __launch_bounds__(64 * kSkinnyMaxWaves) void qgemv_skinny4_kernel(Gem
     }
 }
 
+// Whether the row-contiguous form takes a product: 6-, 4-, 3- and 2-bit codes with rows of
+// scales in whole 16-byte pieces. Measured (graph-replayed): 14336 x 4096 M = 16 13.2 us
+// against 15.4, M = 8 12.2 against 14.6; 4096 x 14336 M = 16 18.3 against 25.5; 2-bit 14336 x
+// 4096 M = 16 11.9 against 12.5, 4096 x 14336 M = 16 18.3 against 21.7; 3-bit (queued
+// launches) 14336 x 4096 M = 16 14.2 against 16.7, 4096 x 4096 M = 8 8.3 against 9.6 at gs 64;
+// 6-bit 4096 x 14336 M = 16 26.7 against 30.6, 14336 x 4096 M = 16 18.2 against 18.7, but 4096
+// x 4096 M = 8 10.7 against 10.2 and, at gs 32 (whose scales and biases take 16 more
+// registers, which spills), 14.4 against 11.3: so 6-bit codes take it from gs 64 and 2^25
+// codes. 8-bit codes measured no faster this way.
+template <int BITS> bool skinny4_takes(const GemvArgs& a, const SkinnyShape& sh)
+{
+    const bool wide = BITS != 6 || (a.gs >= 64 && a.N * a.K >= (int64_t(1) << 25));
+    return BITS != 8 && wide && (2 * (a.K / a.gs)) % 16 == 0 && aligned16(a.scales) && aligned16(a.biases) &&
+           aligned16(a.wq) && sh.rows_per_block % 16 == 0;
+}
+
 template <int BITS, int DT, int GU, int ODT>
 hipError_t skinny4_launch_one(const GemvKernelArgs& k, const SkinnyShape& sh, dim3 grid, hipStream_t st)
 {
