@@ -514,9 +514,13 @@ qp_status qlogits_adjust(const void* logits, qp_dtype dtype, int64_t rows, int64
  *   loss, lse  device, fp32 [m] (outputs)
  *   workspace device, >= qcross_entropy_workspace_bytes(...), 16-byte aligned; a
  *            call's own until it has run (so for each captured graph)
- * The logits are formed and reduced in fp32, in pieces of the vocabulary;
- * nothing of them is rounded to 16 bits. vocab == 0: lse is -infinity. A row of x
- * with an infinity or a NaN gives NaN in its own row. Deterministic.
+ * The logits are formed and reduced in fp32, in pieces of the vocabulary; no weight
+ * is rounded on their way. From 17 rows of 16 bits on, the groups' sums of x that
+ * meet the biases are exact to 2^-17 of themselves (bf16), or to 2^-22 and 2^-39 of
+ * the row's largest (fp16). The workspace holds what a piece needs; k == 32 and k
+ * above 2^18 need 4096 logits of every row, 16 KB each, at the least. vocab == 0: lse
+ * is -infinity. A row of x with an infinity or a NaN gives NaN in its own row.
+ * Deterministic.
  */
 size_t qcross_entropy_workspace_bytes(int64_t m, int64_t k, int64_t vocab, int32_t bits, int32_t group_size,
                                       qp_dtype dtype);
@@ -536,9 +540,11 @@ qp_status qcross_entropy(const void* x, qp_dtype x_dtype, int64_t m, int64_t k, 
  *   dscales, dbiases  device, x_dtype [vocab, k/group_size] (outputs), or both null
  *   workspace device, >= qcross_entropy_backward_workspace_bytes(...), 16-byte aligned
  * The logits are formed again, a piece of the vocabulary at a time. dz is rounded
- * to x_dtype as the products' operand (16-bit types: times a factor that makes the
- * largest |dloss| 2^14, taken out of the sums again); everything else is fp32. Rows
- * of x must be finite where there is no target too.
+ * to x_dtype as the products' operand (16-bit types: times one factor for all rows,
+ * which makes the largest |dloss| 2^14 and is taken out of the sums again; in fp16 a
+ * dz is so kept to 2^-11 of itself or 2^-39 of the largest |dloss|, whichever is
+ * more), and the weights of dx are rounded to 16-bit types as in qffn_backward;
+ * everything else is fp32. Rows of x must be finite where there is no target too.
  * Deterministic. m == 0 or vocab == 0 writes zeros.
  */
 size_t qcross_entropy_backward_workspace_bytes(int64_t m, int64_t k, int64_t vocab, int32_t bits,

@@ -764,7 +764,8 @@ def qcross_entropy_backward_workspace_bytes(m: int, k: int, vocab: int, bits: in
 def qcross_entropy_backward(x, targets, lse, dloss, wq, scales, biases, bits: int, group_size: int,
                             input_grad: bool = True, weight_grads: bool = True, workspace=None):
     """Gradients of qcross_entropy at dloss (fp32 [m], the rows' own upstream gradients: 1 / m for a
-    mean over all rows): (dx, dscales, dbiases) in x's dtype, each None where it is not asked for."""
+    mean over all rows): (dx, dscales, dbiases) in x's dtype, each None where it is not asked for.
+    Rows of x without a target have no gradient and add none, but must be finite."""
     import torch
     _dev(x, "x")
     m, k, v, dt = _check_head(x, targets, (wq, scales, biases), bits, group_size)

@@ -8,7 +8,7 @@
 // reduced at once, to a maximum and a sum of exponentials for each row and part
 // of the piece (forward), or to dz, the operand of the two gradient products
 // (backward, where they are formed a second time: the price of not keeping them,
-// 2 M K V of 8 M K V operations). The parts' pairs are joined in a fixed order.
+// 2 M K V of 6 M K V operations). The parts' pairs are joined in a fixed order.
 #include <algorithm>
 
 #include "common.hpp"
@@ -209,7 +209,8 @@ __global__ __launch_bounds__(256) void loss_dz_kernel(const float* z, int64_t m,
     }
 }
 
-// Vocabulary of a piece: logits of about 256 MB in fp32, whole parts, or all of it.
+// Vocabulary of a piece: logits of about 256 MB in fp32, whole parts, or all of it. (A part
+// at the least: from 16384 rows on 16 KB a row, at 2^20 rows 17 GB.)
 int64_t piece_of(int64_t m, int64_t v)
 {
     const int64_t most = std::max<int64_t>((int64_t(1) << 26) / m / kPart * kPart, kPart);

@@ -41,11 +41,14 @@ template <int LANES = 64> __device__ __forceinline__ Stat wave_stat(Stat s)
 }
 
 // The factor that makes the rows' largest |dloss| 2^14, and what takes it out of the
-// sums again (scale[0] and [1]), by one block of 256 threads. dz is the products' 16-bit operand: most of it is p - 1 or a small p times
-// one and the same dloss, whose own rounding would not average out (2048 rows, a mean
-// over 1843 of them, in bf16: the gradients 0.0040 of their size off 64 bits, with
-// the factor 0.0024); and in fp16 a mean over many rows would leave the normal range
-// (2^-14) for a token of probability 1e-2 already.
+// sums again (scale[0] and [1]), by one block of 256 threads. dz is the products' 16-bit
+// operand: most of it is p - 1 or a small p times one and the same dloss, whose own
+// rounding would not average out (2048 rows, a mean over 1843 of them, in bf16: the
+// gradients 0.0040 of their size off 64 bits, with the factor 0.0024); and in fp16 a mean
+// over many rows would leave the normal range (2^-14) for a token of probability 1e-2
+// already. It is one factor for all rows, since dW sums over them: in fp16 a dz below 2^-28
+// of the largest |dloss| is subnormal, so a row of a far smaller dloss than another's keeps
+// fewer digits of its small probabilities.
 __device__ __forceinline__ void dz_factor(const float* __restrict__ dloss, int64_t m, const int32_t* __restrict__ targets,
                                           int64_t vocab, float* __restrict__ scale)
 {

@@ -115,7 +115,7 @@ struct XgradArgs {
     float* partial;         // fp32 partial sums of the splits (xgrad_plan)
     // A result in pieces of the contraction, a call each: sums [M, K] kept from
     // call to call (the first writes them, the last adds them and writes out),
-    // or null; out is multiplied by *scale (on the device) where that is given.
+    // or null; with sums, out is multiplied by *scale (on the device) where that is given.
     float* sums;
     bool first, last;
     const float* scale;

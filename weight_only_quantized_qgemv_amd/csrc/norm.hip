@@ -229,10 +229,10 @@ struct NormSplit {
     int64_t groups, parts;
 };
 // Threads of a row in the backward pass, and so many blocks as the GPU holds at once
-// (two waves a SIMD): 8192 rows of 4096, bf16, 98 us, with twice as many 103; 4096
-// rows of 2048 34.1 us on 512 blocks of 256 threads, 38.8 on 256, and in another run
-// 37.5 and, on 768, 39.7. Of as many rounds the fewest blocks (600 rows of 1027 on 300
-// blocks 17.6 us, on 512 17.9: less to join).
+// (two waves a SIMD): 8192 rows of 4096, bf16, 86 us, with half as many 148, with twice as
+// many 92; 4096 rows of 2048 30.7 us on 512 blocks of 256 threads, 38.1 on 256, 31.2 on 768,
+// 35.8 on 1024. Of as many rounds the fewest blocks, whose sums take the least room (600
+// rows of 1027 17 us on 300 blocks as on 512).
 int norm_threads(int64_t d) { return d <= 512 ? 64 : d <= 1024 ? 128 : d <= 2048 ? 256 : 512; }
 NormSplit norm_split(int64_t m, int64_t d, int64_t gates)
 {
@@ -415,7 +415,8 @@ __global__ __launch_bounds__(ROWT, 2) void norm_grad_kernel(NormGradArgs a, int6
 // Wider rows: read again for each of the three passes over a row (from L2), a chunk at
 // a time, the column sums in the block's own part of the workspace, where each thread
 // reads and writes the columns that are its own, once for three rows. 2048 rows of
-// 16384, bf16: 232 us; with every row, 0.8 GB of sums' way through the workspace, 310.
+// 16384, bf16, with a gate: 234 us; once for two rows 247; with every row, 0.8 GB of sums'
+// way through the workspace, 309.
 template <int DT, int SDT>
 __global__ __launch_bounds__(512) void norm_grad_wide_kernel(NormGradArgs a, int64_t groups, int64_t parts)
 {
