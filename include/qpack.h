@@ -543,8 +543,10 @@ qp_status qcross_entropy(const void* x, qp_dtype x_dtype, int64_t m, int64_t k, 
  * to x_dtype as the products' operand (16-bit types: times one factor for all rows,
  * which makes the largest |dloss| 2^14 and is taken out of the sums again; in fp16 a
  * dz is so kept to 2^-11 of itself or 2^-39 of the largest |dloss|, whichever is
- * more), and the weights of dx are rounded to 16-bit types as in qffn_backward;
- * everything else is fp32. Rows of x must be finite where there is no target too.
+ * more), and the weights of dx are rounded to 16-bit types as in qffn_backward: where
+ * one token makes a row's dx, its elements are up to three half steps off, dz's, the
+ * weight's and their own. Everything else is fp32. Rows of x must be finite where
+ * there is no target too.
  * Deterministic. m == 0 or vocab == 0 writes zeros.
  */
 size_t qcross_entropy_backward_workspace_bytes(int64_t m, int64_t k, int64_t vocab, int32_t bits,
